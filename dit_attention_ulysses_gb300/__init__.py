@@ -36,6 +36,15 @@ __all__ = [
     "xs_attn_causal_fwd",
     "xs_attn_varlen_fwd",
     "Workspace",
+    "Rope",
+    "xs_rope_init",
+    "xs_rope_fwd",
+    "xs_rope_append_paged",
+    "xs_paged_step",
+    "PagedWorkspace",
+    "xs_attn_paged_workspace_bytes",
+    "xs_attn_paged_plan",
+    "xs_attn_paged_fwd",
     "xs_attn_get_device_error",
     "xs_attn_get_device_error_info",
     "xs_attn_error_string",
@@ -64,6 +73,17 @@ XS_ERR_LAYOUT = -13
 XS_ERR_DEVICE_DRAIN = -14
 XS_ERR_DEVICE_BOUNDS = -15
 XS_ERR_UNAVAILABLE = -16
+XS_ERR_DTYPE = -17
+XS_ERR_PAGE = -18
+XS_ERR_ROPE = -19
+XS_DTYPE_BF16 = 0
+XS_DTYPE_FP16 = 1
+XS_ROPE_HALF = 0
+XS_ROPE_INTERLEAVED = 1
+XS_ROPE_PLAIN = 0
+XS_ROPE_LINEAR = 1
+XS_ROPE_STRETCH = 2
+XS_ROPE_BY_PARTS = 3
 XS_MAX_P = 16
 XS_LAYOUT_A2A = 0
 XS_LAYOUT_CONTIGUOUS = 1
@@ -73,6 +93,15 @@ _vp = ctypes.c_void_p
 _int = ctypes.c_int
 _f32 = ctypes.c_float
 _size = ctypes.c_size_t
+_i64 = ctypes.c_longlong
+_f64 = ctypes.c_double
+
+
+class _RopeStruct(ctypes.Structure):
+    """``xs_rope`` of include/xsattn.h."""
+
+    _fields_ = [("turns", ctypes.c_ulonglong * 64), ("magnitude", _f32), ("layout", _int), ("rot", _int), ("D", _int)]
+
 
 # name -> (restype, argtypes); the full exported C ABI
 EXPORTS = {
@@ -97,6 +126,14 @@ EXPORTS = {
                                        _vp]),
     "xs_attn_ulysses_rank_fwd": (_int, [_vp, _vp, _vp, ctypes.POINTER(_vp), _int, _int, _int, _int, _int, _int, _f32,
                                         _vp, _size, _vp]),
+    "xs_rope_init": (_int, [_vp, _int, _int, _int, _f64, _int, _f64, _f64, _f64, _f64, _f64]),
+    "xs_rope_fwd": (_int, [_vp, _vp, _vp, _int, _int, _i64, _i64, _int, _int, _vp, _vp]),
+    "xs_rope_append_paged": (_int, [_vp] * 8 + [_int] * 3 + [_i64] * 4 + [_int, _int, _vp, _vp, _int, _vp, _vp]),
+    "xs_paged_step": (_int, [_vp] * 5 + [_int] * 5 + [_vp] * 7),
+    "xs_attn_paged_workspace_bytes": (_int, [_int, _int, _int, _int, ctypes.POINTER(_size)]),
+    "xs_attn_paged_plan": (_int, [_vp, _vp] + [_int] * 7 + [_vp, _size, _vp]),
+    "xs_attn_paged_fwd": (_int, [_vp] * 4 + [_int, ctypes.POINTER(_vp), _vp] + [_int] * 5 +
+                          [_i64, _int, _int, _i64, _int, _int, _vp, _vp] + [_int] * 4 + [_f32, _vp, _size, _vp]),
     "xs_burst_gap": (_int, [_vp, _size, _int, _size, _int, ctypes.c_longlong, ctypes.c_longlong, _vp, _vp]),
     "xs_attn_get_device_error": (_int, [_vp]),
     "xs_attn_get_device_error_info": (_int, [_vp, ctypes.POINTER(_int), _int]),
@@ -368,6 +405,216 @@ def xs_attn_varlen_fwd(q, k, v, seqlens, layout: int, outs, scale: float, causal
     _check(lib.xs_attn_varlen_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, len(seqlens), int(bool(causal)),
                                   layout, _ptr_array([o.data_ptr() for o in os_]), T, H, D, len(os_), scale,
                                   _stream_handle(stream)), "xs_attn_varlen_fwd")
+
+
+# ---- serving: new tokens over a paged cache
+
+
+class Rope:
+    """Rotary positions of a model (``xs_rope`` of the C ABI): head dimension ``D``, the first
+    ``rot`` channels of a head rotated, ``layout`` XS_ROPE_HALF or XS_ROPE_INTERLEAVED, ``base``,
+    and the scaling of long contexts (``scaling`` XS_ROPE_PLAIN, _LINEAR, _STRETCH or _BY_PARTS
+    with ``factor``, ``context``, ``low``, ``high``; ``magnitude`` multiplies cos and sin)."""
+
+    def __init__(self, D: int, rot: int | None = None, layout: int = XS_ROPE_HALF, base: float = 10000.0,
+                 scaling: int = XS_ROPE_PLAIN, factor: float = 1.0, context: float = 0.0, low: float = 1.0,
+                 high: float = 32.0, magnitude: float = 1.0):
+        self._struct = _RopeStruct()
+        self.ptr = ctypes.addressof(self._struct)
+        self.D, self.rot = D, D if rot is None else rot
+        xs_rope_init(self, D, self.rot, layout, base, scaling, factor, context, low, high, magnitude)
+
+
+def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling: int, factor: float,
+                 context: float, low: float, high: float, magnitude: float) -> None:
+    """Fill ``rope`` on the host (``Rope(...)`` calls it)."""
+    _check(lib.xs_rope_init(rope.ptr, D, rot, layout, base, scaling, factor, context, low, high, magnitude),
+           "xs_rope_init")
+
+
+_DTYPES = None
+
+
+def _dtype_of(t, name):
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: XS_DTYPE_BF16, torch.float16: XS_DTYPE_FP16}
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}") from None
+
+
+def _on_device(t, name):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise TypeError(f"{name} must be a CUDA tensor on the current device")
+
+
+def _rows(t, name, dtype, D=None):
+    """A [T, H, D] tensor whose heads are contiguous; returns (T, H, row stride)."""
+    if t.dim() != 3 or t.dtype != dtype or (D is not None and t.shape[2] != D):
+        raise TypeError(f"{name} must be a {dtype} tensor [T, H, D]" + (f" with D = {D}" if D else ""))
+    _on_device(t, name)
+    T, H, D = t.shape
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+        raise TypeError(f"{name}: the heads of a row must be contiguous")
+    return T, H, s[0] if T > 1 else H * D
+
+
+def _ints(t, name, dtype_name, *shape):
+    """A contiguous integer tensor of the given shape (None: any extent)."""
+    if (str(t.dtype) != "torch." + dtype_name or t.dim() != len(shape) or not t.is_contiguous() or
+            any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise TypeError(f"{name} must be a contiguous {dtype_name} tensor of shape {list(shape)}")
+    _on_device(t, name)
+    return t.data_ptr()
+
+
+_Strides = _i64 * 3
+
+
+def _cache(t, name, dtype):
+    """A cache [n_pages, page_size, Hkv, D] of any strides with D contiguous."""
+    if t.dim() != 4 or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor [n_pages, page_size, Hkv, D]")
+    _on_device(t, name)
+    s = t.stride()
+    if s[3] != 1:
+        raise TypeError(f"{name}: the channels of a head must be contiguous")
+    return _Strides(s[0], s[1], s[2])
+
+
+def _same(what, *pairs):
+    for a, b in pairs:
+        if a != b:
+            raise TypeError(f"{what}: shapes do not match ({a} against {b})")
+
+
+def xs_rope_fwd(x, positions, out, rope: Rope, grad: bool = False, stream=None) -> None:
+    """Rotary positions of ``x`` [T, H, D] (bf16 or fp16; rows may be slices of a wider matrix)
+    into ``out`` (``out`` may be ``x``); ``grad=True`` applies the transposed map, which takes
+    the gradient of ``out`` to the gradient of ``x``.  ``positions``: int32 [T]."""
+    dtype = _dtype_of(x, "x")
+    T, H, xs_ = _rows(x, "x", x.dtype, rope.D)
+    To, Ho, os_ = _rows(out, "out", x.dtype, rope.D)
+    _same("xs_rope_fwd", ((T, H), (To, Ho)))
+    _check(lib.xs_rope_fwd(x.data_ptr(), _ints(positions, "positions", "int32", T), out.data_ptr(), T, H, xs_, os_,
+                           dtype, int(bool(grad)), rope.ptr, _stream_handle(stream)), "xs_rope_fwd")
+
+
+def xs_rope_append_paged(q, k, v, positions, slots, q_out, k_cache, v_cache, rope: Rope, stream=None) -> None:
+    """Rotate the new tokens' ``q`` [T, H, D] into ``q_out`` and their ``k`` [T, Hkv, D] into the
+    slots of ``k_cache`` [n_pages, page_size, Hkv, D], and copy ``v`` into those of ``v_cache``.
+    ``positions`` int32 [T], ``slots`` int64 [T] (outside the cache: not stored)."""
+    dtype, D = _dtype_of(q, "q"), rope.D
+    T, H, qs = _rows(q, "q", q.dtype, D)
+    Tk, Hkv, ks = _rows(k, "k", q.dtype, D)
+    Tv, Hv, vs = _rows(v, "v", q.dtype, D)
+    To, Ho, os_ = _rows(q_out, "q_out", q.dtype, D)
+    kc, vc = _cache(k_cache, "k_cache", q.dtype), _cache(v_cache, "v_cache", q.dtype)
+    n_pages, page_size = k_cache.shape[:2]
+    _same("xs_rope_append_paged", ((T, Hkv), (Tk, Hv)), ((T, H), (Tv, Ho)), (T, To),
+          (tuple(k_cache.shape), (n_pages, page_size, Hkv, D)), (tuple(v_cache.shape), tuple(k_cache.shape)))
+    _check(lib.xs_rope_append_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ints(positions, "positions", "int32", T),
+                                    _ints(slots, "slots", "int64", T), q_out.data_ptr(), k_cache.data_ptr(),
+                                    v_cache.data_ptr(), T, H, Hkv, qs, ks, vs, os_, n_pages, page_size, kc, vc, dtype,
+                                    rope.ptr, _stream_handle(stream)), "xs_rope_append_paged")
+
+
+def xs_paged_step(cache_lens, new_lens, block_table, free_pages, free_count, page_size: int, kv_lens, cu_q, positions,
+                  slots, free_count_out, status, stream=None) -> None:
+    """Lay out one step on the device: pages for the new tokens of every request (from
+    ``free_pages``, whose first ``free_count`` entries are free) into ``block_table``, pages of
+    ended requests (``new_lens < 0``) back to the list, and ``kv_lens``, ``cu_q``, ``positions``,
+    ``slots``, ``free_count_out`` and ``status`` (include/xsattn.h has the rules).  All int32
+    device tensors, ``slots`` int64; ``free_pages`` has one entry per page of the cache."""
+    n, width = block_table.shape if block_table.dim() == 2 else (0, 0)
+    rows, n_pages = positions.numel(), free_pages.numel()
+    _check(lib.xs_paged_step(_ints(cache_lens, "cache_lens", "int32", n), _ints(new_lens, "new_lens", "int32", n),
+                             _ints(block_table, "block_table", "int32", n, width),
+                             _ints(free_pages, "free_pages", "int32", None),
+                             _ints(free_count, "free_count", "int32", 1), n, width, n_pages, page_size, rows,
+                             _ints(kv_lens, "kv_lens", "int32", n), _ints(cu_q, "cu_q", "int32", n + 1),
+                             _ints(positions, "positions", "int32", None), _ints(slots, "slots", "int64", rows),
+                             _ints(free_count_out, "free_count_out", "int32", 1), _ints(status, "status", "int32", n),
+                             _stream_handle(stream)), "xs_paged_step")
+
+
+def xs_attn_paged_workspace_bytes(n: int, H: int, Hkv: int, D: int) -> int:
+    """Workspace bytes of the paged attention of up to ``n`` sequences."""
+    b = _size(0)
+    _check(lib.xs_attn_paged_workspace_bytes(n, H, Hkv, D, ctypes.byref(b)), "xs_attn_paged_workspace_bytes")
+    return b.value
+
+
+class PagedWorkspace:
+    """Plan and scratch memory of the paged attention of ``n`` sequences with ``H`` query and
+    ``Hkv`` KV heads of dimension ``D`` (torch-allocated, 256-byte aligned).  Filled by
+    :func:`xs_attn_paged_plan`, used by every :func:`xs_attn_paged_fwd` of the step; calls that
+    may overlap in time need one each."""
+
+    def __init__(self, n: int, H: int, Hkv: int, D: int, device="cuda"):
+        import torch
+        self.n, self.H, self.Hkv, self.D = n, H, Hkv, D
+        self.nbytes = xs_attn_paged_workspace_bytes(n, H, Hkv, D)
+        self._buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        self.ptr = (self._buf.data_ptr() + 255) & ~255
+        self.planned = None   # (max_q, causal, window) of the plan
+
+
+def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, causal: bool = True, window: int = 0,
+                       stream=None) -> None:
+    """Divide the attention of a step among the SMs: ``cu_q`` int32 [n + 1], ``kv_lens`` int32 [n]
+    on the device; ``max_q`` an upper estimate of a sequence's new tokens; ``causal`` and
+    ``window`` (0: none) as the attention is to use them."""
+    w = workspace
+    _on_device(w._buf, "workspace")
+    _check(lib.xs_attn_paged_plan(_ints(cu_q, "cu_q", "int32", w.n + 1), _ints(kv_lens, "kv_lens", "int32", w.n), w.n,
+                                  w.H, w.Hkv, w.D, max_q, int(bool(causal)), window, w.ptr, w.nbytes,
+                                  _stream_handle(stream)), "xs_attn_paged_plan")
+    w.planned = (max_q, int(bool(causal)), window)
+
+
+def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale: float, workspace: PagedWorkspace,
+                      lse=None, stream=None) -> None:
+    """Attention of the new tokens ``q`` [T, H, D] over a paged cache ([n_pages, page_size, Hkv, D]
+    each, any strides with D contiguous) as ``workspace`` plans it.  ``block_table`` int32 [n, width];
+    ``layout`` XS_LAYOUT_A2A (P shards [T/P, H, D]), XS_LAYOUT_CONTIGUOUS (one [T, H, D] tensor) or
+    XS_LAYOUT_HEADS (P head shards [T, H/P, D]); ``lse``: fp32 [T, H] or None."""
+    w = workspace
+    if w.planned is None:
+        raise ValueError("xs_attn_paged_fwd: the workspace has no plan (call xs_attn_paged_plan first)")
+    max_q, causal, window = w.planned
+    dtype = _dtype_of(q, "q")
+    T, H, qs = _rows(q, "q", q.dtype, w.D)
+    _on_device(w._buf, "workspace")
+    kc, vc = _cache(k_cache, "k_cache", q.dtype), _cache(v_cache, "v_cache", q.dtype)
+    n_pages, page_size = k_cache.shape[:2]
+    _same("xs_attn_paged_fwd", (H, w.H), (tuple(k_cache.shape[2:]), (w.Hkv, w.D)),
+          (tuple(v_cache.shape), tuple(k_cache.shape)))
+    if block_table.dim() != 2 or str(block_table.dtype) != "torch.int32" or block_table.shape[0] != w.n or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise TypeError(f"block_table must be an int32 tensor [{w.n}, width] with contiguous rows")
+    _on_device(block_table, "block_table")
+    P = len(outs)
+    shape = {XS_LAYOUT_A2A: (T // max(P, 1), H, w.D), XS_LAYOUT_HEADS: (T, H // max(P, 1), w.D)}.get(layout, (T, H, w.D))
+    for o in outs:
+        if tuple(o.shape) != shape or o.dtype != q.dtype or not o.is_contiguous():
+            raise TypeError(f"out must be a contiguous {q.dtype} tensor of shape {list(shape)}")
+        _on_device(o, "out")
+    if lse is not None:
+        if str(lse.dtype) != "torch.float32" or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+            raise TypeError("lse must be a contiguous float32 tensor [T, H]")
+        _on_device(lse, "lse")
+    _check(lib.xs_attn_paged_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), layout,
+                                 _ptr_array([o.data_ptr() for o in outs]), None if lse is None else lse.data_ptr(), T,
+                                 H, w.Hkv, w.D, P, qs, w.n, block_table.shape[1],
+                                 block_table.stride(0) if w.n > 1 else block_table.shape[1], n_pages, page_size, kc, vc,
+                                 dtype, max_q, causal, window, scale, w.ptr, w.nbytes, _stream_handle(stream)),
+           "xs_attn_paged_fwd")
 
 
 def attn_a2a(q, k, v, P: int, scale: float | None = None, stream=None, workspace=None):

@@ -1,6 +1,6 @@
 """Build libxsattn.so (the sm_103a kernels + C ABI) in-tree with nvcc.
 
-Three translation units are compiled in parallel and linked into one shared
+The translation units are compiled in parallel and linked into one shared
 library next to this file.  Only nvcc and the CUDA runtime are needed; no
 PyTorch headers are involved (the C ABI takes plain pointers).
 """
@@ -13,8 +13,9 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["attn_fwd.cu", "relayout.cu", "burst_gap.cu", "api.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", os.path.join("..", "..", "include", "xsattn.h")]
+SOURCES = ["attn_fwd.cu", "attn_paged_rows.cu", "paged_plan.cu", "paged_step.cu", "rope.cu", "relayout.cu",
+           "burst_gap.cu", "api.cu", "api_paged.cu"]
+HEADERS = ["kernels.h", "host.h", "paged.h", "paged_walk.cuh", "device_wait.cuh", "ptx.cuh", os.path.join("..", "..", "include", "xsattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -17,28 +17,27 @@
 #include <vector>
 
 #include "../../include/xsattn.h"
+#include "host.h"
 #include "kernels.h"
+#include "paged.h"
 
 namespace {
 
 thread_local int g_last_cuda_error = 0;
 
+constexpr int MAX_DEVICES = 64;
+std::mutex g_dev_mutex;
+xs::host::DeviceInfo g_dev[MAX_DEVICES];
+
+}  // namespace
+
+namespace xs {
+namespace host {
+
 int cuda_fail(cudaError_t e) {
     g_last_cuda_error = static_cast<int>(e);
     return XS_ERR_CUDA;
 }
-
-struct DeviceInfo {
-    bool known = false;
-    int sms = 0;
-    int major = 0;
-    int minor = 0;
-    int coop = 0;   // cooperative launches supported
-};
-
-constexpr int MAX_DEVICES = 64;
-std::mutex g_dev_mutex;
-DeviceInfo g_dev[MAX_DEVICES];
 
 int device_info(DeviceInfo* out) {
     int dev = 0;
@@ -62,9 +61,9 @@ int device_info(DeviceInfo* out) {
     return XS_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-cudaError_t g_encode_err = cudaSuccess;
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::once_flag g_encode_once;
+static cudaError_t g_encode_err = cudaSuccess;
 
 int get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
     std::call_once(g_encode_once, [] {
@@ -78,6 +77,67 @@ int get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
     *fn = g_encode;
     return XS_OK;
 }
+
+int check_scale(float scale) {
+    if (!std::isfinite(scale) || scale < 0.0f) return XS_ERR_SCALE;
+    return XS_OK;
+}
+
+// Limit for every wait inside the kernels.  One second by default: no single
+// wait of a healthy launch takes more than microseconds.  XSATTN_WAIT_TIMEOUT_NS
+// overrides it (a test sets 0 to make the first unfinished wait expire and
+// check that the launch reports XS_ERR_DEVICE_TIMEOUT and the context stays
+// usable).
+unsigned long long timeout_ns() {
+    const char* env = std::getenv("XSATTN_WAIT_TIMEOUT_NS");
+    if (env && *env) {
+        char* end = nullptr;
+        const unsigned long long v = std::strtoull(env, &end, 10);
+        if (end && *end == '\0') return v;
+    }
+    return 1000000000ull;
+}
+
+// Output layout -> destination parameters and per-buffer byte size.
+int layout_epi(int layout, void* const* outs, int B, int S, int H, int D, int P, xs::EpiParams* epi, int* n_out,
+               int64_t* out_bytes, bool* need_div) {
+    std::memset(epi, 0, sizeof *epi);
+    const int np = (P >= 1 && P <= XS_MAX_P) ? P : 0;
+    switch (layout) {
+        case XS_LAYOUT_A2A:
+            *n_out = np;
+            *out_bytes = P >= 1 ? static_cast<int64_t>(B) * (S / P) * H * D * 2 : 0;
+            *need_div = true;
+            epi->Sl = P >= 1 ? S / P : S;
+            epi->Hl = H;
+            break;
+        case XS_LAYOUT_CONTIGUOUS:
+            *n_out = 1;
+            *out_bytes = static_cast<int64_t>(B) * S * H * D * 2;
+            *need_div = false;
+            epi->Sl = S;
+            epi->Hl = H;
+            break;
+        case XS_LAYOUT_HEADS:
+            *n_out = np;
+            *out_bytes = P >= 1 ? static_cast<int64_t>(B) * S * (H / P) * D * 2 : 0;
+            *need_div = true;
+            epi->Sl = S;
+            epi->Hl = P >= 1 ? H / P : H;
+            break;
+        default:
+            return XS_ERR_LAYOUT;
+    }
+    for (int i = 0; i < *n_out && outs; ++i) epi->ptr[i] = outs[i];
+    return XS_OK;
+}
+
+}  // namespace host
+}  // namespace xs
+
+namespace {
+
+using namespace xs::host;
 
 // [B, S, H, D] bf16 as a 4-D tensor (D, H, S, B); box = 64 channels x 1 head x 128 rows.
 int encode_bshd(CUtensorMap* m, const void* base, int B, int S, int H, int D) {
@@ -97,14 +157,6 @@ int encode_bshd(CUtensorMap* m, const void* base, int B, int S, int H, int D) {
     return XS_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
 // Shape checks shared by every attention entry point.
 int check_shape(int B, int S, int H, int D, int P, bool need_div) {
     if (B < 1 || S < 1 || H < 1 || P < 1) return XS_ERR_SHAPE;
@@ -119,11 +171,6 @@ int check_shape(int B, int S, int H, int D, int P, bool need_div) {
     return XS_OK;
 }
 
-int check_scale(float scale) {
-    if (!std::isfinite(scale) || scale < 0.0f) return XS_ERR_SCALE;
-    return XS_OK;
-}
-
 // Outputs must be pairwise disjoint and disjoint from every input.
 int check_disjoint(const Range* outs, int n_out, const Range* ins, int n_in) {
     for (int i = 0; i < n_out; ++i) {
@@ -133,11 +180,6 @@ int check_disjoint(const Range* outs, int n_out, const Range* ins, int n_in) {
             if (overlaps(outs[i], ins[j])) return XS_ERR_OVERLAP;
     }
     return XS_OK;
-}
-
-Range range_of(const void* p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + static_cast<uintptr_t>(bytes)};
 }
 
 // Validation of (q, k, v, P output buffers of out_bytes each).
@@ -157,21 +199,6 @@ int validate_attn(const void* q, const void* k, const void* v, void* const* outs
     Range o[XS_MAX_P];
     for (int i = 0; i < n_out; ++i) o[i] = range_of(outs[i], out_bytes);
     return check_disjoint(o, n_out, ins, 3);
-}
-
-// Limit for every wait inside the kernels.  One second by default: no single
-// wait of a healthy launch takes more than microseconds.  XSATTN_WAIT_TIMEOUT_NS
-// overrides it (a test sets 0 to make the first unfinished wait expire and
-// check that the launch reports XS_ERR_DEVICE_TIMEOUT and the context stays
-// usable).
-unsigned long long timeout_ns() {
-    const char* env = std::getenv("XSATTN_WAIT_TIMEOUT_NS");
-    if (env && *env) {
-        char* end = nullptr;
-        const unsigned long long v = std::strtoull(env, &end, 10);
-        if (end && *end == '\0') return v;
-    }
-    return 1000000000ull;
 }
 
 // Work schedule of one attention launch.  Plain: grid = min(tiles, SMs), tile
@@ -364,40 +391,6 @@ int run_attention(const void* q, const void* k, const void* v, const void* const
                            : xs::launch_attn<64>(tq, tk, tv, a, grid, split, stream);
     }
     if (e != cudaSuccess) return cuda_fail(e);
-    return XS_OK;
-}
-
-// Output layout -> destination parameters and per-buffer byte size.
-int layout_epi(int layout, void* const* outs, int B, int S, int H, int D, int P, xs::EpiParams* epi, int* n_out,
-               int64_t* out_bytes, bool* need_div) {
-    std::memset(epi, 0, sizeof *epi);
-    const int np = (P >= 1 && P <= XS_MAX_P) ? P : 0;
-    switch (layout) {
-        case XS_LAYOUT_A2A:
-            *n_out = np;
-            *out_bytes = P >= 1 ? static_cast<int64_t>(B) * (S / P) * H * D * 2 : 0;
-            *need_div = true;
-            epi->Sl = P >= 1 ? S / P : S;
-            epi->Hl = H;
-            break;
-        case XS_LAYOUT_CONTIGUOUS:
-            *n_out = 1;
-            *out_bytes = static_cast<int64_t>(B) * S * H * D * 2;
-            *need_div = false;
-            epi->Sl = S;
-            epi->Hl = H;
-            break;
-        case XS_LAYOUT_HEADS:
-            *n_out = np;
-            *out_bytes = P >= 1 ? static_cast<int64_t>(B) * S * (H / P) * D * 2 : 0;
-            *need_div = true;
-            epi->Sl = S;
-            epi->Hl = P >= 1 ? H / P : H;
-            break;
-        default:
-            return XS_ERR_LAYOUT;
-    }
-    for (int i = 0; i < *n_out && outs; ++i) epi->ptr[i] = outs[i];
     return XS_OK;
 }
 
@@ -998,7 +991,17 @@ int xs_attn_get_device_error_info(void* stream, int* info, int n_info) {
     if (e != cudaSuccess) return cuda_fail(e);
     int v = 0, drain = 0;
     xs::DeviceErrorInfo r{};
-    if ((e = xs::read_and_clear_device_error(&v, &r, &drain)) != cudaSuccess) return cuda_fail(e);
+    // each kernel family keeps its own words; the first family with an error is reported, all are cleared
+    for (auto read : {xs::read_and_clear_device_error, xs::read_and_clear_paged_rows_error}) {
+        int v1 = 0, d1 = 0;
+        xs::DeviceErrorInfo r1{};
+        if ((e = read(&v1, &r1, &d1)) != cudaSuccess) return cuda_fail(e);
+        if (v == 0 && v1 != 0) {
+            v = v1;
+            r = r1;
+        }
+        drain |= d1;
+    }
     const int fields[8] = {v ? r.code : 0, r.cta, r.warp, r.lane, r.site, r.detail[0], r.detail[1], r.detail[2]};
     for (int i = 0; i < n_info; ++i) info[i] = v ? fields[i] : 0;
     if (drain) return XS_ERR_DEVICE_DRAIN;
@@ -1028,6 +1031,11 @@ const char* xs_attn_error_string(int code) {
             return "after an expired wait, a kernel gave up waiting for its own copies or MMAs in flight";
         case XS_ERR_DEVICE_BOUNDS: return "an index check inside a kernel failed; the access was skipped";
         case XS_ERR_UNAVAILABLE: return "this variant is disabled in this build";
+        case XS_ERR_DTYPE: return "dtype must be XS_DTYPE_BF16 or XS_DTYPE_FP16";
+        case XS_ERR_PAGE: return "page size must be a power of two from 16 to 1024";
+        case XS_ERR_ROPE:
+            return "rotary parameters: rot a multiple of 16 up to D, base >= 1, factor >= 1, context >= 1, low < high, "
+                   "all finite";
         default: return "unknown xsattn error code";
     }
 }

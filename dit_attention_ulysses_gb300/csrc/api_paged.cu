@@ -1,0 +1,494 @@
+// C ABI of the paged-cache entry points: host-side argument checks (everything is
+// checked before any CUDA call, so an invalid call launches nothing), tensor maps and
+// launches.  The declarations and their contracts are in include/xsattn.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/xsattn.h"
+#include "host.h"
+#include "kernels.h"
+#include "paged.h"
+
+namespace {
+
+using namespace xs::host;
+
+constexpr int64_t MAX_ELEMS = int64_t(1) << 40;
+constexpr int64_t MAX_STRIDE = int64_t(1) << 38;   // elements: TMA strides stay below 2^40 bytes
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// T rows of `width` elements, `stride` elements apart (2 bytes each).
+struct Rows {
+    uintptr_t base;
+    int64_t n, width, stride;
+};
+
+Rows rows_of(const void* p, int64_t n, int64_t width, int64_t stride) {
+    return Rows{reinterpret_cast<uintptr_t>(p), n, width * 2, stride * 2};
+}
+
+Range span(const Rows& r) {
+    return Range{r.base, r.base + static_cast<uintptr_t>(r.n > 0 ? (r.n - 1) * r.stride + r.width : 0)};
+}
+
+// Rows of equal stride (columns of one wider matrix) overlap only where their
+// columns do; otherwise the address ranges decide.
+bool rows_overlap(const Rows& a, const Rows& b) {
+    if (!overlaps(span(a), span(b))) return false;
+    if (a.stride != b.stride || a.stride <= 0) return true;
+    const int64_t d = b.base >= a.base ? static_cast<int64_t>((b.base - a.base) % static_cast<uintptr_t>(a.stride))
+                                       : a.stride - 1 - static_cast<int64_t>((a.base - b.base - 1) %
+                                                                             static_cast<uintptr_t>(a.stride));
+    return d < a.width || a.stride - d < b.width;
+}
+
+int log2_of(int x) {
+    int k = 0;
+    while ((1 << k) < x) ++k;
+    return k;
+}
+
+int check_page(int page_size, int n_pages) {
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return XS_ERR_PAGE;
+    if (n_pages < 1 || static_cast<int64_t>(n_pages) * page_size > INT32_MAX) return XS_ERR_SHAPE;
+    return XS_OK;
+}
+
+// Strides (page, token, head) of a cache; those of an extent of one are not used.
+struct CacheStrides {
+    long long s[3];
+};
+
+int check_cache(const long long* strides, int n_pages, int page_size, int Hkv, int D, CacheStrides* out) {
+    if (!strides) return XS_ERR_NULL;
+    const int dims[3] = {n_pages, page_size, Hkv};
+    for (int i = 0; i < 3; ++i) {
+        long long s = dims[i] == 1 ? D : strides[i];
+        if (s < D || s > MAX_STRIDE) return XS_ERR_SHAPE;
+        if (s % 8 != 0) return XS_ERR_ALIGNMENT;
+        out->s[i] = s;
+    }
+    return XS_OK;
+}
+
+Range cache_span(const void* p, const CacheStrides& c, int n_pages, int page_size, int Hkv, int D) {
+    const int64_t last = (n_pages - 1) * static_cast<int64_t>(c.s[0]) + (page_size - 1) * static_cast<int64_t>(c.s[1]) +
+                         (Hkv - 1) * static_cast<int64_t>(c.s[2]) + D;
+    return range_of(p, last * 2);
+}
+
+int check_rope(const xs_rope* rope) {
+    if (!rope) return XS_ERR_NULL;
+    if (rope->D != 64 && rope->D != 128) return XS_ERR_HEAD_DIM;
+    if (rope->rot < 16 || rope->rot > rope->D || rope->rot % 16 != 0) return XS_ERR_ROPE;
+    if (rope->layout != XS_ROPE_HALF && rope->layout != XS_ROPE_INTERLEAVED) return XS_ERR_LAYOUT;
+    if (!std::isfinite(rope->magnitude)) return XS_ERR_ROPE;
+    return XS_OK;
+}
+
+int check_rows(int T, int H, int D, long long stride) {
+    if (T < 1 || H < 1 || H > 4096) return XS_ERR_SHAPE;
+    if (stride < static_cast<long long>(H) * D || stride > MAX_STRIDE || T * static_cast<int64_t>(stride) > MAX_ELEMS)
+        return XS_ERR_SHAPE;
+    if (stride % 8 != 0) return XS_ERR_ALIGNMENT;
+    return XS_OK;
+}
+
+void fill_rope(xs::RopeArgs* a, const xs_rope* rope, int T, int H, const int* positions) {
+    std::memset(a, 0, sizeof *a);
+    a->positions = positions;
+    a->T = T;
+    a->H = H;
+    a->D = rope->D;
+    a->rot = rope->rot;
+    a->magnitude = rope->magnitude;
+    std::memcpy(a->turns, rope->turns, sizeof a->turns);
+}
+
+// [n_pages, page, Hkv, D] as a 4-D tensor (D, token, head, page); box = 64 channels x
+// `box` tokens of one head of one page.
+int encode_cache(CUtensorMap* m, const void* base, const CacheStrides& c, int n_pages, int page_size, int Hkv, int D,
+                 int box_rows, int dtype) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    int rc = get_encoder(&enc);
+    if (rc != XS_OK) return rc;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size),
+                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(n_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.s[1]) * 2, static_cast<cuuint64_t>(c.s[2]) * 2,
+                                   static_cast<cuuint64_t>(c.s[0]) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type =
+        dtype == XS_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = enc(m, type, 4, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return XS_OK;
+}
+
+// ---- tiling of the paged attention, a function of the shape alone
+constexpr int ROWS_SMALL = 16, ROWS_WIDE = 32;
+
+struct Tiling {
+    int rows;   // packed query rows of a tile
+    xs::PagedTiling t;
+};
+
+Tiling make_tiling(int G, int max_q, int sms) {
+    Tiling x;
+    const int64_t need = static_cast<int64_t>(G) * max_q;
+    x.rows = need <= ROWS_SMALL ? ROWS_SMALL : ROWS_WIDE;
+    x.t.tokens = x.rows / G;
+    x.t.block = 64;
+    x.t.grid = 2 * sms;
+    x.t.start_cost = 128;
+    x.t.snap = 1;
+    return x;
+}
+
+int check_paged_shape(int n, int H, int Hkv, int D, int max_q, int causal, int window) {
+    if (n < 1 || n > xs::MAX_PAGED_SEQS || H < 1 || Hkv < 1 || max_q < 1) return XS_ERR_SHAPE;
+    if (D != 64 && D != 128) return XS_ERR_HEAD_DIM;
+    if (H % Hkv != 0) return XS_ERR_DIVISIBILITY;
+    if (H / Hkv > ROWS_WIDE || H > 4096) return XS_ERR_SHAPE;
+    if (window < 0 || (window > 0 && !causal)) return XS_ERR_SHAPE;
+    return XS_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Workspace: header | counters | ranges | sequences | partial (m, l) | partial O.  Sized
+// for every tiling of the shape, so one workspace serves steps of any max_q.
+size_t paged_work(char* base, int n, int D, int sms, xs::PagedWork* w) {
+    const size_t grid = 2 * static_cast<size_t>(sms);
+    const size_t part_rows = 2 * grid * ROWS_WIDE;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += align256(bytes);
+        return base ? base + at : nullptr;
+    };
+    char* p;
+    p = take(sizeof(xs::PagedHeader));
+    if (w) w->header = reinterpret_cast<xs::PagedHeader*>(p);
+    p = take(grid * sizeof(unsigned));
+    if (w) w->counters = reinterpret_cast<unsigned*>(p);
+    p = take(grid * sizeof(xs::PagedRange));
+    if (w) w->ranges = reinterpret_cast<xs::PagedRange*>(p);
+    p = take(static_cast<size_t>(n) * sizeof(xs::PagedSeq));
+    if (w) w->seqs = reinterpret_cast<xs::PagedSeq*>(p);
+    p = take(part_rows * sizeof(float2));
+    if (w) w->part_ml = reinterpret_cast<float2*>(p);
+    p = take(part_rows * D * sizeof(float));
+    if (w) w->part_o = reinterpret_cast<float*>(p);
+    return off;
+}
+
+}  // namespace
+
+extern "C" {
+
+int xs_rope_init(xs_rope* rope, int D, int rot, int layout, double base, int scaling, double factor, double context,
+                 double low, double high, double magnitude) {
+    if (!rope) return XS_ERR_NULL;
+    if (D != 64 && D != 128) return XS_ERR_HEAD_DIM;
+    if (rot < 16 || rot > D || rot % 16 != 0) return XS_ERR_ROPE;
+    if (layout != XS_ROPE_HALF && layout != XS_ROPE_INTERLEAVED) return XS_ERR_LAYOUT;
+    if (!std::isfinite(base) || base < 1.0 || !std::isfinite(magnitude) || std::fabs(magnitude) > 1e30)
+        return XS_ERR_ROPE;
+    if (scaling < XS_ROPE_PLAIN || scaling > XS_ROPE_BY_PARTS) return XS_ERR_ROPE;
+    if (scaling != XS_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0)) return XS_ERR_ROPE;
+    if (scaling == XS_ROPE_BY_PARTS && !(context >= 1.0 && std::isfinite(context) && high > low && std::isfinite(low) &&
+                                         std::isfinite(high)))
+        return XS_ERR_ROPE;
+    const double tau = 6.283185307179586476925286766559;
+    std::memset(rope, 0, sizeof *rope);
+    rope->D = D;
+    rope->rot = rot;
+    rope->layout = layout;
+    rope->magnitude = static_cast<float>(magnitude);
+    if (scaling == XS_ROPE_STRETCH) base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double theta = std::pow(base, -2.0 * i / rot);
+        if (scaling == XS_ROPE_LINEAR) theta /= factor;
+        if (scaling == XS_ROPE_BY_PARTS) {
+            double keep = (theta * context / tau - low) / (high - low);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            theta = theta * keep + theta / factor * (1.0 - keep);
+        }
+        rope->turns[i] = static_cast<unsigned long long>(theta / tau * 18446744073709551616.0 + 0.5);   // < 2^64 / 6
+    }
+    return XS_OK;
+}
+
+int xs_rope_fwd(const void* x, const int* positions, void* out, int T, int H, long long x_stride,
+                long long out_stride, int dtype, int grad, const xs_rope* rope, void* stream) {
+    if (!x || !positions || !out) return XS_ERR_NULL;
+    int rc = check_rope(rope);
+    if (rc != XS_OK) return rc;
+    if (dtype != XS_DTYPE_BF16 && dtype != XS_DTYPE_FP16) return XS_ERR_DTYPE;
+    if ((rc = check_rows(T, H, rope->D, x_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, H, rope->D, out_stride)) != XS_OK) return rc;
+    if (!aligned16(x) || !aligned16(out) || !aligned(positions, 4)) return XS_ERR_ALIGNMENT;
+    const int64_t width = static_cast<int64_t>(H) * rope->D;
+    const Rows in = rows_of(x, T, width, x_stride), o = rows_of(out, T, width, out_stride);
+    if (!(x == out && x_stride == out_stride) && rows_overlap(in, o)) return XS_ERR_OVERLAP;
+    if (overlaps(span(o), range_of(positions, static_cast<int64_t>(T) * 4))) return XS_ERR_OVERLAP;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != XS_OK) return rc;
+    xs::RopeArgs a;
+    fill_rope(&a, rope, T, H, positions);
+    a.q = x;
+    a.q_out = out;
+    a.q_stride = x_stride;
+    a.qo_stride = out_stride;
+    a.grad = grad ? 1 : 0;
+    const cudaError_t e =
+        xs::launch_rope(a, dtype, rope->layout, false, dev.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? XS_OK : cuda_fail(e);
+}
+
+int xs_rope_append_paged(const void* q, const void* k, const void* v, const int* positions, const long long* slots,
+                         void* q_out, void* k_cache, void* v_cache, int T, int H, int Hkv, long long q_stride,
+                         long long k_stride, long long v_stride, long long q_out_stride, int n_pages, int page_size,
+                         const long long* k_cache_strides, const long long* v_cache_strides, int dtype,
+                         const xs_rope* rope, void* stream) {
+    if (!q || !k || !v || !positions || !slots || !q_out || !k_cache || !v_cache) return XS_ERR_NULL;
+    int rc = check_rope(rope);
+    if (rc != XS_OK) return rc;
+    if (dtype != XS_DTYPE_BF16 && dtype != XS_DTYPE_FP16) return XS_ERR_DTYPE;
+    const int D = rope->D;
+    if ((rc = check_rows(T, H, D, q_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, Hkv, D, k_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, Hkv, D, v_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, H, D, q_out_stride)) != XS_OK) return rc;
+    if ((rc = check_page(page_size, n_pages)) != XS_OK) return rc;
+    CacheStrides ks, vs;
+    if ((rc = check_cache(k_cache_strides, n_pages, page_size, Hkv, D, &ks)) != XS_OK) return rc;
+    if ((rc = check_cache(v_cache_strides, n_pages, page_size, Hkv, D, &vs)) != XS_OK) return rc;
+    for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_cache),
+                          static_cast<const void*>(v_cache)})
+        if (!aligned16(p)) return XS_ERR_ALIGNMENT;
+    if (!aligned(positions, 4) || !aligned(slots, 8)) return XS_ERR_ALIGNMENT;
+    const Rows rq = rows_of(q, T, static_cast<int64_t>(H) * D, q_stride),
+               rk = rows_of(k, T, static_cast<int64_t>(Hkv) * D, k_stride),
+               rv = rows_of(v, T, static_cast<int64_t>(Hkv) * D, v_stride),
+               ro = rows_of(q_out, T, static_cast<int64_t>(H) * D, q_out_stride);
+    if (!(q == q_out && q_stride == q_out_stride) && rows_overlap(rq, ro)) return XS_ERR_OVERLAP;
+    if (rows_overlap(rk, ro) || rows_overlap(rv, ro)) return XS_ERR_OVERLAP;
+    const Range kc = cache_span(k_cache, ks, n_pages, page_size, Hkv, D),
+                vc = cache_span(v_cache, vs, n_pages, page_size, Hkv, D);
+    // K and V may be interleaved in one buffer (equal strides, other heads or pages); which
+    // elements two strided caches share is the caller's to keep apart, equal pointers are refused
+    if (k_cache == v_cache) return XS_ERR_OVERLAP;
+    const Range pos = range_of(positions, static_cast<int64_t>(T) * 4), sl = range_of(slots, static_cast<int64_t>(T) * 8);
+    for (const Range& c : {kc, vc}) {
+        for (const Rows* r : {&rq, &rk, &rv, &ro})
+            if (overlaps(c, span(*r))) return XS_ERR_OVERLAP;
+        if (overlaps(c, pos) || overlaps(c, sl)) return XS_ERR_OVERLAP;
+    }
+    if (overlaps(span(ro), pos) || overlaps(span(ro), sl)) return XS_ERR_OVERLAP;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != XS_OK) return rc;
+    xs::RopeArgs a;
+    fill_rope(&a, rope, T, H, positions);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.slots = slots;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.qo_stride = q_out_stride;
+    for (int i = 0; i < 3; ++i) {
+        a.ks[i] = ks.s[i];
+        a.vs[i] = vs.s[i];
+    }
+    a.n_slots = static_cast<long long>(n_pages) * page_size;
+    a.Hkv = Hkv;
+    a.page_shift = log2_of(page_size);
+    const cudaError_t e = xs::launch_rope(a, dtype, rope->layout, true, dev.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? XS_OK : cuda_fail(e);
+}
+
+int xs_paged_step(const int* cache_lens, const int* new_lens, int* block_table, int* free_pages,
+                  const int* free_count, int n, int table_width, int n_pages, int page_size, int rows, int* kv_lens,
+                  int* cu_q, int* positions, long long* slots, int* free_count_out, int* status, void* stream) {
+    const void* all[] = {cache_lens, new_lens, free_count, block_table, free_pages, kv_lens, cu_q, positions,
+                         free_count_out, status, slots};
+    for (const void* p : all)
+        if (!p) return XS_ERR_NULL;
+    if (n < 1 || n > xs::MAX_PAGED_SEQS || table_width < 1 || rows < 1) return XS_ERR_SHAPE;
+    int rc = check_page(page_size, n_pages);
+    if (rc != XS_OK) return rc;
+    if (static_cast<int64_t>(table_width) * page_size > INT32_MAX) return XS_ERR_SHAPE;
+    for (const void* p : all)
+        if (!aligned(p, 4)) return XS_ERR_ALIGNMENT;
+    if (!aligned(slots, 8)) return XS_ERR_ALIGNMENT;
+    const int64_t n4 = static_cast<int64_t>(n) * 4, r4 = static_cast<int64_t>(rows) * 4;
+    const Range ins[3] = {range_of(cache_lens, n4), range_of(new_lens, n4), range_of(free_count, 4)};
+    const Range outs[8] = {range_of(block_table, n4 * table_width), range_of(free_pages, static_cast<int64_t>(n_pages) * 4),
+                           range_of(kv_lens, n4), range_of(cu_q, n4 + 4), range_of(positions, r4),
+                           range_of(free_count_out, 4), range_of(status, n4), range_of(slots, 2 * r4)};
+    for (int i = 0; i < 8; ++i) {
+        for (int j = i + 1; j < 8; ++j)
+            if (overlaps(outs[i], outs[j])) return XS_ERR_OVERLAP;
+        for (const Range& r : ins)
+            if (overlaps(outs[i], r)) return XS_ERR_OVERLAP;
+    }
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != XS_OK) return rc;
+    xs::StepArgs a;
+    a.cache_lens = cache_lens;
+    a.new_lens = new_lens;
+    a.table = block_table;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.kv_lens = kv_lens;
+    a.cu_q = cu_q;
+    a.positions = positions;
+    a.slots = slots;
+    a.free_count_out = free_count_out;
+    a.status = status;
+    a.n = n;
+    a.width = table_width;
+    a.n_pages = n_pages;
+    a.rows = rows;
+    a.page_shift = log2_of(page_size);
+    const cudaError_t e = xs::launch_paged_step(a, dev.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? XS_OK : cuda_fail(e);
+}
+
+int xs_attn_paged_workspace_bytes(int n, int H, int Hkv, int D, size_t* bytes) {
+    if (!bytes) return XS_ERR_NULL;
+    int rc = check_paged_shape(n, H, Hkv, D, 1, 1, 0);
+    if (rc != XS_OK) return rc;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != XS_OK) return rc;
+    *bytes = paged_work(nullptr, n, D, dev.sms, nullptr);
+    return XS_OK;
+}
+
+int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,
+                       int window, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!cu_q || !kv_lens || !workspace) return XS_ERR_NULL;
+    int rc = check_paged_shape(n, H, Hkv, D, max_q, causal, window);
+    if (rc != XS_OK) return rc;
+    if (!aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(workspace, 256)) return XS_ERR_ALIGNMENT;
+    const Range w = range_of(workspace, static_cast<int64_t>(workspace_bytes));
+    if (overlaps(w, range_of(cu_q, 4 * (static_cast<int64_t>(n) + 1))) || overlaps(w, range_of(kv_lens, 4 * static_cast<int64_t>(n))))
+        return XS_ERR_OVERLAP;
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != XS_OK) return rc;
+    xs::PagedPlanArgs a;
+    std::memset(&a, 0, sizeof a);
+    if (workspace_bytes < paged_work(static_cast<char*>(workspace), n, D, dev.sms, &a.work)) return XS_ERR_WORKSPACE;
+    a.cu_q = cu_q;
+    a.kv_lens = kv_lens;
+    a.n = n;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.causal = causal ? 1 : 0;
+    a.window = window;
+    a.tile = make_tiling(H / Hkv, max_q, dev.sms).t;
+    const cudaError_t e = xs::launch_paged_plan(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? XS_OK : cuda_fail(e);
+}
+
+int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, const int* block_table, int layout,
+                      void* const* outs, float* lse, int T, int H, int Hkv, int D, int P, long long q_stride, int n,
+                      int table_width, long long table_stride, int n_pages, int page_size,
+                      const long long* k_cache_strides, const long long* v_cache_strides, int dtype, int max_q,
+                      int causal, int window, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !block_table || !outs || !workspace) return XS_ERR_NULL;
+    xs::PagedAttnArgs a;
+    std::memset(&a, 0, sizeof a);
+    int n_out = 0;
+    int64_t out_bytes = 0;
+    bool need_div = false;
+    if (T < 1) return XS_ERR_SHAPE;
+    int rc = check_paged_shape(n, H, Hkv, D, max_q, causal, window);
+    if (rc != XS_OK) return rc;
+    if ((rc = layout_epi(layout, outs, 1, T, H, D, P, &a.epi, &n_out, &out_bytes, &need_div)) != XS_OK) return rc;
+    if (layout != XS_LAYOUT_CONTIGUOUS) {
+        if (P < 1) return XS_ERR_SHAPE;
+        if (P > XS_MAX_P) return XS_ERR_TOO_MANY_RANKS;
+        if (T % P != 0 || H % P != 0) return XS_ERR_DIVISIBILITY;
+    }
+    if (dtype != XS_DTYPE_BF16 && dtype != XS_DTYPE_FP16) return XS_ERR_DTYPE;
+    if ((rc = check_rows(T, H, D, q_stride)) != XS_OK) return rc;
+    if ((rc = check_page(page_size, n_pages)) != XS_OK) return rc;
+    if (table_width < 1 || table_stride < (n > 1 ? table_width : 0)) return XS_ERR_SHAPE;
+    CacheStrides ks, vs;
+    if ((rc = check_cache(k_cache_strides, n_pages, page_size, Hkv, D, &ks)) != XS_OK) return rc;
+    if ((rc = check_cache(v_cache_strides, n_pages, page_size, Hkv, D, &vs)) != XS_OK) return rc;
+    if ((rc = check_scale(scale)) != XS_OK) return rc;
+    for (int i = 0; i < n_out; ++i)
+        if (!outs[i]) return XS_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned(block_table, 4) || !aligned(lse, 4) ||
+        !aligned(workspace, 256))
+        return XS_ERR_ALIGNMENT;
+    for (int i = 0; i < n_out; ++i)
+        if (!aligned16(outs[i])) return XS_ERR_ALIGNMENT;
+    const Range ins[4] = {span(rows_of(q, T, static_cast<int64_t>(H) * D, q_stride)),
+                          cache_span(k_cache, ks, n_pages, page_size, Hkv, D),
+                          cache_span(v_cache, vs, n_pages, page_size, Hkv, D),
+                          range_of(block_table, ((n - 1) * static_cast<int64_t>(table_stride) + table_width) * 4)};
+    Range o[XS_MAX_P + 2];
+    int n_all = 0;
+    for (int i = 0; i < n_out; ++i) o[n_all++] = range_of(outs[i], out_bytes);
+    if (lse) o[n_all++] = range_of(lse, static_cast<int64_t>(T) * H * 4);
+    o[n_all++] = range_of(workspace, static_cast<int64_t>(workspace_bytes));
+    for (int i = 0; i < n_all; ++i) {
+        for (int j = i + 1; j < n_all; ++j)
+            if (overlaps(o[i], o[j])) return XS_ERR_OVERLAP;
+        for (const Range& r : ins)
+            if (overlaps(o[i], r)) return XS_ERR_OVERLAP;
+    }
+    DeviceInfo dev;
+    if ((rc = device_info(&dev)) != XS_OK) return rc;
+    if (workspace_bytes < paged_work(static_cast<char*>(workspace), n, D, dev.sms, &a.work)) return XS_ERR_WORKSPACE;
+    const Tiling tiling = make_tiling(H / Hkv, max_q, dev.sms);
+    a.q = q;
+    a.table = block_table;
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.table_stride = table_stride;
+    a.T = T;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.G = H / Hkv;
+    a.D = D;
+    a.n = n;
+    a.width = table_width;
+    a.page_shift = log2_of(page_size);
+    a.n_pages = n_pages;
+    a.causal = causal ? 1 : 0;
+    a.window = window;
+    a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.tile = tiling.t;
+    a.timeout_ns = timeout_ns();
+    a.fd_G = xs::make_fastdiv(a.G);
+    a.epi.fd_Sl = xs::make_fastdiv(a.epi.Sl);
+    a.epi.fd_Hl = xs::make_fastdiv(a.epi.Hl);
+    const int box = page_size < 32 ? page_size : 32;
+    CUtensorMap tk, tv;
+    if ((rc = encode_cache(&tk, k_cache, ks, n_pages, page_size, Hkv, D, box, dtype)) != XS_OK) return rc;
+    if ((rc = encode_cache(&tv, v_cache, vs, n_pages, page_size, Hkv, D, box, dtype)) != XS_OK) return rc;
+    const cudaError_t e =
+        xs::launch_attn_paged_rows(tk, tv, a, dtype, tiling.rows, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? XS_OK : cuda_fail(e);
+}
+
+}  // extern "C"

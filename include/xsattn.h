@@ -69,8 +69,17 @@ enum {
     XS_ERR_DEVICE_DRAIN = -14,   /* after an expired wait, a copy or MMA may still have
                                     been in flight when a CTA freed its tensor memory   */
     XS_ERR_DEVICE_BOUNDS = -15,  /* a kernel's index check failed; the access was skipped */
-    XS_ERR_UNAVAILABLE = -16     /* reserved for a variant disabled in a build; no entry
+    XS_ERR_UNAVAILABLE = -16,    /* reserved for a variant disabled in a build; no entry
                                     point of this build returns it                      */
+    XS_ERR_DTYPE = -17,          /* dtype is not an XS_DTYPE_* value                    */
+    XS_ERR_PAGE = -18,           /* page size is not a power of two from 16 to 1024     */
+    XS_ERR_ROPE = -19            /* rotary parameters out of range                      */
+};
+
+/* Element types of the paged-cache and rotary entry points (the others are bf16). */
+enum {
+    XS_DTYPE_BF16 = 0,
+    XS_DTYPE_FP16 = 1
 };
 
 /* Output layouts of xs_attn_fwd_balanced (the three layouts of the entry points
@@ -387,6 +396,181 @@ int xs_attn_causal_fwd(const void* q, const void* k, const void* v, int layout, 
 int xs_attn_varlen_fwd(const void* q, const void* k, const void* v, const int* seqlens, int n_seqs,
                        int causal, int layout, void* const* outs, int T, int H, int D, int P, float scale,
                        void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Serving: new tokens over a paged cache.
+ *
+ * Keys and values of earlier tokens are kept in pages of `page_size` tokens (a power
+ * of two, 16 .. 1024).  A cache is [n_pages, page_size, Hkv, D], D contiguous, with
+ * caller-given strides between pages, tokens and heads (elements, multiples of 8, at
+ * least D), so token-major and head-major pages are the same to the library, and K and
+ * V may share a buffer.  Row i of a block table [n, width] lists the pages of request
+ * i in order; entries past its tokens are not read.  A step brings a_i new tokens to
+ * request i, which holds c_i already:
+ *     xs_paged_step         pages, positions and slots of the new tokens
+ *     xs_attn_paged_plan    the division of the step's attention (once per step)
+ *     then per layer:
+ *     xs_rope_append_paged  rotary positions; K and V into the cache
+ *     xs_attn_paged_fwd     attention of the new tokens over the cache
+ * Lengths, tables, positions and slots live on the device and nothing synchronises, so
+ * a step can be captured in a CUDA graph and replayed with other lengths.
+ * Calls are asynchronous on `stream`; every buffer is the caller's and must belong to
+ * the current device; two calls that may run at the same time must not share a
+ * workspace.  Inputs hold finite values, except in places that the definitions below
+ * do not read (entries, slots and rows past the sequences).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * xs_rope -- rotary positions of a model, filled by xs_rope_init (plain data; the
+ * caller owns it and may copy it).  Pair i of the first `rot` channels of a head turns
+ * by position * theta_i; the channels after them pass through.
+ */
+enum { XS_ROPE_HALF = 0,           /* pair i: channels (i, i + rot/2)      */
+       XS_ROPE_INTERLEAVED = 1 };  /* pair i: channels (2i, 2i + 1)        */
+
+enum { XS_ROPE_PLAIN = 0,     /* theta_i = base^(-2i/rot)                                    */
+       XS_ROPE_LINEAR = 1,    /* theta_i / factor                                            */
+       XS_ROPE_STRETCH = 2,   /* base * factor^(rot/(rot-2)) in place of base: the slowest
+                                 pair slows down by `factor`, the fastest not at all         */
+       XS_ROPE_BY_PARTS = 3   /* pairs that turn more than `high` times within `context`
+                                 positions keep theta_i, those that turn less than `low`
+                                 times get theta_i / factor, linear in the turns between     */
+};
+
+typedef struct xs_rope {
+    unsigned long long turns[64];  /* theta_i / (2 pi) * 2^64                     */
+    float magnitude;               /* factor on cos and sin                       */
+    int layout;                    /* XS_ROPE_HALF or XS_ROPE_INTERLEAVED         */
+    int rot;                       /* rotated channels of a head                  */
+    int D;                         /* head dimension                              */
+} xs_rope;
+
+/*
+ * xs_rope_init -- fills `rope` on the host (no CUDA call).
+ *   D 64 or 128; rot a multiple of 16, 16 .. D; base >= 1; factor >= 1 (ignored by
+ *   XS_ROPE_PLAIN); context >= 1, low < high (XS_ROPE_BY_PARTS only); magnitude finite
+ *   (1 for the plain rotation).
+ * Returns XS_OK, XS_ERR_NULL, XS_ERR_HEAD_DIM, XS_ERR_LAYOUT or XS_ERR_ROPE.
+ */
+int xs_rope_init(xs_rope* rope, int D, int rot, int layout, double base, int scaling, double factor,
+                 double context, double low, double high, double magnitude);
+
+/*
+ * xs_rope_fwd -- rotary positions of one tensor:
+ *     (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t),  t = positions[row] * theta_i
+ * in fp32, rounded once; the angle is reduced exactly whatever the position (also a
+ * negative one).
+ *   x, out     device, [T, H, D] of `dtype`, rows x_stride / out_stride elements apart
+ *              (multiples of 8, at least H*D; a slice of a fused projection is fine).
+ *              out == x with equal strides rotates in place; otherwise no overlap.
+ *   positions  device int32 [T].
+ *   grad       0: as above; otherwise the transposed map (t -> -t), which takes the
+ *              gradient of `out` to the gradient of `x`.
+ * Returns XS_OK or XS_ERR_NULL / _HEAD_DIM / _ROPE / _LAYOUT / _DTYPE / _SHAPE / _ALIGNMENT /
+ * _OVERLAP / _UNSUPPORTED_DEVICE / _CUDA.
+ */
+int xs_rope_fwd(const void* x, const int* positions, void* out, int T, int H, long long x_stride,
+                long long out_stride, int dtype, int grad, const xs_rope* rope, void* stream);
+
+/*
+ * xs_rope_append_paged -- rotates the new tokens' q into q_out and their k into the K
+ * cache, and copies v into the V cache, in one launch.  Row t goes to slot slots[t] =
+ * page * page_size + offset; a slot outside [0, n_pages * page_size) (padding) stores
+ * no K and V.  Rows with equal slots race.  Values as xs_rope_fwd's, bit for bit.
+ *   q, q_out   [T, H, D]; k, v [T, Hkv, D], row strides as in xs_rope_fwd; q_out may be
+ *              q itself (in place), and must not overlap k, v or a cache otherwise.
+ *   positions  device int32 [T];  slots device int64 [T].
+ *   k_cache_strides, v_cache_strides  host, 3 each: elements between pages, tokens of a
+ *              page and heads.
+ */
+int xs_rope_append_paged(const void* q, const void* k, const void* v, const int* positions, const long long* slots,
+                         void* q_out, void* k_cache, void* v_cache, int T, int H, int Hkv, long long q_stride,
+                         long long k_stride, long long v_stride, long long q_out_stride, int n_pages, int page_size,
+                         const long long* k_cache_strides, const long long* v_cache_strides, int dtype,
+                         const xs_rope* rope, void* stream);
+
+/*
+ * xs_paged_step -- lays out one step on the device.  With c_i = cache_lens[i], a_i =
+ * new_lens[i], held_i = ceil(c_i / page_size), need_i = ceil((c_i + a_i) / page_size) - held_i:
+ *   a_i < 0   the request has ended: its held_i pages go behind the free list (in the
+ *             order of the requests and of their rows), kv_lens[i] = 0.
+ *   a_i >= 0  it gets need_i pages from the end of the free list (in the order of the
+ *             requests, each page one entry further down) into columns [held_i, held_i +
+ *             need_i) of its row, and a_i rows of the packed tokens.
+ * Requests are refused whole, with kv_lens[i] = max(c_i, 0), no row and no page:
+ *   status[i] = 2  c_i < 0, or its pages do not fit the table's width;
+ *   status[i] = 3  the rows of the requests up to it (status 2 left out) exceed `rows`;
+ *   status[i] = 1  it needs pages, and the requests up to it (status 2 and 3 left out)
+ *                  need more than there are.
+ * Everyone else has status 0 and kv_lens[i] = c_i + a_i.
+ *   cache_lens, new_lens  int32 [n], n <= 8192
+ *   block_table           int32 [n, table_width], new pages written in place
+ *   free_pages            int32 [n_pages]; the first *free_count entries are free pages;
+ *                         pages given back are written behind them (in place)
+ *   free_count, free_count_out   int32 [1] each, before and after; not the same word
+ *   cu_q                  int32 [n + 1]: first row of each request; cu_q[n] rows in use
+ *   positions, slots      int32 / int64 [rows]: row t of request i at position p = c_i +
+ *                         t - cu_q[i] has slot page * page_size + p % page_size; a page
+ *                         number outside [0, n_pages) gives slot -1.  Rows from cu_q[n]
+ *                         on: position 0, slot -1.
+ * Only the outputs named are written; equal inputs give equal outputs, so the call can be
+ * repeated before *free_count_out and kv_lens are taken over.  Outputs must not overlap
+ * each other or the inputs.
+ * Returns XS_OK or XS_ERR_NULL / _SHAPE / _PAGE / _ALIGNMENT / _OVERLAP / _UNSUPPORTED_DEVICE / _CUDA.
+ */
+int xs_paged_step(const int* cache_lens, const int* new_lens, int* block_table, int* free_pages,
+                  const int* free_count, int n, int table_width, int n_pages, int page_size, int rows, int* kv_lens,
+                  int* cu_q, int* positions, long long* slots, int* free_count_out, int* status, void* stream);
+
+/*
+ * xs_attn_paged_workspace_bytes -- device workspace of the two calls below for up to n
+ * sequences (any contents; 256-byte aligned).
+ */
+int xs_attn_paged_workspace_bytes(int n, int H, int Hkv, int D, size_t* bytes);
+
+/*
+ * xs_attn_paged_plan -- divides the attention of a step among the SMs, from the lengths
+ * on the device, into `workspace`.  Every layer of the step uses it.
+ *   cu_q, kv_lens  device int32 [n + 1], [n] (as xs_paged_step writes them): sequence i
+ *                  has new rows [cu_q[i], cu_q[i+1]) and kv_lens[i] keys, its new tokens'
+ *                  own keys among them.  They are copied: later changes need a new plan.
+ *   max_q          an upper estimate of the new tokens of a sequence, known on the host;
+ *                  it chooses the kernel, a wrong one costs time only.
+ *   causal, window as in xs_attn_paged_fwd.
+ */
+int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,
+                       int window, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * xs_attn_paged_fwd -- attention of the new tokens over the cache.  Row j of sequence i
+ * stands at position p = kv_len_i - q_len_i + j and sees the keys t of its sequence with
+ *     0 <= t < kv_len_i,   t <= p if causal,   t > p - window if window > 0:
+ *     O = sum_t exp(x_t - m) V_t / sum_t exp(x_t - m),   x_t = scale <Q, K_t>,
+ *     lse = m + ln sum_t exp(x_t - m);
+ * a row that sees no key (kv_len_i < q_len_i, say) gets O = 0 and lse = -infinity.
+ * Without `causal` a chunk's tokens see each other and the whole cache (the next chunk
+ * of a video).  Query head h reads KV head h / (H / Hkv).  K, V and the probabilities
+ * enter the products in `dtype`; sums, maxima and the accumulators are fp32.
+ *   q            device, [T, H, D], rows q_stride elements apart (multiple of 8).
+ *   outs, layout, P   the rows in one of the library's layouts (B = 1, S = T), as in
+ *                xs_attn_varlen_fwd.  Rows from cu_q[n] on are left as they are.
+ *   lse          device fp32 [T, H], or NULL.
+ *   block_table  device int32, rows table_stride entries apart; the pages of a
+ *                sequence's kv_len_i tokens (with a window: of those some row sees).  A page
+ *                number outside [0, n_pages) and columns from table_width on read as zeros.
+ *   n, H, Hkv, D, max_q, causal, window, workspace   as planned: a launch that does not
+ *                match its plan computes nothing and xs_attn_get_device_error returns
+ *                XS_ERR_DEVICE_BOUNDS.  H % Hkv == 0, H / Hkv <= 32.  window needs causal.
+ * The sums of a tile that is cut among SMs are joined in a fixed order: equal calls on
+ * equal plans give equal bits.  After XS_ERR_DEVICE_TIMEOUT plan again.
+ */
+int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, const int* block_table, int layout,
+                      void* const* outs, float* lse, int T, int H, int Hkv, int D, int P, long long q_stride, int n,
+                      int table_width, long long table_stride, int n_pages, int page_size,
+                      const long long* k_cache_strides, const long long* v_cache_strides, int dtype, int max_q,
+                      int causal, int window, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * xs_burst_gap -- Burst-Gap microbenchmark of the store path the fused epilogue
