@@ -432,96 +432,128 @@ def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling
            "xs_rope_init")
 
 
-_DTYPES = None
+# The checks below run on every call of a decoding loop, where they cost more than the
+# kernels: the accepted case takes a few attribute reads per tensor, and the reason of a
+# refusal is worked out only once there is one.
+_I32 = _I64 = _F32 = None
+_DTYPES = {}
+_current_device = _raw_stream = None
+
+
+def _bind_torch():
+    global _I32, _I64, _F32, _current_device, _raw_stream
+    import torch
+    _DTYPES.update({torch.bfloat16: XS_DTYPE_BF16, torch.float16: XS_DTYPE_FP16})
+    if torch.cuda.is_available():
+        torch.cuda.init()
+        _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    else:
+        _current_device, _raw_stream = (lambda: -2), (lambda dev: 0)   # no tensor is on device -2
+    _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
+def _device():
+    """The current device's index (-2 without CUDA)."""
+    if _I32 is None:
+        _bind_torch()
+    return _current_device()
+
+
+def _stream_of(stream, dev):
+    return _raw_stream(dev) if stream is None else _stream_handle(stream)
 
 
 def _dtype_of(t, name):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: XS_DTYPE_BF16, torch.float16: XS_DTYPE_FP16}
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}") from None
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}")
+    return d
 
 
-def _on_device(t, name):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _on_device(t, name, dev):
+    if t.get_device() != dev:
         raise TypeError(f"{name} must be a CUDA tensor on the current device")
 
 
-def _rows(t, name, dtype, D=None):
+def _rows(t, name, dtype, D, dev):
     """A [T, H, D] tensor whose heads are contiguous; returns (T, H, row stride)."""
-    if t.dim() != 3 or t.dtype != dtype or (D is not None and t.shape[2] != D):
-        raise TypeError(f"{name} must be a {dtype} tensor [T, H, D]" + (f" with D = {D}" if D else ""))
-    _on_device(t, name)
-    T, H, D = t.shape
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+    if t.dim() != 3 or t.dtype is not dtype or t.shape[2] != D:
+        raise TypeError(f"{name} must be a {dtype} tensor [T, H, D] with D = {D}")
+    _on_device(t, name, dev)
+    T, H, _ = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and H > 1):
         raise TypeError(f"{name}: the heads of a row must be contiguous")
-    return T, H, s[0] if T > 1 else H * D
+    return T, H, s0 if T > 1 else H * D
 
 
-def _ints(t, name, dtype_name, *shape):
-    """A contiguous integer tensor of the given shape (None: any extent)."""
-    if (str(t.dtype) != "torch." + dtype_name or t.dim() != len(shape) or not t.is_contiguous() or
-            any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        raise TypeError(f"{name} must be a contiguous {dtype_name} tensor of shape {list(shape)}")
-    _on_device(t, name)
-    return t.data_ptr()
+def _vec(t, name, dtype, n, dev):
+    """Address of a contiguous vector of n integers."""
+    if t.dtype is dtype and t.dim() == 1 and t.numel() == n and t.is_contiguous():
+        if t.get_device() == dev:
+            return t.data_ptr()
+        _on_device(t, name, dev)
+    raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape [{n}]")
 
 
 _Strides = _i64 * 3
 
 
-def _cache(t, name, dtype):
-    """A cache [n_pages, page_size, Hkv, D] of any strides with D contiguous."""
-    if t.dim() != 4 or t.dtype != dtype:
+def _cache(t, name, dtype, dev):
+    """Strides of a cache [n_pages, page_size, Hkv, D] with D contiguous."""
+    if t.dim() != 4 or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor [n_pages, page_size, Hkv, D]")
-    _on_device(t, name)
-    s = t.stride()
-    if s[3] != 1:
+    _on_device(t, name, dev)
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
         raise TypeError(f"{name}: the channels of a head must be contiguous")
-    return _Strides(s[0], s[1], s[2])
+    return _Strides(s0, s1, s2)
 
 
-def _same(what, *pairs):
-    for a, b in pairs:
-        if a != b:
-            raise TypeError(f"{what}: shapes do not match ({a} against {b})")
+def _same(what, a, b):
+    if a != b:
+        raise TypeError(f"{what}: shapes do not match ({a} against {b})")
 
 
 def xs_rope_fwd(x, positions, out, rope: Rope, grad: bool = False, stream=None) -> None:
     """Rotary positions of ``x`` [T, H, D] (bf16 or fp16; rows may be slices of a wider matrix)
     into ``out`` (``out`` may be ``x``); ``grad=True`` applies the transposed map, which takes
     the gradient of ``out`` to the gradient of ``x``.  ``positions``: int32 [T]."""
+    dev, D, dt = _device(), rope.D, x.dtype
     dtype = _dtype_of(x, "x")
-    T, H, xs_ = _rows(x, "x", x.dtype, rope.D)
-    To, Ho, os_ = _rows(out, "out", x.dtype, rope.D)
-    _same("xs_rope_fwd", ((T, H), (To, Ho)))
-    _check(lib.xs_rope_fwd(x.data_ptr(), _ints(positions, "positions", "int32", T), out.data_ptr(), T, H, xs_, os_,
-                           dtype, int(bool(grad)), rope.ptr, _stream_handle(stream)), "xs_rope_fwd")
+    T, H, x_stride = _rows(x, "x", dt, D, dev)
+    To, Ho, out_stride = _rows(out, "out", dt, D, dev)
+    if T != To or H != Ho:
+        _same("xs_rope_fwd", (T, H), (To, Ho))
+    code = lib.xs_rope_fwd(x.data_ptr(), _vec(positions, "positions", _I32, T, dev), out.data_ptr(), T, H, x_stride,
+                           out_stride, dtype, 1 if grad else 0, rope.ptr, _stream_of(stream, dev))
+    if code:
+        _check(code, "xs_rope_fwd")
 
 
 def xs_rope_append_paged(q, k, v, positions, slots, q_out, k_cache, v_cache, rope: Rope, stream=None) -> None:
     """Rotate the new tokens' ``q`` [T, H, D] into ``q_out`` and their ``k`` [T, Hkv, D] into the
     slots of ``k_cache`` [n_pages, page_size, Hkv, D], and copy ``v`` into those of ``v_cache``.
     ``positions`` int32 [T], ``slots`` int64 [T] (outside the cache: not stored)."""
-    dtype, D = _dtype_of(q, "q"), rope.D
-    T, H, qs = _rows(q, "q", q.dtype, D)
-    Tk, Hkv, ks = _rows(k, "k", q.dtype, D)
-    Tv, Hv, vs = _rows(v, "v", q.dtype, D)
-    To, Ho, os_ = _rows(q_out, "q_out", q.dtype, D)
-    kc, vc = _cache(k_cache, "k_cache", q.dtype), _cache(v_cache, "v_cache", q.dtype)
-    n_pages, page_size = k_cache.shape[:2]
-    _same("xs_rope_append_paged", ((T, Hkv), (Tk, Hv)), ((T, H), (Tv, Ho)), (T, To),
-          (tuple(k_cache.shape), (n_pages, page_size, Hkv, D)), (tuple(v_cache.shape), tuple(k_cache.shape)))
-    _check(lib.xs_rope_append_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ints(positions, "positions", "int32", T),
-                                    _ints(slots, "slots", "int64", T), q_out.data_ptr(), k_cache.data_ptr(),
+    dev, D, dt = _device(), rope.D, q.dtype
+    dtype = _dtype_of(q, "q")
+    T, H, qs = _rows(q, "q", dt, D, dev)
+    Tk, Hkv, ks = _rows(k, "k", dt, D, dev)
+    Tv, Hv, vs = _rows(v, "v", dt, D, dev)
+    To, Ho, os_ = _rows(q_out, "q_out", dt, D, dev)
+    kc, vc = _cache(k_cache, "k_cache", dt, dev), _cache(v_cache, "v_cache", dt, dev)
+    shape = k_cache.shape
+    n_pages, page_size, Hc, Dc = shape
+    if T != Tk or T != Tv or T != To or H != Ho or Hkv != Hv or Hc != Hkv or Dc != D or v_cache.shape != shape:
+        _same("xs_rope_append_paged", [(T, H), (T, Hkv), (T, Hkv), (To, Ho), (n_pages, page_size, Hkv, D)] * 2,
+              [(To, Ho), (Tk, Hkv), (Tv, Hv), (T, H), tuple(shape), (T, H), (T, Hkv), (T, Hkv), (To, Ho),
+               tuple(v_cache.shape)])
+    code = lib.xs_rope_append_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), _vec(positions, "positions", _I32, T, dev),
+                                    _vec(slots, "slots", _I64, T, dev), q_out.data_ptr(), k_cache.data_ptr(),
                                     v_cache.data_ptr(), T, H, Hkv, qs, ks, vs, os_, n_pages, page_size, kc, vc, dtype,
-                                    rope.ptr, _stream_handle(stream)), "xs_rope_append_paged")
+                                    rope.ptr, _stream_of(stream, dev))
+    if code:
+        _check(code, "xs_rope_append_paged")
 
 
 def xs_paged_step(cache_lens, new_lens, block_table, free_pages, free_count, page_size: int, kv_lens, cu_q, positions,
@@ -531,16 +563,21 @@ def xs_paged_step(cache_lens, new_lens, block_table, free_pages, free_count, pag
     ended requests (``new_lens < 0``) back to the list, and ``kv_lens``, ``cu_q``, ``positions``,
     ``slots``, ``free_count_out`` and ``status`` (include/xsattn.h has the rules).  All int32
     device tensors, ``slots`` int64; ``free_pages`` has one entry per page of the cache."""
-    n, width = block_table.shape if block_table.dim() == 2 else (0, 0)
+    dev, i32 = _device(), _I32
+    if block_table.dim() != 2 or block_table.dtype is not i32 or not block_table.is_contiguous():
+        raise TypeError(f"block_table must be a contiguous {i32} tensor [n, width]")
+    _on_device(block_table, "block_table", dev)
+    n, width = block_table.shape
     rows, n_pages = positions.numel(), free_pages.numel()
-    _check(lib.xs_paged_step(_ints(cache_lens, "cache_lens", "int32", n), _ints(new_lens, "new_lens", "int32", n),
-                             _ints(block_table, "block_table", "int32", n, width),
-                             _ints(free_pages, "free_pages", "int32", None),
-                             _ints(free_count, "free_count", "int32", 1), n, width, n_pages, page_size, rows,
-                             _ints(kv_lens, "kv_lens", "int32", n), _ints(cu_q, "cu_q", "int32", n + 1),
-                             _ints(positions, "positions", "int32", None), _ints(slots, "slots", "int64", rows),
-                             _ints(free_count_out, "free_count_out", "int32", 1), _ints(status, "status", "int32", n),
-                             _stream_handle(stream)), "xs_paged_step")
+    code = lib.xs_paged_step(_vec(cache_lens, "cache_lens", i32, n, dev), _vec(new_lens, "new_lens", i32, n, dev),
+                             block_table.data_ptr(), _vec(free_pages, "free_pages", i32, n_pages, dev),
+                             _vec(free_count, "free_count", i32, 1, dev), n, width, n_pages, page_size, rows,
+                             _vec(kv_lens, "kv_lens", i32, n, dev), _vec(cu_q, "cu_q", i32, n + 1, dev),
+                             _vec(positions, "positions", i32, rows, dev), _vec(slots, "slots", _I64, rows, dev),
+                             _vec(free_count_out, "free_count_out", i32, 1, dev), _vec(status, "status", i32, n, dev),
+                             _stream_of(stream, dev))
+    if code:
+        _check(code, "xs_paged_step")
 
 
 def xs_attn_paged_workspace_bytes(n: int, H: int, Hkv: int, D: int) -> int:
@@ -570,12 +607,17 @@ def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, cau
     """Divide the attention of a step among the SMs: ``cu_q`` int32 [n + 1], ``kv_lens`` int32 [n]
     on the device; ``max_q`` an upper estimate of a sequence's new tokens; ``causal`` and
     ``window`` (0: none) as the attention is to use them."""
-    w = workspace
-    _on_device(w._buf, "workspace")
-    _check(lib.xs_attn_paged_plan(_ints(cu_q, "cu_q", "int32", w.n + 1), _ints(kv_lens, "kv_lens", "int32", w.n), w.n,
-                                  w.H, w.Hkv, w.D, max_q, int(bool(causal)), window, w.ptr, w.nbytes,
-                                  _stream_handle(stream)), "xs_attn_paged_plan")
-    w.planned = (max_q, int(bool(causal)), window)
+    w, dev = workspace, _device()
+    _on_device(w._buf, "workspace", dev)
+    causal = 1 if causal else 0
+    code = lib.xs_attn_paged_plan(_vec(cu_q, "cu_q", _I32, w.n + 1, dev), _vec(kv_lens, "kv_lens", _I32, w.n, dev), w.n,
+                                  w.H, w.Hkv, w.D, max_q, causal, window, w.ptr, w.nbytes, _stream_of(stream, dev))
+    if code:
+        _check(code, "xs_attn_paged_plan")
+    w.planned = (max_q, causal, window)
+
+
+_OnePtr = _vp * 1
 
 
 def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale: float, workspace: PagedWorkspace,
@@ -584,37 +626,47 @@ def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale
     each, any strides with D contiguous) as ``workspace`` plans it.  ``block_table`` int32 [n, width];
     ``layout`` XS_LAYOUT_A2A (P shards [T/P, H, D]), XS_LAYOUT_CONTIGUOUS (one [T, H, D] tensor) or
     XS_LAYOUT_HEADS (P head shards [T, H/P, D]); ``lse``: fp32 [T, H] or None."""
-    w = workspace
+    w, dev, dt = workspace, _device(), q.dtype
     if w.planned is None:
         raise ValueError("xs_attn_paged_fwd: the workspace has no plan (call xs_attn_paged_plan first)")
     max_q, causal, window = w.planned
+    D, n = w.D, w.n
     dtype = _dtype_of(q, "q")
-    T, H, qs = _rows(q, "q", q.dtype, w.D)
-    _on_device(w._buf, "workspace")
-    kc, vc = _cache(k_cache, "k_cache", q.dtype), _cache(v_cache, "v_cache", q.dtype)
-    n_pages, page_size = k_cache.shape[:2]
-    _same("xs_attn_paged_fwd", (H, w.H), (tuple(k_cache.shape[2:]), (w.Hkv, w.D)),
-          (tuple(v_cache.shape), tuple(k_cache.shape)))
-    if block_table.dim() != 2 or str(block_table.dtype) != "torch.int32" or block_table.shape[0] != w.n or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise TypeError(f"block_table must be an int32 tensor [{w.n}, width] with contiguous rows")
-    _on_device(block_table, "block_table")
+    T, H, qs = _rows(q, "q", dt, D, dev)
+    _on_device(w._buf, "workspace", dev)
+    kc, vc = _cache(k_cache, "k_cache", dt, dev), _cache(v_cache, "v_cache", dt, dev)
+    shape = k_cache.shape
+    n_pages, page_size, Hkv, Dc = shape
+    if H != w.H or Hkv != w.Hkv or Dc != D or v_cache.shape != shape:
+        _same("xs_attn_paged_fwd", (H, Hkv, Dc, tuple(shape)), (w.H, w.Hkv, D, tuple(v_cache.shape)))
+    if block_table.dim() != 2 or block_table.dtype is not _I32 or block_table.shape[0] != n:
+        raise TypeError(f"block_table must be an int32 tensor [{n}, width]")
+    _on_device(block_table, "block_table", dev)
+    width = block_table.shape[1]
+    ts, ts1 = block_table.stride()
+    if ts1 != 1 and width > 1:
+        raise TypeError("block_table: the entries of a row must be contiguous")
     P = len(outs)
-    shape = {XS_LAYOUT_A2A: (T // max(P, 1), H, w.D), XS_LAYOUT_HEADS: (T, H // max(P, 1), w.D)}.get(layout, (T, H, w.D))
+    if layout == XS_LAYOUT_CONTIGUOUS or P == 0:
+        want = (T, H, D)
+    else:
+        want = (T // P, H, D) if layout == XS_LAYOUT_A2A else (T, H // P, D)
     for o in outs:
-        if tuple(o.shape) != shape or o.dtype != q.dtype or not o.is_contiguous():
-            raise TypeError(f"out must be a contiguous {q.dtype} tensor of shape {list(shape)}")
-        _on_device(o, "out")
+        if o.shape != want or o.dtype is not dt or not o.is_contiguous():
+            raise TypeError(f"out must be a contiguous {dt} tensor of shape {list(want)}")
+        _on_device(o, "out", dev)
+    z = None
     if lse is not None:
-        if str(lse.dtype) != "torch.float32" or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        if lse.dtype is not _F32 or lse.shape != (T, H) or not lse.is_contiguous():
             raise TypeError("lse must be a contiguous float32 tensor [T, H]")
-        _on_device(lse, "lse")
-    _check(lib.xs_attn_paged_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), layout,
-                                 _ptr_array([o.data_ptr() for o in outs]), None if lse is None else lse.data_ptr(), T,
-                                 H, w.Hkv, w.D, P, qs, w.n, block_table.shape[1],
-                                 block_table.stride(0) if w.n > 1 else block_table.shape[1], n_pages, page_size, kc, vc,
-                                 dtype, max_q, causal, window, scale, w.ptr, w.nbytes, _stream_handle(stream)),
-           "xs_attn_paged_fwd")
+        _on_device(lse, "lse", dev)
+        z = lse.data_ptr()
+    code = lib.xs_attn_paged_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), layout,
+                                 _OnePtr(outs[0].data_ptr()) if P == 1 else _ptr_array([o.data_ptr() for o in outs]), z,
+                                 T, H, Hkv, D, P, qs, n, width, ts if n > 1 else width, n_pages, page_size, kc, vc, dtype,
+                                 max_q, causal, window, scale, w.ptr, w.nbytes, _stream_of(stream, dev))
+    if code:
+        _check(code, "xs_attn_paged_fwd")
 
 
 def attn_a2a(q, k, v, P: int, scale: float | None = None, stream=None, workspace=None):
