@@ -13,9 +13,9 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["attn_fwd.cu", "attn_paged_rows.cu", "paged_plan.cu", "paged_step.cu", "rope.cu", "relayout.cu",
+SOURCES = ["attn_fwd.cu", "attn_paged.cu", "attn_paged_rows.cu", "paged_plan.cu", "paged_step.cu", "rope.cu", "relayout.cu",
            "burst_gap.cu", "api.cu", "api_paged.cu"]
-HEADERS = ["kernels.h", "host.h", "paged.h", "paged_walk.cuh", "device_wait.cuh", "ptx.cuh", os.path.join("..", "..", "include", "xsattn.h")]
+HEADERS = ["kernels.h", "host.h", "paged.h", "paged_walk.cuh", "attn_tile.cuh", "device_wait.cuh", "ptx.cuh", os.path.join("..", "..", "include", "xsattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -992,7 +992,7 @@ int xs_attn_get_device_error_info(void* stream, int* info, int n_info) {
     int v = 0, drain = 0;
     xs::DeviceErrorInfo r{};
     // each kernel family keeps its own words; the first family with an error is reported, all are cleared
-    for (auto read : {xs::read_and_clear_device_error, xs::read_and_clear_paged_rows_error}) {
+    for (auto read : {xs::read_and_clear_device_error, xs::read_and_clear_paged_error, xs::read_and_clear_paged_rows_error}) {
         int v1 = 0, d1 = 0;
         xs::DeviceErrorInfo r1{};
         if ((e = read(&v1, &r1, &d1)) != cudaSuccess) return cuda_fail(e);

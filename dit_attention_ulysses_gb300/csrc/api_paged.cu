@@ -133,8 +133,30 @@ int encode_cache(CUtensorMap* m, const void* base, const CacheStrides& c, int n_
     return XS_OK;
 }
 
+// q as a 4-D tensor (D, G, Hkv, T); box = 64 channels x the G heads of one KV head x `tokens`
+// tokens: the packed rows of a tile, token-major.
+int encode_q(CUtensorMap* m, const void* base, int T, int Hkv, int G, int D, long long stride, int tokens, int dtype) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    int rc = get_encoder(&enc);
+    if (rc != XS_OK) return rc;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
+                                static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(G) * D * 2,
+                                   static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type =
+        dtype == XS_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = enc(m, type, 4, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return XS_OK;
+}
+
 // ---- tiling of the paged attention, a function of the shape alone
-constexpr int ROWS_SMALL = 16, ROWS_WIDE = 32;
+// rows 16 and 32: attn_paged_rows.cu; 128: attn_paged.cu
+constexpr int ROWS_SMALL = 16, ROWS_WIDE = 32, ROWS_TILE = 128;
 
 struct Tiling {
     int rows;   // packed query rows of a tile
@@ -144,6 +166,15 @@ struct Tiling {
 Tiling make_tiling(int G, int max_q, int sms) {
     Tiling x;
     const int64_t need = static_cast<int64_t>(G) * max_q;
+    if (need > ROWS_WIDE) {
+        x.rows = ROWS_TILE;
+        x.t.tokens = ROWS_TILE / G;
+        x.t.block = 128;
+        x.t.grid = sms;
+        x.t.start_cost = 384;
+        x.t.snap = 2;
+        return x;
+    }
     x.rows = need <= ROWS_SMALL ? ROWS_SMALL : ROWS_WIDE;
     x.t.tokens = x.rows / G;
     x.t.block = 64;
@@ -157,7 +188,7 @@ int check_paged_shape(int n, int H, int Hkv, int D, int max_q, int causal, int w
     if (n < 1 || n > xs::MAX_PAGED_SEQS || H < 1 || Hkv < 1 || max_q < 1) return XS_ERR_SHAPE;
     if (D != 64 && D != 128) return XS_ERR_HEAD_DIM;
     if (H % Hkv != 0) return XS_ERR_DIVISIBILITY;
-    if (H / Hkv > ROWS_WIDE || H > 4096) return XS_ERR_SHAPE;
+    if (H / Hkv > ROWS_TILE || H > 4096) return XS_ERR_SHAPE;
     if (window < 0 || (window > 0 && !causal)) return XS_ERR_SHAPE;
     return XS_OK;
 }
@@ -168,7 +199,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // for every tiling of the shape, so one workspace serves steps of any max_q.
 size_t paged_work(char* base, int n, int D, int sms, xs::PagedWork* w) {
     const size_t grid = 2 * static_cast<size_t>(sms);
-    const size_t part_rows = 2 * grid * ROWS_WIDE;
+    const size_t part_rows = 2 * static_cast<size_t>(sms) * ROWS_TILE;   // two parts per CTA: 2 * grid * ROWS_WIDE is as many
+    static_assert(2 * 2 * ROWS_WIDE <= 2 * ROWS_TILE, "the parts of both kernels fit");
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -476,18 +508,26 @@ int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, c
     a.n_pages = n_pages;
     a.causal = causal ? 1 : 0;
     a.window = window;
-    a.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    // never 0: a masked score is -infinity and stays so
+    a.c = std::fmax(static_cast<float>(static_cast<double>(scale) * 1.4426950408889634), 1e-30f);
     a.tile = tiling.t;
     a.timeout_ns = timeout_ns();
     a.fd_G = xs::make_fastdiv(a.G);
     a.epi.fd_Sl = xs::make_fastdiv(a.epi.Sl);
     a.epi.fd_Hl = xs::make_fastdiv(a.epi.Hl);
-    const int box = page_size < 32 ? page_size : 32;
+    const int box_max = tiling.rows == ROWS_TILE ? 128 : 32, box = page_size < box_max ? page_size : box_max;
     CUtensorMap tk, tv;
     if ((rc = encode_cache(&tk, k_cache, ks, n_pages, page_size, Hkv, D, box, dtype)) != XS_OK) return rc;
     if ((rc = encode_cache(&tv, v_cache, vs, n_pages, page_size, Hkv, D, box, dtype)) != XS_OK) return rc;
-    const cudaError_t e =
-        xs::launch_attn_paged_rows(tk, tv, a, dtype, tiling.rows, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (tiling.rows == ROWS_TILE) {
+        CUtensorMap tq;
+        if ((rc = encode_q(&tq, q, T, Hkv, a.G, D, q_stride, tiling.t.tokens, dtype)) != XS_OK) return rc;
+        e = xs::launch_attn_paged(tq, tk, tv, a, dtype, st);
+    } else {
+        e = xs::launch_attn_paged_rows(tk, tv, a, dtype, tiling.rows, st);
+    }
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
 

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             const int key = key_of(g) + (lane & 1) * box;
             if (g >= groups || (lane & 1) >= halves || key >= seq.kv_len || key + box <= lo_tile) return -1;
             const int col = key >> a.page_shift;
-            return col < a.width ? table[col] : -1;
+            return static_cast<unsigned>(col) < static_cast<unsigned>(a.width) ? table[col] : -1;
         };
         int pages = load_pages(0), pages_next = load_pages(16);
         int page_base = 0;   // group of `pages`' first lane pair

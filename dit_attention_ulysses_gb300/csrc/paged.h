@@ -125,7 +125,7 @@ struct PagedAttnArgs {
     long long q_stride, table_stride;
     int T, H, Hkv, G, D, n, width, page_shift, n_pages;
     int causal, window;         // window: 0 for none
-    float c;                    // scale * log2(e)
+    float c;                    // scale * log2(e), positive
     EpiParams epi;
     PagedTiling tile;
     PagedWork work;
@@ -137,6 +137,11 @@ struct PagedAttnArgs {
 cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int dtype,
                                    int rows, cudaStream_t stream);
 
+// Tiles of up to 128 packed rows; tq covers [T, Hkv, G, D] in boxes of one tile's rows.
+cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const PagedAttnArgs& a, int dtype, cudaStream_t stream);
+
+cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed);
 cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed);
 
 }  // namespace xs

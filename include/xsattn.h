@@ -562,7 +562,7 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
  *                number outside [0, n_pages) and columns from table_width on read as zeros.
  *   n, H, Hkv, D, max_q, causal, window, workspace   as planned: a launch that does not
  *                match its plan computes nothing and xs_attn_get_device_error returns
- *                XS_ERR_DEVICE_BOUNDS.  H % Hkv == 0, H / Hkv <= 32.  window needs causal.
+ *                XS_ERR_DEVICE_BOUNDS.  H % Hkv == 0, H / Hkv <= 128.  window needs causal.
  * The sums of a tile that is cut among SMs are joined in a fixed order: equal calls on
  * equal plans give equal bits.  After XS_ERR_DEVICE_TIMEOUT plan again.
  */

@@ -44,6 +44,9 @@ DECODE = [
     ([1, 1], [3000, 2100], 28, 4, 128, 256),      # 7 heads to a KV head
     ([1, 5], [70, 900], 5, 1, 128, 1024),
     ([1], [700], 32, 1, 128, 32),                 # 32 heads to a KV head
+    ([1, 2], [500, 3000], 40, 1, 128, 16),        # 40, and 128: a tile of its own size
+    ([1, 1, 0, 3], [900, 128, 5, 40000], 128, 1, 64, 64),
+    ([33], [1300], 48, 2, 128, 128),
 ]
 
 
@@ -73,6 +76,10 @@ CHUNKS = [  # q_lens, kv_lens, H, Hkv, D, page, causal, window
     ([40, 200], [30, 150], 2, 1, 128, 16, True, 7),
     ([17] * 33, [17 + 13 * i for i in range(33)], 4, 1, 128, 16, True, 0),
     ([515], [2061], 8, 1, 128, 64, True, 0),
+    ([77, 400], [1500, 400], 7, 1, 128, 32, True, 0),     # 18 tokens of 7 heads: 126 of 128 rows
+    ([301], [700], 24, 1, 64, 16, True, 333),
+    ([2000], [2000], 2, 1, 64, 16, True, 0),
+    ([129] * 9, [129 * (i + 1) for i in range(9)], 12, 3, 128, 64, False, 0),
 ]
 
 
