@@ -173,6 +173,7 @@ Tiling make_tiling(int G, int max_q, int sms) {
         x.t.grid = sms;
         x.t.start_cost = 384;
         x.t.snap = 2;
+        x.t.waves = xs::MAX_PAGED_WAVES;
         return x;
     }
     x.rows = need <= ROWS_SMALL ? ROWS_SMALL : ROWS_WIDE;
@@ -181,6 +182,7 @@ Tiling make_tiling(int G, int max_q, int sms) {
     x.t.grid = 2 * sms;
     x.t.start_cost = 128;
     x.t.snap = 1;
+    x.t.waves = 0;   // one tile per sequence and KV head: no keys to share in L2
     return x;
 }
 
@@ -216,6 +218,8 @@ size_t paged_work(char* base, int n, int D, int sms, xs::PagedWork* w) {
     if (w) w->ranges = reinterpret_cast<xs::PagedRange*>(p);
     p = take(static_cast<size_t>(n) * sizeof(xs::PagedSeq));
     if (w) w->seqs = reinterpret_cast<xs::PagedSeq*>(p);
+    p = take(grid * xs::MAX_PAGED_WAVES * sizeof(xs::PagedSlot));
+    if (w) w->slots = reinterpret_cast<xs::PagedSlot*>(p);
     p = take(part_rows * sizeof(float2));
     if (w) w->part_ml = reinterpret_cast<float2*>(p);
     p = take(part_rows * D * sizeof(float));

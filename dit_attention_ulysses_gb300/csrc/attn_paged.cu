@@ -25,7 +25,8 @@
 //              (128 / page_size boxes per block and 64 channels)
 // TMEM: S buffers 0-2 (P over their first halves) and the O accumulator, as in attn_fwd.cu.
 //
-// Work: paged_plan.cu gives every CTA one contiguous range of equal cost.  A tile cut
+// Work: paged_plan.cu deals out whole tiles in waves and then gives every CTA a range of
+// the rest, so that all end together.  A tile cut
 // among CTAs goes to the workspace in parts; the last CTA to finish one joins the parts in
 // CTA order.  No CTA waits for another, so the launch is an ordinary one.
 #include <cuda.h>
@@ -131,14 +132,30 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
 
     PagedRange range = a.work.ranges[blockIdx.x];
     const PagedHeader& h = *a.work.header;
-    const int n_seqs = h.n_seqs;
+    const int n_seqs = h.n_seqs, per_slot = h.slot;
+    int waves = h.waves;
     if (h.n != a.n || h.H != a.H || h.Hkv != a.Hkv || h.D != D || h.tokens != tokens || h.block != BLOCK_N ||
         h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window) {
         if (lane == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, h.n, h.tokens, h.grid);
         range.end = range.start;
+        waves = 0;
     }
+    // whole tiles first: slot `wave` has `left` tiles to go; then the range
+    const PagedSlot* slots = a.work.slots + static_cast<size_t>(blockIdx.x) * MAX_PAGED_WAVES;
+    int wave = 0, left = 0;
     PagedPos pos = range.start;
     PagedSeq seq = range.first;
+    auto begin = [&]() {
+        if (wave < waves) {
+            pos = slots[wave].pos;
+            seq = slots[wave].seq;
+            left = per_slot;
+        } else {
+            pos = range.start;
+            seq = range.first;
+        }
+    };
+    begin();
     uint32_t item = 0;        // ring items issued over the CTA's lifetime
     int u = 0;
     int q_last = -1;          // piece of the last Q load issued
@@ -152,7 +169,8 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
         return r;
     };
     for (;; ++u) {
-        bool more = paged_before(pos, range.end);
+        const bool in_wave = wave < waves;
+        bool more = in_wave || paged_before(pos, range.end);
         if (more && !paged_valid(pos, seq, n_seqs, tokens, a.Hkv)) {
             if (lane == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, pos.seq, pos.head, pos.tile);
             more = false;
@@ -167,7 +185,7 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
             int b0, count, hi_tile;
             paged_tile_blocks(seq, pos.tile, a.tile, a.causal, a.window, b0, count);
             paged_tile_keys(seq, pos.tile, tokens, a.causal, a.window, lo_tile, hi_tile);
-            cut_end = paged_same_tile(pos, range.end);
+            cut_end = !in_wave && paged_same_tile(pos, range.end);
             const int k1 = cut_end && range.end.k < count ? range.end.k : count;
             const int tok0 = pos.tile * tokens;
             const int n_tok = seq.q_len - tok0 < tokens ? seq.q_len - tok0 : tokens;
@@ -236,9 +254,12 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
             ++item;
         }
         if (!ok) break;
-        if (cut_end) {
+        if (in_wave && --left == 0) {
+            ++wave;
+            begin();
+        } else if (cut_end) {
             pos = range.end;   // the rest of the tile is the next CTA's
-        } else if (paged_next(pos, seq, tokens, a.Hkv) && paged_before(pos, range.end) && pos.seq < n_seqs) {
+        } else if (paged_next(pos, seq, tokens, a.Hkv) && (in_wave || paged_before(pos, range.end)) && pos.seq < n_seqs) {
             seq = a.work.seqs[pos.seq];
         }
     }

@@ -65,7 +65,9 @@ struct PagedTiling {
     int grid;       // CTAs, one contiguous range of the work each
     int start_cost; // cost of a tile's start and end, in keys
     int snap;       // a cut leaves at least this many blocks on both sides
+    int waves;      // whole tiles are dealt out in up to this many waves before the rest is cut (0: all is cut)
 };
+constexpr int MAX_PAGED_WAVES = 64;
 
 // A sequence of the step (those with new tokens only).
 struct PagedSeq {
@@ -78,7 +80,13 @@ struct PagedPos {
     int seq, head, tile, k;
 };
 
-// The work of one CTA: from `start` (inclusive) to `end` (exclusive), plus what it
+// `slot` consecutive tiles that a CTA runs whole in one wave, from `pos` on.
+struct PagedSlot {
+    PagedPos pos;
+    PagedSeq seq;   // the sequence of `pos`
+};
+
+// The part of the work that is cut, for one CTA: from `start` (inclusive) to `end` (exclusive), plus what it
 // needs to begin and to publish unfinished tiles.  A tile cut over CTAs c0 .. c1 is
 // merged by the last of them to finish, in the order of the CTAs.
 struct PagedRange {
@@ -95,7 +103,9 @@ struct PagedHeader {
     int n_seqs;           // sequences with new tokens
     int ranges;           // CTAs with work
     int n, H, Hkv, D, tokens, block, grid, causal, window;
-    int unused[5];
+    int waves;            // slots of every CTA before its range
+    int slot;             // tiles per slot
+    int unused[3];
 };
 constexpr int PAGED_MAGIC_SITE = 3;   // error record: the plan does not match the call
 
@@ -104,6 +114,7 @@ struct PagedWork {
     unsigned* counters;   // [grid] pieces of a cut tile finished, indexed by its first CTA
     PagedRange* ranges;   // [grid]
     PagedSeq* seqs;       // [n]
+    PagedSlot* slots;     // [grid][MAX_PAGED_WAVES]
     float2* part_ml;      // [2 grid][rows] running max (log2 units) and sum of a partial result
     float* part_o;        // [2 grid][rows][D] unnormalised partial result
 };

@@ -2,14 +2,23 @@
 //
 // A tile (a group of new tokens of one sequence and one KV head) costs the keys it
 // walks plus a constant for its start and end.  The tiles, in the order (sequence, KV
-// head, tile), form one line of cost; CTA c of `ranges` takes [c, c + 1) / ranges of
-// it, so all CTAs end together however ragged the lengths are, and neighbouring CTAs
-// share a sequence and head in L2.  A range may start and end inside a tile; cuts fall
-// on key blocks and leave at least `snap` blocks on both sides, and a range is long
-// enough that no two cuts meet.
+// head, tile), form one line of cost.
 //
-// Costs are arithmetic series (paged_walk.cuh), so nothing per tile is stored: one CTA
-// scans the sequences, then one thread per CTA of the attention bisects for its cut.
+// Cut part: CTA c takes a contiguous range of the line such that all CTAs end together
+// however ragged the lengths are.  A range may start and end inside a tile; cuts fall on
+// key blocks and leave at least `snap` blocks on both sides, and a range is long enough
+// that no two cuts meet.
+//
+// Waves (tiles of 128 rows): before that, whole tiles are dealt out wave by wave, tile
+// w * grid + c (or the w * grid + c-th group of `slot` tiles) to CTA c, for as many waves
+// as leave every CTA below its share of the whole; the ranges make up the difference.
+// The CTAs then walk the keys of the same one or few KV heads at the same time, from the
+// same end, and share them in L2.  One range each over the whole line had every CTA at
+// another place of all heads' keys: 226 MB of them at 24 heads of 18432 keys, read at 9
+// TB/s (895 us; with waves: see attn_paged.cu).
+//
+// Costs are arithmetic series (paged_walk.cuh), so nothing per tile is stored but the
+// waves' slots: one CTA scans the sequences, then its threads bisect for slots and cuts.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -22,15 +31,54 @@ namespace {
 
 constexpr int PLAN_THREADS = 512;
 
-__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ PagedPlanArgs a) {
-    extern __shared__ long long prefix[];   // [n + 1] cost before each kept sequence (all KV heads)
-    PagedPos* cut = reinterpret_cast<PagedPos*>(prefix + a.n + 1);   // [grid + 1]
-    __shared__ long long warp_cost[PLAN_THREADS / 32];
-    __shared__ int warp_count[PLAN_THREADS / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Exclusive prefix sum over the block's threads, and the total.
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    long long before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+        const long long s = warp_sums[w];
+        if (w < warp) before += s;
+        sum += s;
+    }
+    __syncthreads();   // warp_sums may be written again
+    total = sum;
+    return before + x - v;
+}
 
-    long long cost_before = 0;
-    int kept_before = 0;
+// Last i in [0, n) with p[i] <= x.
+template <typename T>
+__device__ __forceinline__ int find(const T* p, int n, long long x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ PagedPlanArgs a) {
+    extern __shared__ long long prefix[];                 // [n + 1] cost before each kept sequence (all KV heads)
+    long long* tiles = prefix + a.n + 1;                  // [n + 1] tiles before it
+    PagedPos* cut = reinterpret_cast<PagedPos*>(tiles + a.n + 1);      // [grid + 1]
+    float* slot_cost = reinterpret_cast<float*>(cut + a.tile.grid + 1);   // [grid][waves]
+    __shared__ long long warp_sums[PLAN_THREADS / 32];
+    __shared__ int waves_min;
+    const int tid = threadIdx.x;
+
+    long long total = 0, all_tiles = 0;
+    int kept = 0;
     for (int i0 = 0; i0 < a.n; i0 += PLAN_THREADS) {
         const int i = i0 + tid;
         PagedSeq s{0, 0, 0, i};
@@ -40,71 +88,124 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             s.q_len = q1 > s.q_start ? q1 - s.q_start : 0;
             s.kv_len = kv > 0 ? kv : 0;
         }
-        const int keep = s.q_len > 0;
-        const long long cost =
-            keep ? a.Hkv * paged_cost(s, paged_tiles(s, a.tile.tokens), a.tile, a.causal, a.window) : 0;
-        long long x = cost;
-        int k = keep;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, d);
-            const int z = __shfl_up_sync(0xffffffffu, k, d);
-            if (lane >= d) {
-                x += y;
-                k += z;
-            }
-        }
-        if (lane == 31) {
-            warp_cost[warp] = x;
-            warp_count[warp] = k;
-        }
-        __syncthreads();
-        long long cb = 0, call = 0;
-        int kb = 0, kall = 0;
-#pragma unroll
-        for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-            if (w == warp) {
-                cb = call;
-                kb = kall;
-            }
-            call += warp_cost[w];
-            kall += warp_count[w];
-        }
-        if (keep) {
-            const int at = kept_before + kb + k - 1;
-            prefix[at] = cost_before + cb + x - cost;
+        const int mine = s.q_len > 0 ? paged_tiles(s, a.tile.tokens) : 0;
+        const long long cost = mine > 0 ? a.Hkv * paged_cost(s, mine, a.tile, a.causal, a.window) : 0;
+        long long cost_all, kept_all, tiles_all;
+        const long long cost_at = block_scan(cost, warp_sums, cost_all);
+        const long long tiles_at = block_scan(static_cast<long long>(mine) * a.Hkv, warp_sums, tiles_all);
+        const long long kept_at = block_scan(mine > 0 ? 1 : 0, warp_sums, kept_all);
+        if (mine > 0) {
+            const int at = kept + static_cast<int>(kept_at);
+            prefix[at] = total + cost_at;
+            tiles[at] = all_tiles + tiles_at;
             a.work.seqs[at] = s;
         }
-        cost_before += call;
-        kept_before += kall;
-        __syncthreads();
+        total += cost_all;
+        all_tiles += tiles_all;
+        kept += static_cast<int>(kept_all);
     }
-    const int kept = kept_before;
-    const long long total = cost_before;
-    if (tid == 0) prefix[kept] = total;
+    if (tid == 0) {
+        prefix[kept] = total;
+        tiles[kept] = all_tiles;
+        waves_min = a.tile.waves;
+    }
+    __syncthreads();   // the prefix sums, and the sequences written by other threads of this CTA
+
     // every range at least twice the snap plus a start, so that cuts in one tile differ
     const long long least = static_cast<long long>(2 * a.tile.snap + 1) * a.tile.block + a.tile.start_cost;
+    const int grid = a.tile.grid;
     long long ranges = total / least;
-    if (ranges > a.tile.grid) ranges = a.tile.grid;
+    if (ranges > grid) ranges = grid;
     if (ranges < 1) ranges = kept > 0 ? 1 : 0;
-    __syncthreads();   // prefix, and the seqs written by other threads of this CTA
-    for (int c = tid; c <= ranges && ranges > 0; c += PLAN_THREADS) {
-        PagedPos p{kept, 0, 0, 0};
-        if (c == 0) p.seq = 0;
-        if (c > 0 && c < ranges) {
-            const long long x = total / ranges * c + total % ranges * c / ranges;
-            int lo = 0, hi = kept;   // prefix[lo] <= x < prefix[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (prefix[mid] <= x)
-                    lo = mid;
-                else
-                    hi = mid;
+
+    // ---- waves
+    int waves = 0;
+    long long per_slot = 1;
+    const long long share = ranges > 0 ? total / ranges : 0;   // of every CTA
+    if (a.tile.waves > 0 && ranges == grid && all_tiles >= grid) {
+        // one tile per slot, more (up to 64) where there are more tiles than slots; what is left is cut
+        const long long slots = static_cast<long long>(grid) * a.tile.waves;
+        per_slot = min((all_tiles + slots - 1) / slots, 64ll);
+        const int most = static_cast<int>(min(all_tiles / (grid * per_slot), static_cast<long long>(a.tile.waves)));
+        for (int i = tid; i < grid * most; i += PLAN_THREADS) {
+            const int w = i / grid, c = i - w * grid;
+            const long long first = (static_cast<long long>(w) * grid + c) * per_slot;
+            PagedSlot slot;
+            double cost = 0.0;
+            long long left = per_slot, t = first;
+            while (left > 0) {   // one turn per KV head that the slot touches
+                const int q = find(tiles, kept, t);
+                const PagedSeq s = a.work.seqs[q];
+                const int of_head = paged_tiles(s, a.tile.tokens);
+                const long long x = t - tiles[q];
+                PagedPos p;
+                p.seq = q;
+                p.head = static_cast<int>(x / of_head);
+                p.tile = static_cast<int>(x - static_cast<long long>(p.head) * of_head);
+                p.k = 0;
+                const long long n = left < of_head - p.tile ? left : of_head - p.tile;
+                if (t == first) {
+                    slot.pos = p;
+                    slot.seq = s;
+                }
+                cost += static_cast<double>(paged_cost(s, p.tile + n, a.tile, a.causal, a.window) -
+                                            paged_cost(s, p.tile, a.tile, a.causal, a.window));
+                t += n;
+                left -= n;
             }
-            p = paged_locate(a.work.seqs[lo], lo, x - prefix[lo], (prefix[lo + 1] - prefix[lo]) / a.Hkv, a.tile, a.Hkv,
-                             a.causal, a.window);
+            a.work.slots[static_cast<size_t>(c) * MAX_PAGED_WAVES + w] = slot;
+            slot_cost[i] = static_cast<float>(cost);
         }
-        cut[c] = p;
+        __syncthreads();
+        if (tid < grid) {
+            double sum = 0.0;
+            int w = 0;
+            for (; w < most; ++w) {
+                sum += slot_cost[w * grid + tid];
+                if (sum > static_cast<double>(share - least)) break;
+            }
+            atomicMin(&waves_min, w);   // a minimum: the order does not matter
+        }
+        __syncthreads();
+        waves = waves_min;
+    }
+    // ---- cuts: CTA c gets its share less what its waves cost, along the rest of the line
+    long long x0 = 0;   // cost of the waves' tiles
+    if (waves > 0) {
+        const long long t = static_cast<long long>(waves) * grid * per_slot;
+        if (t >= all_tiles) {
+            x0 = total;
+        } else {
+            const int q = find(tiles, kept, t);
+            const PagedSeq s = a.work.seqs[q];
+            const int of_head = paged_tiles(s, a.tile.tokens);
+            const long long x = t - tiles[q], head = x / of_head;
+            x0 = prefix[q] + head * paged_cost(s, of_head, a.tile, a.causal, a.window) +
+                 paged_cost(s, x - head * of_head, a.tile, a.causal, a.window);
+        }
+    }
+    // grid <= PLAN_THREADS: one thread per CTA
+    double spent = 0.0;
+    if (tid < ranges)
+        for (int w = 0; w < waves; ++w) spent += slot_cost[w * grid + tid];
+    const long long mine = tid < ranges ? share - static_cast<long long>(spent) : 0;
+    long long shares;
+    const long long before = block_scan(mine > 0 ? mine : 0, warp_sums, shares);
+    if (tid <= ranges && ranges > 0) {
+        PagedPos p{kept, 0, 0, 0};
+        if (tid < ranges && shares > 0) {
+            // in proportion, so that rounding leaves nothing over
+            const long long rest = total - x0;
+            const long long x =
+                x0 + (tid == 0 ? 0 : waves == 0 ? total / ranges * tid + total % ranges * tid / ranges
+                                                : static_cast<long long>(static_cast<double>(before) / shares * rest));
+            if (x < total) {
+                const int q = find(prefix, kept, x);
+                p = paged_locate(a.work.seqs[q], q, x - prefix[q], (prefix[q + 1] - prefix[q]) / a.Hkv, a.tile, a.Hkv, a.causal,
+                                 a.window);
+            }
+        }
+        cut[tid] = p;
     }
     __syncthreads();
     // first cut at or past p
@@ -154,6 +255,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         h.grid = a.tile.grid;
         h.causal = a.causal;
         h.window = a.window;
+        h.waves = waves;
+        h.slot = static_cast<int>(per_slot);
         *a.work.header = h;
     }
 }
@@ -161,7 +264,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(a.n + 2) / 2 * 16 + static_cast<size_t>(a.tile.grid + 1) * sizeof(PagedPos);
+    static_assert(MAX_PAGED_WAVES * sizeof(float) * PLAN_THREADS <= 128 * 1024, "shared memory of the waves");
+    if (a.tile.grid >= PLAN_THREADS || a.tile.waves > MAX_PAGED_WAVES) return cudaErrorInvalidConfiguration;
+    const size_t smem = static_cast<size_t>(a.n + 1) * 16 + static_cast<size_t>(a.tile.grid + 1) * sizeof(PagedPos) +
+                        static_cast<size_t>(a.tile.grid) * a.tile.waves * sizeof(float);
     if (smem > 47 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
