@@ -19,7 +19,7 @@ namespace {
 using namespace xs::host;
 
 constexpr int64_t MAX_ELEMS = int64_t(1) << 40;
-constexpr int64_t MAX_STRIDE = int64_t(1) << 38;   // elements: TMA strides stay below 2^40 bytes
+constexpr int64_t MAX_STRIDE = int64_t(1) << 35;   // elements: 8 tokens' TMA stride stays below 2^40 bytes
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -74,6 +74,7 @@ int check_cache(const long long* strides, int n_pages, int page_size, int Hkv, i
         if (s % 8 != 0) return XS_ERR_ALIGNMENT;
         out->s[i] = s;
     }
+    if ((Hkv - 1) * out->s[2] + D > INT32_MAX) return XS_ERR_SHAPE;   // a head's start is a TMA coordinate
     return XS_OK;
 }
 
@@ -111,22 +112,22 @@ void fill_rope(xs::RopeArgs* a, const xs_rope* rope, int T, int H, const int* po
     std::memcpy(a->turns, rope->turns, sizeof a->turns);
 }
 
-// [n_pages, page, Hkv, D] as a 4-D tensor (D, token, head, page); box = 64 channels x
-// `box` tokens of one head of one page.
+// [n_pages, page, Hkv, D] as the 5-D tensor (element, token % 8, panel, token / 8, page); the heads
+// lie along the first dimension, whatever their stride.  Box: `box_rows` tokens of one head.
 int encode_cache(CUtensorMap* m, const void* base, const CacheStrides& c, int n_pages, int page_size, int Hkv, int D,
                  int box_rows, int dtype) {
     PFN_cuTensorMapEncodeTiled_v12000 enc;
     int rc = get_encoder(&enc);
     if (rc != XS_OK) return rc;
-    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page_size),
-                                static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(n_pages)};
-    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.s[1]) * 2, static_cast<cuuint64_t>(c.s[2]) * 2,
-                                   static_cast<cuuint64_t>(c.s[0]) * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>((Hkv - 1) * c.s[2] + D), 8, static_cast<cuuint64_t>(D / 64),
+                                static_cast<cuuint64_t>(page_size / 8), static_cast<cuuint64_t>(n_pages)};
+    const cuuint64_t token = static_cast<cuuint64_t>(c.s[1]) * 2;
+    const cuuint64_t strides[4] = {token, 128, 8 * token, static_cast<cuuint64_t>(c.s[0]) * 2};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(box_rows / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUtensorMapDataType type =
         dtype == XS_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUresult r = enc(m, type, 4, const_cast<void*>(base), dims, strides, box, estr,
+    const CUresult r = enc(m, type, 5, const_cast<void*>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
@@ -510,6 +511,8 @@ int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, c
     a.width = table_width;
     a.page_shift = log2_of(page_size);
     a.n_pages = n_pages;
+    a.k_head = static_cast<int>(ks.s[2]);
+    a.v_head = static_cast<int>(vs.s[2]);
     a.causal = causal ? 1 : 0;
     a.window = window;
     // never 0: a masked score is -infinity and stays so

@@ -21,8 +21,7 @@
 //              sequence's end, whose stale contents 0 * NaN would carry into O)
 //   warp 11    producer: walks the CTA's range of the plan, describes every piece of work
 //              in shared memory for the other roles, and loads: the lanes hold the page
-//              numbers of four blocks at a time and issue a page's copies side by side
-//              (128 / page_size boxes per block and 64 channels)
+//              numbers of four blocks at a time, and each issues one page's copy
 // TMEM: S buffers 0-2 (P over their first halves) and the O accumulator, as in attn_fwd.cu.
 //
 // Work: paged_plan.cu deals out whole tiles in waves and then gives every CTA a range of
@@ -76,6 +75,7 @@ template <int D>
 struct Cfg {
     static constexpr int TILE_BYTES = BLOCK_M * D * 2;
     static constexpr int PANELS = D / 64;
+    static constexpr int GROUP = PANELS * 1024;        // 8 keys of a K/V tile: [panel][key][64 channels]
     static constexpr int Q_BUFS = (D == 128) ? 1 : 2;
     static constexpr int KV_STAGES = (D == 128) ? 4 : 10;
     static constexpr int Q_OFF = 0;
@@ -245,12 +245,12 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
             const uint32_t full = bar(C::B_KV_FULL + stage);
             if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
             const int pages = (blk >> 2) < group ? g_prev : g_cur;
-            const int b = lane / C::PANELS, pnl = lane % C::PANELS;
-            const int page = __shfl_sync(0xffffffffu, pages, (blk & 3) * 8 + (b & 7));
+            const int page = __shfl_sync(0xffffffffu, pages, (blk & 3) * 8 + (lane & 7));
             __syncwarp();
-            if (b < boxes)
-                tma_load_4d(sbase + C::KV_OFF + stage * C::TILE_BYTES + pnl * PANEL_BYTES + b * box * 128, is_v ? tv : tk,
-                            full, pnl * 64, (d.key0 + blk * BLOCK_N) & (page_size - 1), d.head, page);
+            if (lane < boxes)
+                tma_load_5d(sbase + C::KV_OFF + stage * C::TILE_BYTES + lane * box * (D * 2), is_v ? tv : tk, full,
+                            d.head * (is_v ? a.v_head : a.k_head), 0, 0,
+                            ((d.key0 + blk * BLOCK_N) & (page_size - 1)) >> 3, page);
             ++item;
         }
         if (!ok) break;
@@ -275,6 +275,17 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
 }
 
 // --------------------------------------------------------------------- MMA
+// A K/V tile is [8-key group][panel][key][64 channels] (paged.h): the 8-key groups are C::GROUP apart
+// (SBO of both operands), the panels 1024 B.  As K (K-major), k-step kk covers 16 channels, 32 B within
+// the rows of panel kk / 4; as V (MN-major, panels by LBO), 16 keys, two groups.
+__device__ __forceinline__ constexpr uint32_t kv_k_step16(int kk) {
+    return static_cast<uint32_t>((kk >> 2) * (1024 >> 4) + (kk & 3) * 2);
+}
+template <int D>
+__device__ __forceinline__ constexpr uint32_t kv_v_step16(int kk) {
+    return static_cast<uint32_t>(kk * (2 * Cfg<D>::GROUP >> 4));
+}
+
 // Issuer of S(j) = Q K_j^T (SS) into S buffer (block index) % 3.  One thread.
 template <int D, bool F16>
 __device__ void mma_s_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0, uint32_t tmem_base,
@@ -284,7 +295,7 @@ __device__ void mma_s_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0,
     auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
     constexpr uint32_t IDESC_QK = idesc<F16>(BLOCK_M, BLOCK_N, 0);
     const uint64_t qdesc0 = smem_desc_sw128(sbase + C::Q_OFF, 16, 1024);   // Q buffer 0
-    const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, 1024);  // ring stage 0, as K
+    const uint64_t kdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 16, C::GROUP);  // ring stage 0, as K
     uint32_t g = 0;      // key blocks over the CTA's lifetime
     uint32_t sb = 0, sph = 0;   // S buffer of block g (g % 3) and its phase parity ((g / 3) & 1)
     uint32_t item0 = 0;  // first ring item of the current piece of work
@@ -312,7 +323,7 @@ __device__ void mma_s_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0,
             const uint64_t kdesc = desc_add(kdesc0, stage * (C::TILE_BYTES >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                mma_ss(tmem_base + S_COL + sb * 128u, desc_add(qdesc, k_step16(kk)), desc_add(kdesc, k_step16(kk)),
+                mma_ss(tmem_base + S_COL + sb * 128u, desc_add(qdesc, k_step16(kk)), desc_add(kdesc, kv_k_step16(kk)),
                        IDESC_QK, kk > 0);
             mma_commit(bar(C::B_S_FULL + sb));
             mma_commit(bar(C::B_KV_FREE + stage));
@@ -339,7 +350,7 @@ __device__ void mma_pv_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0
     const uint32_t sbase = smem_addr(smem);
     auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
     constexpr uint32_t IDESC_PV = idesc<F16>(BLOCK_M, D, 1);
-    const uint64_t vdesc0 = smem_desc_sw128(sbase + C::KV_OFF, PANEL_BYTES, 1024);  // ring stage 0, as V
+    const uint64_t vdesc0 = smem_desc_sw128(sbase + C::KV_OFF, 1024, C::GROUP);  // ring stage 0, as V
     uint32_t pb = 0, pph = 0;   // buffer of block g (g % 3) and its phase parity ((g / 3) & 1)
     uint32_t item0 = 0;
     int u = 0;
@@ -366,7 +377,7 @@ __device__ void mma_pv_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0
                 uint8_t* v = smem + C::KV_OFF + stage * C::TILE_BYTES;
                 for (int i = lane; i < (BLOCK_N - first) * (D / 8); i += 32) {
                     const int r = first + i / (D / 8), c8 = i % (D / 8);
-                    *reinterpret_cast<uint4*>(v + (c8 >> 3) * PANEL_BYTES + r * 128 + (c8 & 7) * 16) =
+                    *reinterpret_cast<uint4*>(v + (r >> 3) * C::GROUP + (c8 >> 3) * 1024 + (r & 7) * 128 + (c8 & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();   // before the MMA reads it, and the next copy writes it
@@ -386,7 +397,7 @@ __device__ void mma_pv_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0
                     const uint64_t vdesc = desc_add(vdesc0, stage * (C::TILE_BYTES >> 4));
 #pragma unroll
                     for (int kk = 0; kk < BLOCK_N / 16; ++kk)
-                        mma_ts(tmem_base + O_COL, tmem_base + S_COL + pb * 128u + kk * 8, desc_add(vdesc, v_step16(kk)),
+                        mma_ts(tmem_base + O_COL, tmem_base + S_COL + pb * 128u + kk * 8, desc_add(vdesc, kv_v_step16<D>(kk)),
                                IDESC_PV, (j > 0) || (kk > 0));
                     mma_commit(bar(C::B_P_FREE + pb));
                     mma_commit(bar(C::B_KV_FREE + stage));

@@ -47,7 +47,7 @@ template <int D, int MT>
 struct RowsCfg {
     static constexpr int SLOT = GROUP * D * 2;
     static constexpr int SLOTS = 3 * 128 / D;          // per warp
-    static constexpr int PANEL = GROUP * 128;          // 64 channels of a slot
+    static constexpr int OCTET = D / 64 * 1024;        // 8 keys of a slot: [64-channel panel][key][channel]
     static constexpr int ROWS = 16 * MT;
     static constexpr int RING = WARPS * SLOTS * SLOT;  // 96 KB; reused to join the warps' results
     static constexpr int O_STRIDE = D + 8;             // floats; keeps the joining stores off each other's banks
@@ -227,13 +227,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const uint32_t bar = bars + slot * 8;
                 mbar_arrive_expect_tx(bar, C::SLOT);
                 const int row = key_of(g) & (page_size - 1);
-#pragma unroll
-                for (int p = 0; p < D / 64; ++p) {
-                    const uint32_t dst = ring + slot * C::SLOT + p * C::PANEL;
-                    const CUtensorMap* m = (i & 1) ? &tv : &tk;
-                    tma_load_4d(dst, m, bar, p * 64, row, pos.head, p0);
-                    if (halves == 2) tma_load_4d(dst + 16 * 128, m, bar, p * 64, row, pos.head, p1);
-                }
+                const uint32_t dst = ring + slot * C::SLOT;
+                const CUtensorMap* m = (i & 1) ? &tv : &tk;
+                const int x = pos.head * ((i & 1) ? a.v_head : a.k_head);
+                tma_load_5d(dst, m, bar, x, 0, 0, row >> 3, p0);
+                if (halves == 2) tma_load_5d(dst + C::SLOT / 2, m, bar, x, 0, 0, row >> 3, p1);
             }
         };
         const int items = 2 * groups;
@@ -328,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                     for (int kb = 0; kb < GROUP / 16; ++kb) {
                         const int r = kb * 16 + krow;
-                        ldmatrix4(kbase + (cc >> 3) * C::PANEL + r * 128 + (((cc & 7) ^ (r & 7)) << 4), b[kb][0],
+                        ldmatrix4(kbase + (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 + (((cc & 7) ^ (r & 7)) << 4), b[kb][0],
                                   b[kb][1], b[kb][2], b[kb][3]);
                     }
 #pragma unroll
@@ -418,7 +416,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (int i = lane; i < (GROUP - bad) * (D / 8); i += 32) {
                     const int r = bad + i / (D / 8), cc = i % (D / 8);
                     *reinterpret_cast<uint4*>(smem + (ring - smem_addr(smem)) + slot * C::SLOT +
-                                              (cc >> 3) * C::PANEL + r * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                              (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 + (cc & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();   // before the next TMA copy into the slot
                 __syncwarp();
@@ -433,7 +432,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                     for (int nb = 0; nb < D / 16; ++nb) {
                         const int cc = nb * 2 + (lane >> 4);
                         uint32_t b0, b1, b2, b3;
-                        ldmatrix4_trans(vbase + (cc >> 3) * C::PANEL + r * 128 + (((cc & 7) ^ (r & 7)) << 4), b0, b1,
+                        ldmatrix4_trans(vbase + (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 +
+                                            (((cc & 7) ^ (r & 7)) << 4), b0, b1,
                                         b2, b3);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {

@@ -135,6 +135,7 @@ struct PagedAttnArgs {
     float* lse;                 // [T, H] or null
     long long q_stride, table_stride;
     int T, H, Hkv, G, D, n, width, page_shift, n_pages;
+    int k_head, v_head;         // elements between the heads of a cache
     int causal, window;         // window: 0 for none
     float c;                    // scale * log2(e), positive
     EpiParams epi;
@@ -144,6 +145,11 @@ struct PagedAttnArgs {
     FastDiv fd_G;
 };
 
+// tk, tv: a cache as the 5-D tensor (element, token % 8, 64-channel panel, token / 8, page), the
+// head in the first coordinate.  A box is one page's tokens of one head (at most a block's), and
+// lands as [token / 8][panel][token % 8][64 channels]: 1024-byte swizzle atoms, so that any
+// number of pages side by side form one operand tile, with one copy per page.
+//
 // rows: 16 or 32 (the tile's packed rows, tile.tokens * G, fit)
 cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int dtype,
                                    int rows, cudaStream_t stream);
