@@ -16,12 +16,13 @@
 //
 // Organisation (one persistent CTA per SM, 12 warps, as in attn_fwd.cu):
 //   warps 0-7  softmax + epilogue, two threads per row
+//   warp  8    producer of V: lanes hold the page numbers of four blocks at a time, and each
+//              issues one page's copy
 //   warp  9    issuer of the S = Q K^T MMAs (one lane) and TMEM owner
 //   warp 10    issuer of the O += P V MMAs (one lane; all lanes clear the V rows past a
 //              sequence's end, whose stale contents 0 * NaN would carry into O)
-//   warp 11    producer: walks the CTA's range of the plan, describes every piece of work
-//              in shared memory for the other roles, and loads: the lanes hold the page
-//              numbers of four blocks at a time, and each issues one page's copy
+//   warp 11    producer of Q and K: walks the CTA's part of the plan and describes every
+//              piece of work in shared memory for the other roles
 // TMEM: S buffers 0-2 (P over their first halves) and the O accumulator, as in attn_fwd.cu.
 //
 // Work: paged_plan.cu deals out whole tiles in waves and then gives every CTA a range of
@@ -45,16 +46,17 @@ namespace {
 
 constexpr int NUM_THREADS = 384;
 constexpr int NUM_SOFTMAX_WARPS = 8;
+constexpr int WARP_V = 8;
 constexpr int WARP_MMA_S = 9;
 constexpr int WARP_MMA_PV = 10;
-constexpr int WARP_TMA = 11;
+constexpr int WARP_K = 11;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL = 0;     // + 128 * buffer; P(g) over the first 64 columns of buffer g % 3
 constexpr int S_BUFS = 3;
 constexpr uint32_t O_COL = 384;
 constexpr float RESCALE_THRESHOLD = 8.0f;   // log2 units
 constexpr float NO_MAX = -1e30f;            // running maximum of a row that has seen nothing
-constexpr int PIECES = 4;                   // descriptors in flight (see producer_role)
+constexpr int PIECES = 4;                   // descriptors in flight (see producer_k_role)
 
 // One piece of work: key blocks of one tile, written by the producer.
 struct Piece {
@@ -67,7 +69,9 @@ struct Piece {
     int head;       // KV head
     int part;       // workspace slot of an unfinished tile; -1: the whole tile
     int c0, c1;     // CTAs of an unfinished tile
-    int unused[6];
+    int index;      // row of the block table
+    int lo_key;     // first key that some row sees
+    int unused[4];
 };
 static_assert(sizeof(Piece) == 64, "descriptor");
 
@@ -98,7 +102,8 @@ struct Cfg {
     static constexpr int NUM_BARS = 22 + 2 * KV_STAGES;
     static constexpr int PIECE_OFF = (BAR_OFF + NUM_BARS * 8 + 63) / 64 * 64;
     static constexpr int MISC_OFF = PIECE_OFF + PIECES * 64;
-    static constexpr int SMEM_BYTES = MISC_OFF + 16;
+    static constexpr int LOADED_OFF = MISC_OFF + 16;
+    static constexpr int SMEM_BYTES = LOADED_OFF + KV_STAGES * 4;
     static constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
 };
 static_assert(Cfg<128>::SMEM_ALLOC <= 232448 && Cfg<64>::SMEM_ALLOC <= 232448, "shared memory budget");
@@ -114,20 +119,69 @@ __device__ __forceinline__ const Piece& piece_of(const uint8_t* smem, int piece_
     return *reinterpret_cast<const Piece*>(smem + piece_off + (u % PIECES) * 64);
 }
 
-// ---------------------------------------------------------------- producer
-// The whole warp.  A descriptor slot is reused four pieces later: the producer is then
-// past the wait for the Q buffer of piece u - 1 or u - 2, whose scores are issued only
-// after the last PV of the piece before, so every role has left piece u - 4.
+// --------------------------------------------------------------- producers
+// Two warps share the K/V ring: one loads K blocks (and walks the plan, describes the
+// pieces and loads Q), one V blocks; each item goes to the ring position of the
+// consumption order K0, K1, V0, K2, V1, ...  A copy costs its warp some 30 ns to issue
+// (lanes with different pages issue one after the other), so with 16-token pages one warp
+// for both held every block back to 16 of them: 1060 us at 4608 x 18432, 24 heads.
+//
+// loaded[stage] (shared memory) is one more than the round of the stage's newest copy, for
+// an aborting CTA to let the copies in flight land.
+
+// Page numbers of a piece's blocks: lane 8 j + i holds page i of block 4 m + j of group m.
+// Past the keys, before the window and past the table: -1, a page out of range, which
+// reads as zeros.
+__device__ __forceinline__ int load_pages(const PagedAttnArgs& a, const int* table, int m, int key0, int nb, int kv_len,
+                                          int lo_key, int boxes, int box) {
+    const int lane = static_cast<int>(lane_id());
+    const int blk = 4 * m + (lane >> 3);
+    const int key = key0 + blk * BLOCK_N + (lane & 7) * box;
+    if ((lane & 7) >= boxes || blk >= nb || key >= kv_len || key + box <= lo_key) return -1;
+    const int col = key >> a.page_shift;
+    return static_cast<unsigned>(col) < static_cast<unsigned>(a.width) ? table[col] : -1;
+}
+
+// One ring item, by the whole warp: waits for its stage, then one copy per page.
 template <int D>
-__device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv,
-                              const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0, volatile int* abort_flag) {
+__device__ __forceinline__ bool load_item(const CUtensorMap* map, const PagedAttnArgs& a, uint32_t kv_base, uint32_t bar0,
+                                          uint32_t item, int pages, int blk, int key0, int x, int boxes, int box,
+                                          volatile int* abort_flag, int u, volatile uint32_t* loaded) {
+    using C = Cfg<D>;
+    const int lane = static_cast<int>(lane_id());
+    const uint32_t stage = item % C::KV_STAGES, round = item / C::KV_STAGES;
+    const uint32_t full = bar0 + (C::B_KV_FULL + stage) * 8u;
+    bool ok = true;
+    if (lane == 0) {
+        if (round > 0)
+            ok = thread_wait(bar0 + (C::B_KV_FREE + stage) * 8u, (round - 1) & 1, abort_flag, a.timeout_ns, u, blk);
+        if (ok) {
+            mbar_arrive_expect_tx(full, C::TILE_BYTES);
+            loaded[stage] = round + 1;
+        }
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    const int page = __shfl_sync(0xffffffffu, pages, (blk & 3) * 8 + (lane & 7));
+    __syncwarp();
+    if (!ok) return false;
+    if (lane < boxes)
+        tma_load_5d(kv_base + stage * C::TILE_BYTES + lane * box * (D * 2), map, full, x, 0, 0,
+                    ((key0 + blk * BLOCK_N) & ((1 << a.page_shift) - 1)) >> 3, page);
+    return true;
+}
+
+// A descriptor slot is reused four pieces later: the producer is then past the wait for
+// the Q buffer of piece u - 1 or u - 2, whose scores are issued only after the last PV of
+// the piece before, so every role has left piece u - 4.
+template <int D>
+__device__ void producer_k_role(const CUtensorMap* tq, const CUtensorMap* tk, const PagedAttnArgs& a, uint8_t* smem,
+                                uint32_t bar0, volatile int* abort_flag) {
     using C = Cfg<D>;
     const int lane = static_cast<int>(lane_id());
     const uint32_t sbase = smem_addr(smem);
     auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
-    const int page_size = 1 << a.page_shift;
-    const int box = page_size < BLOCK_N ? page_size : BLOCK_N;   // keys of one copy
-    const int boxes = BLOCK_N / box;                             // 1 .. 8
+    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);   // keys of one copy
+    const int boxes = BLOCK_N / box;                              // 1 .. 8
     const int tokens = a.tile.tokens;
 
     PagedRange range = a.work.ranges[blockIdx.x];
@@ -156,18 +210,11 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
         }
     };
     begin();
-    uint32_t item = 0;        // ring items issued over the CTA's lifetime
+    uint32_t item0 = 0;       // first ring item of the piece
     int u = 0;
     int q_last = -1;          // piece of the last Q load issued
+    volatile uint32_t* const loaded = reinterpret_cast<volatile uint32_t*>(smem + C::LOADED_OFF);
     bool ok = true;
-    // a bounded wait of lane 0, for the warp
-    auto wait = [&](int b, uint32_t parity, int blk) -> bool {
-        bool r = true;
-        if (lane == 0) r = thread_wait(bar(b), parity, abort_flag, a.timeout_ns, u, blk);
-        r = __shfl_sync(0xffffffffu, r, 0);
-        __syncwarp();
-        return r;
-    };
     for (;; ++u) {
         const bool in_wave = wave < waves;
         bool more = in_wave || paged_before(pos, range.end);
@@ -176,15 +223,19 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
             more = false;
         }
         const int qb = u % C::Q_BUFS;
-        if (u >= C::Q_BUFS) ok = wait(C::B_Q_FREE + qb, ((u / C::Q_BUFS) - 1) & 1, -1);
+        if (u >= C::Q_BUFS) {
+            if (lane == 0)
+                ok = thread_wait(bar(C::B_Q_FREE + qb), ((u / C::Q_BUFS) - 1) & 1, abort_flag, a.timeout_ns, u);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            __syncwarp();
+        }
         if (!ok) break;
         Piece d{};
-        int lo_tile = 0;
         bool cut_end = false;
         if (more) {
             int b0, count, hi_tile;
             paged_tile_blocks(seq, pos.tile, a.tile, a.causal, a.window, b0, count);
-            paged_tile_keys(seq, pos.tile, tokens, a.causal, a.window, lo_tile, hi_tile);
+            paged_tile_keys(seq, pos.tile, tokens, a.causal, a.window, d.lo_key, hi_tile);
             cut_end = !in_wave && paged_same_tile(pos, range.end);
             const int k1 = cut_end && range.end.k < count ? range.end.k : count;
             const int tok0 = pos.tile * tokens;
@@ -196,6 +247,7 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
             d.n_rows = n_tok * a.G;
             d.pos0 = seq.kv_len - seq.q_len + tok0;
             d.head = pos.head;
+            d.index = seq.index;
             const bool whole = pos.k == 0 && !cut_end;
             d.part = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos.k == 0 ? 1 : 0);
             d.c0 = pos.k == 0 ? static_cast<int>(blockIdx.x) : range.c0;
@@ -218,42 +270,18 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
                             pnl * 64, 0, d.head, d.row0);
         }
         q_last = u;
-        // Page numbers: lane 8 j + i holds box i of block 4 m + j; groups m - 1, m, m + 1 in registers
-        const int* table = a.table + static_cast<long long>(seq.index) * a.table_stride;
-        auto load_pages = [&](int m) -> int {
-            const int key = d.key0 + (4 * m + (lane >> 3)) * BLOCK_N + (lane & 7) * box;
-            // past the keys, before the window, past the table: a page out of range reads as zeros
-            if ((lane & 7) >= boxes || 4 * m + (lane >> 3) >= d.nb || key >= d.kv_len || key + box <= lo_tile) return -1;
-            const int col = key >> a.page_shift;
-            return static_cast<unsigned>(col) < static_cast<unsigned>(a.width) ? table[col] : -1;
-        };
-        int g_prev = -1, g_cur = load_pages(0), g_next = load_pages(1), group = 0;
-        for (int i = 0; i < 2 * d.nb && ok; ++i) {
-            int blk;
-            bool is_v;
-            ring_item(i, d.nb, blk, is_v);
-            if (!is_v && (blk >> 2) > group) {
-                ++group;
-                g_prev = g_cur;
-                g_cur = g_next;
-                g_next = load_pages(group + 1);
+        const int* table = a.table + static_cast<long long>(d.index) * a.table_stride;
+        int cur = -1, next = load_pages(a, table, 0, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
+        for (int j = 0; j < d.nb && ok; ++j) {
+            if ((j & 3) == 0) {
+                cur = next;
+                next = load_pages(a, table, (j >> 2) + 1, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
             }
-            const uint32_t stage = item % C::KV_STAGES;
-            const uint32_t round = item / C::KV_STAGES;
-            if (round > 0) ok = wait(C::B_KV_FREE + stage, (round - 1) & 1, blk);
-            if (!ok) break;
-            const uint32_t full = bar(C::B_KV_FULL + stage);
-            if (lane == 0) mbar_arrive_expect_tx(full, C::TILE_BYTES);
-            const int pages = (blk >> 2) < group ? g_prev : g_cur;
-            const int page = __shfl_sync(0xffffffffu, pages, (blk & 3) * 8 + (lane & 7));
-            __syncwarp();
-            if (lane < boxes)
-                tma_load_5d(sbase + C::KV_OFF + stage * C::TILE_BYTES + lane * box * (D * 2), is_v ? tv : tk, full,
-                            d.head * (is_v ? a.v_head : a.k_head), 0, 0,
-                            ((d.key0 + blk * BLOCK_N) & (page_size - 1)) >> 3, page);
-            ++item;
+            ok = load_item<D>(tk, a, sbase + C::KV_OFF, bar0, item0 + ring_pos_k(j), cur, j, d.key0, d.head * a.k_head,
+                              boxes, box, abort_flag, u, loaded);
         }
         if (!ok) break;
+        item0 += 2u * d.nb;
         if (in_wave && --left == 0) {
             ++wave;
             begin();
@@ -263,13 +291,38 @@ __device__ void producer_role(const CUtensorMap* tq, const CUtensorMap* tk, cons
             seq = a.work.seqs[pos.seq];
         }
     }
-    if (!ok && lane == 0) {
-        // copies already issued land before the CTA exits
-        for (uint32_t back = 1; back <= C::KV_STAGES && back <= item; ++back) {
-            const uint32_t it = item - back;
-            drain_wait(bar(C::B_KV_FULL + it % C::KV_STAGES), (it / C::KV_STAGES) & 1, 20000000ull);
+    // the newest Q copy lands before the CTA exits
+    if (!ok && lane == 0 && q_last >= 0)
+        drain_wait(bar(C::B_Q_FULL + q_last % C::Q_BUFS), (q_last / C::Q_BUFS) & 1, 20000000ull);
+    __syncwarp();
+}
+
+template <int D>
+__device__ void producer_v_role(const CUtensorMap* tv, const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0,
+                                volatile int* abort_flag) {
+    using C = Cfg<D>;
+    const uint32_t sbase = smem_addr(smem);
+    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
+    const int boxes = BLOCK_N / box;
+    uint32_t item0 = 0;
+    volatile uint32_t* const loaded = reinterpret_cast<volatile uint32_t*>(smem + C::LOADED_OFF);
+    bool ok = true;
+    for (int u = 0; ok; ++u) {
+        ok = warp_wait(bar0 + (C::B_PIECE + u % PIECES) * 8u, (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
+        if (!ok) break;
+        const Piece d = piece_of(smem, C::PIECE_OFF, u);
+        if (d.nb == 0) break;
+        const int* table = a.table + static_cast<long long>(d.index) * a.table_stride;
+        int cur = -1, next = load_pages(a, table, 0, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
+        for (int j = 0; j < d.nb && ok; ++j) {
+            if ((j & 3) == 0) {
+                cur = next;
+                next = load_pages(a, table, (j >> 2) + 1, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
+            }
+            ok = load_item<D>(tv, a, sbase + C::KV_OFF, bar0, item0 + ring_pos_v(j, d.nb), cur, j, d.key0,
+                              d.head * a.v_head, boxes, box, abort_flag, u, loaded);
         }
-        if (q_last >= 0) drain_wait(bar(C::B_Q_FULL + q_last % C::Q_BUFS), (q_last / C::Q_BUFS) & 1, 20000000ull);
+        item0 += 2u * d.nb;
     }
     __syncwarp();
 }
@@ -715,10 +768,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_init(bar0 + 8 * (C::B_KV_FULL + s), 1);
             mbar_init(bar0 + 8 * (C::B_KV_FREE + s), 1);
         }
+        for (int s = 0; s < C::KV_STAGES; ++s) reinterpret_cast<uint32_t*>(smem + C::LOADED_OFF)[s] = 0;
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == WARP_TMA && lane_id() == 0) {
+    if (warp == WARP_K && lane_id() == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
@@ -741,8 +795,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     if (warp < NUM_SOFTMAX_WARPS)
         softmax_role<D, F16>(args, smem, bar0, tmem_base, abort_flag);
-    else if (warp == WARP_TMA)
-        producer_role<D>(&tq, &tk, &tv, args, smem, bar0, abort_flag);
+    else if (warp == WARP_K)
+        producer_k_role<D>(&tq, &tk, args, smem, bar0, abort_flag);
+    else if (warp == WARP_V)
+        producer_v_role<D>(&tv, args, smem, bar0, abort_flag);
     else if (warp == WARP_MMA_PV)
         mma_pv_role<D, F16>(args, smem, bar0, tmem_base, abort_flag);
     else if (warp == WARP_MMA_S && lane_id() == 0)
@@ -753,6 +809,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == WARP_MMA_S) tmem_dealloc(tmem_base, TMEM_COLS);
+    if (*abort_flag && threadIdx.x == 0) {   // copies already issued land before the CTA exits
+        const uint32_t* loaded = reinterpret_cast<const uint32_t*>(smem + C::LOADED_OFF);
+        for (int s = 0; s < C::KV_STAGES; ++s)
+            if (loaded[s] > 0) drain_wait(bar0 + 8 * (C::B_KV_FULL + s), (loaded[s] - 1) & 1, 20000000ull);
+    }
 }
 
 template <int D, bool F16>
