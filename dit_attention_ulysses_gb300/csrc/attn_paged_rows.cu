@@ -40,6 +40,7 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int GROUP = 32;                  // keys of a ring slot
+constexpr int JOIN_BATCH = 16;             // parts of a cut tile read at once
 constexpr float NO_MAX = -1e30f;           // running maximum of a row that has seen nothing
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units; P stays below 2^8
 
@@ -526,19 +527,37 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const int r = i / (D / 4), c4 = i % (D / 4);
                     float m = NO_MAX, l = 0.0f;
                     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {   // in CTA order
-                        const size_t at = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * C::ROWS + r;
-                        const float2 ml = __ldcg(a.work.part_ml + at);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.work.part_o + at * D + c4 * 4));
-                        const float m_new = fmaxf(m, ml.x);
-                        const float f0 = ex2_approx(m - m_new), f1 = ex2_approx(ml.x - m_new);
+                    // in CTA order, a batch at a time in flight (past the last: the last once more, at weight 0)
+                    for (int cb = c0; cb <= c1; cb += JOIN_BATCH) {
+                        float2 ml[JOIN_BATCH];
+                        float4 v[JOIN_BATCH];
+#pragma unroll
+                        for (int j = 0; j < JOIN_BATCH; ++j) {
+                            const int c = min(cb + j, c1);
+                            const size_t at = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * C::ROWS + r;
+                            ml[j] = __ldcg(a.work.part_ml + at);
+                            v[j] = __ldcg(reinterpret_cast<const float4*>(a.work.part_o + at * D + c4 * 4));
+                            if (cb + j > c1) ml[j] = make_float2(NO_MAX, 0.0f);
+                        }
+                        float m_new = m;
+#pragma unroll
+                        for (int j = 0; j < JOIN_BATCH; ++j) m_new = fmaxf(m_new, ml[j].x);
+                        const float f0 = ex2_approx(m - m_new);
                         m = m_new;
-                        l = l * f0 + ml.y * f1;
-                        acc.x = acc.x * f0 + v.x * f1;
-                        acc.y = acc.y * f0 + v.y * f1;
-                        acc.z = acc.z * f0 + v.z * f1;
-                        acc.w = acc.w * f0 + v.w * f1;
+                        l *= f0;
+                        acc.x *= f0;
+                        acc.y *= f0;
+                        acc.z *= f0;
+                        acc.w *= f0;
+#pragma unroll
+                        for (int j = 0; j < JOIN_BATCH; ++j) {
+                            const float f = cb + j > c1 ? 0.0f : ex2_approx(ml[j].x - m);
+                            l += ml[j].y * f;
+                            acc.x += v[j].x * f;
+                            acc.y += v[j].y * f;
+                            acc.z += v[j].z * f;
+                            acc.w += v[j].w * f;
+                        }
                     }
                     int t, gh;
                     fdivmod(r, a.fd_G, t, gh);

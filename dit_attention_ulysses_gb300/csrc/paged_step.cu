@@ -11,8 +11,8 @@
 //
 // What bounds it: the launch and a chain of dependent steps (load the lengths,
 // scan, look up, store); the bytes are a few MB at most.  So it is one launch with
-// no exchange between CTAs: every CTA scans all requests itself (at most 8192, in
-// shared memory), then the CTAs share the outputs out between them, one thread per
+// no exchange between CTAs: every CTA scans all requests itself (at most 8192: up to
+// eight per thread in registers, all three sums in one scan), then the CTAs share the outputs out between them, one thread per
 // token, per page taken and per page given back, each finding its request by
 // bisection.  A page that this step hands out is never read from the table or the
 // list cell that another CTA writes: it is computed again from the prefix sums and
@@ -26,31 +26,49 @@
 namespace xs {
 namespace {
 
-constexpr int STEP_THREADS = 512;
-
 enum { GRANTED = 0, NO_PAGES = 1, TOO_LONG = 2, NO_ROWS = 3 };
 
-// Exclusive prefix sum over the block's threads (64 bits), and the total.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+// Three sums over the requests before a thread's own, and over all of them.
+struct Sums {
+    long long rows, need, give;
+};
+
+template <int THREADS>
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = v;
+    Sums x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+        const long long r = __shfl_up_sync(0xffffffffu, x.rows, d), n = __shfl_up_sync(0xffffffffu, x.need, d),
+                        g = __shfl_up_sync(0xffffffffu, x.give, d);
+        if (lane >= d) {
+            x.rows += r;
+            x.need += n;
+            x.give += g;
+        }
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    long long before = 0, sum = 0;
+    // lane w holds the sums of warp w
+    Sums s = lane < THREADS / 32 ? warp_sums[lane] : Sums{0, 0, 0}, before = s;
 #pragma unroll
-    for (int w = 0; w < STEP_THREADS / 32; ++w) {
-        const long long s = warp_sums[w];
-        if (w < warp) before += s;
-        sum += s;
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long r = __shfl_up_sync(0xffffffffu, before.rows, d), n = __shfl_up_sync(0xffffffffu, before.need, d),
+                        g = __shfl_up_sync(0xffffffffu, before.give, d);
+        if (lane >= d) {
+            before.rows += r;
+            before.need += n;
+            before.give += g;
+        }
     }
+    total.rows = __shfl_sync(0xffffffffu, before.rows, 31);
+    total.need = __shfl_sync(0xffffffffu, before.need, 31);
+    total.give = __shfl_sync(0xffffffffu, before.give, 31);
+    const long long wr = __shfl_sync(0xffffffffu, before.rows - s.rows, warp);
+    const long long wn = __shfl_sync(0xffffffffu, before.need - s.need, warp);
+    const long long wg = __shfl_sync(0xffffffffu, before.give - s.give, warp);
     __syncthreads();   // warp_sums may be written again
-    total = sum;
-    return before + x - v;
+    return Sums{wr + x.rows - v.rows, wn + x.need - v.need, wg + x.give - v.give};
 }
 
 // The request whose part [p[i], p[i+1]) of a prefix sum holds x (0 <= x < p[n]).
@@ -68,94 +86,109 @@ __device__ __forceinline__ int find(const int* p, int n, int x) {
 
 __device__ __forceinline__ int clamp_int(long long x) { return x > 0x7fffffffll ? 0x7fffffff : static_cast<int>(x); }
 
-__global__ void __launch_bounds__(STEP_THREADS) paged_step_kernel(const __grid_constant__ StepArgs a) {
+// Thread tid owns requests [tid K, tid K + K).
+template <int THREADS, int K>
+__global__ void __launch_bounds__(THREADS) paged_step_kernel(const __grid_constant__ StepArgs a) {
     extern __shared__ int smem[];
-    __shared__ long long warp_sums[STEP_THREADS / 32];
+    __shared__ Sums warp_sums[THREADS / 32];
     __shared__ int taken_max;
     const int n = a.n, tid = threadIdx.x;
     int* len = smem;           // [n] cached tokens (not negative)
-    int* add = len + n;        // [n] new tokens; -1: ended
-    int* tok = add + n;        // [n + 1] first row
+    int* tok = len + n;        // [n + 1] first row
     int* need = tok + n + 1;   // [n + 1] pages needed before
     int* give = need + n + 1;  // [n + 1] pages given back before
-    unsigned char* stat = reinterpret_cast<unsigned char*>(give + n + 1);   // [n]
     const int shift = a.page_shift;
     auto pages_of = [&](long long tokens) -> long long { return (tokens + (1ll << shift) - 1) >> shift; };
 
-    for (int i = tid; i < n; i += STEP_THREADS) {
-        const int c = a.cache_lens[i], x = a.new_lens[i];
-        const bool bad = c < 0 || pages_of(static_cast<long long>(c > 0 ? c : 0) + (x > 0 ? x : 0)) > a.width;
-        len[i] = c > 0 ? c : 0;
-        add[i] = x < 0 ? (bad ? 0 : -1) : x;
-        stat[i] = bad ? TOO_LONG : GRANTED;
-    }
     const int list = min(max(*a.free_count, 0), a.n_pages);   // entries of the free list
+    int c[K], stat[K], rows_of[K], need_of[K];
+    Sums sum{0, 0, 0};
+    bool ended[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const int i = tid * K + j;
+        const int cached = i < n ? a.cache_lens[i] : 0, x = i < n ? a.new_lens[i] : 0;
+        c[j] = max(cached, 0);
+        const long long after = pages_of(static_cast<long long>(c[j]) + max(x, 0)), held = pages_of(c[j]);
+        const bool bad = cached < 0 || after > a.width;
+        stat[j] = bad ? TOO_LONG : GRANTED;
+        ended[j] = x < 0 && !bad;
+        rows_of[j] = bad ? 0 : max(x, 0);
+        need_of[j] = bad ? 0 : static_cast<int>(after - held);
+        sum.rows += rows_of[j];
+        sum.need += need_of[j];
+        sum.give += ended[j] ? held : 0;
+    }
     if (tid == 0) taken_max = 0;
-    __syncthreads();
-
-    // thread tid scans requests [i0, i1)
-    const int per = (n + STEP_THREADS - 1) / STEP_THREADS;
-    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    long long total;
-    // pages given back
-    long long v = 0;
-    for (int i = i0; i < i1; ++i) v += add[i] < 0 ? pages_of(len[i]) : 0;
-    long long x = block_scan(v, warp_sums, total);
-    for (int i = i0; i < i1; ++i) {
-        give[i] = clamp_int(x);
-        x += add[i] < 0 ? pages_of(len[i]) : 0;
+    Sums total;
+    Sums before = block_scan<THREADS>(sum, warp_sums, total);
+    const int avail = static_cast<int>(min(static_cast<long long>(a.n_pages), list + total.give));
+    int taken = static_cast<int>(min(total.need, static_cast<long long>(a.n_pages)));
+    if (total.rows > a.rows || total.need > avail) {   // some are refused: their rows and pages go to nobody
+        Sums at = before;
+        sum = Sums{0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            at.rows += rows_of[j];
+            if (rows_of[j] > 0 && at.rows > a.rows) {
+                stat[j] = NO_ROWS;
+                rows_of[j] = need_of[j] = 0;
+            }
+            sum.need += need_of[j];
+        }
+        Sums all;
+        at = block_scan<THREADS>(sum, warp_sums, all);
+        before.need = at.need;
+        total.need = all.need;
+        int mine = 0;
+        sum = Sums{0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            at.need += need_of[j];
+            if (need_of[j] > 0) {
+                if (at.need > avail) {
+                    stat[j] = NO_PAGES;   // its pages stay counted: requests behind it that need some are refused too
+                    rows_of[j] = 0;
+                } else {
+                    mine = static_cast<int>(at.need);
+                }
+            }
+            sum.rows += rows_of[j];
+        }
+        if (mine > 0) atomicMax(&taken_max, mine);   // a maximum: the order does not matter
+        before.rows = block_scan<THREADS>(sum, warp_sums, all).rows;
+        total.rows = all.rows;
+        taken = taken_max;   // (the scan synchronises)
     }
-    if (tid == 0) give[n] = clamp_int(total);
-    const long long given_all = total;
-    const int avail = static_cast<int>(min(static_cast<long long>(a.n_pages), list + given_all));
-    // rows
-    auto tokens = [&](int i) -> long long { return stat[i] == GRANTED && add[i] > 0 ? add[i] : 0; };
-    v = 0;
-    for (int i = i0; i < i1; ++i) v += tokens(i);
-    x = block_scan(v, warp_sums, total);
-    const bool all_rows = total <= a.rows;
-    for (int i = i0; i < i1; ++i) {
-        tok[i] = clamp_int(x);
-        const long long t = tokens(i);
-        x += t;
-        if (t > 0 && x > a.rows) stat[i] = NO_ROWS;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        const int i = tid * K + j;
+        if (i < n) {
+            len[i] = c[j];
+            tok[i] = clamp_int(before.rows);
+            need[i] = clamp_int(before.need);
+            give[i] = clamp_int(before.give);
+            if (blockIdx.x == 0) {
+                a.kv_lens[i] = ended[j] ? 0 : c[j] + rows_of[j];
+                a.cu_q[i] = tok[i];
+                a.status[i] = stat[j];
+            }
+        }
+        before.rows += rows_of[j];
+        before.need += need_of[j];
+        before.give += ended[j] ? pages_of(c[j]) : 0;
     }
-    if (tid == 0) tok[n] = clamp_int(total);
-    // pages needed
-    auto needed = [&](int i) -> long long {
-        return stat[i] == GRANTED && add[i] > 0 ? pages_of(static_cast<long long>(len[i]) + add[i]) - pages_of(len[i])
-                                                : 0;
-    };
-    v = 0;
-    for (int i = i0; i < i1; ++i) v += needed(i);
-    x = block_scan(v, warp_sums, total);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) {
-        need[i] = clamp_int(x);
-        const long long p = needed(i);
-        x += p;
-        if (p > 0) {
-            if (x > avail)
-                stat[i] = NO_PAGES;
-            else
-                mine = static_cast<int>(x);
+    const int rows = static_cast<int>(total.rows);
+    if (tid == 0) {
+        tok[n] = rows;
+        need[n] = clamp_int(total.need);
+        give[n] = clamp_int(total.give);
+        if (blockIdx.x == 0) {
+            a.cu_q[n] = rows;
+            *a.free_count_out = avail - taken;
         }
     }
-    if (tid == 0) need[n] = clamp_int(total);
-    const bool all_pages = total <= avail;
-    if (mine > 0) atomicMax(&taken_max, mine);   // a maximum: the order does not matter
-    if (!all_rows || !all_pages) {               // refused requests give their rows up: scan once more
-        v = 0;
-        for (int i = i0; i < i1; ++i) v += tokens(i);
-        x = block_scan(v, warp_sums, total);
-        for (int i = i0; i < i1; ++i) {
-            tok[i] = clamp_int(x);
-            x += tokens(i);
-        }
-        if (tid == 0) tok[n] = clamp_int(total);
-    }
     __syncthreads();
-    const int taken = taken_max, rows = tok[n];
 
     // page k of the step
     auto page_at = [&](int k) -> int {
@@ -164,17 +197,7 @@ __global__ void __launch_bounds__(STEP_THREADS) paged_step_kernel(const __grid_c
         const int q = find(give, n, e - list);
         return a.table[static_cast<long long>(q) * a.width + (e - list - give[q])];
     };
-    const int gtid = blockIdx.x * STEP_THREADS + tid, gsize = gridDim.x * STEP_THREADS;
-    for (int i = gtid; i < n; i += gsize) {
-        const int t = static_cast<int>(tokens(i));
-        a.kv_lens[i] = add[i] < 0 ? 0 : len[i] + t;
-        a.cu_q[i] = tok[i];
-        a.status[i] = stat[i];
-    }
-    if (gtid == 0) {
-        a.cu_q[n] = rows;
-        *a.free_count_out = avail - taken;
-    }
+    const int gtid = blockIdx.x * THREADS + tid, gsize = gridDim.x * THREADS;
     // pages given back, behind the list's own
     for (int e = list + gtid; e < avail; e += gsize) {
         const int q = find(give, n, e - list);
@@ -206,19 +229,28 @@ __global__ void __launch_bounds__(STEP_THREADS) paged_step_kernel(const __grid_c
 
 }  // namespace
 
-// One CTA per 512 rows (at most one per SM): a single CTA for a decoding batch.
-cudaError_t launch_paged_step(const StepArgs& a, int num_sms, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(a.n) * 21 + 12 + 4;
-    if (smem > 48 * 1024 - 256) {   // 256: the static part
-        const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   MAX_PAGED_SEQS * 21 + 16);
+template <int THREADS, int K>
+static cudaError_t launch(const StepArgs& a, int num_sms, cudaStream_t stream) {
+    const size_t smem = (static_cast<size_t>(a.n) * 4 + 3) * sizeof(int);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel<THREADS, K>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    long long work = a.rows > a.n ? a.rows : a.n;
-    long long grid = (work + STEP_THREADS - 1) / STEP_THREADS;
+    const long long work = a.rows > a.n ? a.rows : a.n;
+    long long grid = (work + THREADS - 1) / THREADS;
     if (grid > num_sms) grid = num_sms;
-    paged_step_kernel<<<static_cast<unsigned>(grid), STEP_THREADS, smem, stream>>>(a);
+    paged_step_kernel<THREADS, K><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
     return cudaGetLastError();
+}
+
+// One CTA per 512 or 1024 rows, at most one per SM: a single one for a decoding batch.
+cudaError_t launch_paged_step(const StepArgs& a, int num_sms, cudaStream_t stream) {
+    if (a.n <= 512) return launch<512, 1>(a, num_sms, stream);
+    if (a.n <= 2048) return launch<1024, 2>(a, num_sms, stream);
+    if (a.n <= 4096) return launch<1024, 4>(a, num_sms, stream);
+    static_assert(MAX_PAGED_SEQS <= 8 * 1024, "eight requests per thread at most");
+    return launch<1024, 8>(a, num_sms, stream);
 }
 
 }  // namespace xs
