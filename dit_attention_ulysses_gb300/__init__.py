@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "XsError",
@@ -128,12 +129,11 @@ EXPORTS = {
                                         _vp, _size, _vp]),
     "xs_rope_init": (_int, [_vp, _int, _int, _int, _f64, _int, _f64, _f64, _f64, _f64, _f64]),
     "xs_rope_fwd": (_int, [_vp, _vp, _vp, _int, _int, _i64, _i64, _int, _int, _vp, _vp]),
-    "xs_rope_append_paged": (_int, [_vp] * 8 + [_int] * 3 + [_i64] * 4 + [_int, _int, _vp, _vp, _int, _vp, _vp]),
+    "xs_rope_append_paged": (_int, [ctypes.c_char_p, _vp]),
     "xs_paged_step": (_int, [_vp] * 5 + [_int] * 5 + [_vp] * 7),
     "xs_attn_paged_workspace_bytes": (_int, [_int, _int, _int, _int, ctypes.POINTER(_size)]),
     "xs_attn_paged_plan": (_int, [_vp, _vp] + [_int] * 7 + [_vp, _size, _vp]),
-    "xs_attn_paged_fwd": (_int, [_vp] * 4 + [_int, ctypes.POINTER(_vp), _vp] + [_int] * 5 +
-                          [_i64, _int, _int, _i64, _int, _int, _vp, _vp] + [_int] * 4 + [_f32, _vp, _size, _vp]),
+    "xs_attn_paged_fwd": (_int, [ctypes.c_char_p, _vp]),
     "xs_burst_gap": (_int, [_vp, _size, _int, _size, _int, ctypes.c_longlong, ctypes.c_longlong, _vp, _vp]),
     "xs_attn_get_device_error": (_int, [_vp]),
     "xs_attn_get_device_error_info": (_int, [_vp, ctypes.POINTER(_int), _int]),
@@ -496,7 +496,10 @@ def _vec(t, name, dtype, n, dev):
     raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape [{n}]")
 
 
-_Strides = _i64 * 3
+# The argument structs of include/xsattn.h, packed in one go (no field of theirs needs padding):
+# xs_paged_cache is "2Q6q6i".
+_APPEND_ARGS = struct.Struct("=7Q2Q6q6i4q2i")
+_ATTN_ARGS = {P: struct.Struct(f"=5Q{P}Q{8 * (XS_MAX_P - P)}x2Q6q6i2q9if") for P in range(1, XS_MAX_P + 1)}
 
 
 def _cache(t, name, dtype, dev):
@@ -507,7 +510,7 @@ def _cache(t, name, dtype, dev):
     s0, s1, s2, s3 = t.stride()
     if s3 != 1:
         raise TypeError(f"{name}: the channels of a head must be contiguous")
-    return _Strides(s0, s1, s2)
+    return s0, s1, s2
 
 
 def _same(what, a, b):
@@ -548,10 +551,10 @@ def xs_rope_append_paged(q, k, v, positions, slots, q_out, k_cache, v_cache, rop
         _same("xs_rope_append_paged", [(T, H), (T, Hkv), (T, Hkv), (To, Ho), (n_pages, page_size, Hkv, D)] * 2,
               [(To, Ho), (Tk, Hkv), (Tv, Hv), (T, H), tuple(shape), (T, H), (T, Hkv), (T, Hkv), (To, Ho),
                tuple(v_cache.shape)])
-    code = lib.xs_rope_append_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), _vec(positions, "positions", _I32, T, dev),
-                                    _vec(slots, "slots", _I64, T, dev), q_out.data_ptr(), k_cache.data_ptr(),
-                                    v_cache.data_ptr(), T, H, Hkv, qs, ks, vs, os_, n_pages, page_size, kc, vc, dtype,
-                                    rope.ptr, _stream_of(stream, dev))
+    args = _APPEND_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _vec(positions, "positions", _I32, T, dev),
+                             _vec(slots, "slots", _I64, T, dev), q_out.data_ptr(), rope.ptr, k_cache.data_ptr(),
+                             v_cache.data_ptr(), *kc, *vc, n_pages, page_size, Hkv, D, dtype, 0, qs, ks, vs, os_, T, H)
+    code = lib.xs_rope_append_paged(args, _stream_of(stream, dev))
     if code:
         _check(code, "xs_rope_append_paged")
 
@@ -617,9 +620,6 @@ def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, cau
     w.planned = (max_q, causal, window)
 
 
-_OnePtr = _vp * 1
-
-
 def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale: float, workspace: PagedWorkspace,
                       lse=None, stream=None) -> None:
     """Attention of the new tokens ``q`` [T, H, D] over a paged cache ([n_pages, page_size, Hkv, D]
@@ -655,16 +655,19 @@ def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale
         if o.shape != want or o.dtype is not dt or not o.is_contiguous():
             raise TypeError(f"out must be a contiguous {dt} tensor of shape {list(want)}")
         _on_device(o, "out", dev)
-    z = None
+    z = 0
     if lse is not None:
         if lse.dtype is not _F32 or lse.shape != (T, H) or not lse.is_contiguous():
             raise TypeError("lse must be a contiguous float32 tensor [T, H]")
         _on_device(lse, "lse", dev)
         z = lse.data_ptr()
-    code = lib.xs_attn_paged_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), layout,
-                                 _OnePtr(outs[0].data_ptr()) if P == 1 else _ptr_array([o.data_ptr() for o in outs]), z,
-                                 T, H, Hkv, D, P, qs, n, width, ts if n > 1 else width, n_pages, page_size, kc, vc, dtype,
-                                 max_q, causal, window, scale, w.ptr, w.nbytes, _stream_of(stream, dev))
+    pack = _ATTN_ARGS.get(P)
+    if pack is None:
+        raise XsError(XS_ERR_SHAPE if P < 1 else XS_ERR_TOO_MANY_RANKS, "xs_attn_paged_fwd")
+    args = pack.pack(q.data_ptr(), block_table.data_ptr(), z, w.ptr, w.nbytes, *[o.data_ptr() for o in outs],
+                     k_cache.data_ptr(), v_cache.data_ptr(), *kc, *vc, n_pages, page_size, Hkv, D, dtype, 0, qs, ts,
+                     layout, P, T, H, n, width, max_q, causal, window, scale)
+    code = lib.xs_attn_paged_fwd(args, _stream_of(stream, dev))
     if code:
         _check(code, "xs_attn_paged_fwd")
 

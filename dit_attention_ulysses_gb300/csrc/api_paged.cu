@@ -60,22 +60,33 @@ int check_page(int page_size, int n_pages) {
     return XS_OK;
 }
 
-// Strides (page, token, head) of a cache; those of an extent of one are not used.
+// Strides (page, token, head) of a cache's K or V; those of an extent of one are not used.
 struct CacheStrides {
     long long s[3];
 };
 
-int check_cache(const long long* strides, int n_pages, int page_size, int Hkv, int D, CacheStrides* out) {
-    if (!strides) return XS_ERR_NULL;
-    const int dims[3] = {n_pages, page_size, Hkv};
+int check_strides(const xs_paged_cache& c, const long long* strides, CacheStrides* out) {
+    const int dims[3] = {c.n_pages, c.page_size, c.Hkv};
     for (int i = 0; i < 3; ++i) {
-        long long s = dims[i] == 1 ? D : strides[i];
-        if (s < D || s > MAX_STRIDE) return XS_ERR_SHAPE;
+        const long long s = dims[i] == 1 ? c.D : strides[i];
+        if (s < c.D || s > MAX_STRIDE) return XS_ERR_SHAPE;
         if (s % 8 != 0) return XS_ERR_ALIGNMENT;
         out->s[i] = s;
     }
-    if ((Hkv - 1) * out->s[2] + D > INT32_MAX) return XS_ERR_SHAPE;   // a head's start is a TMA coordinate
+    if ((c.Hkv - 1) * out->s[2] + c.D > INT32_MAX) return XS_ERR_SHAPE;   // a head's start is a TMA coordinate
     return XS_OK;
+}
+
+int check_cache(const xs_paged_cache& c, CacheStrides* ks, CacheStrides* vs) {
+    if (!c.k || !c.v) return XS_ERR_NULL;
+    if (c.D != 64 && c.D != 128) return XS_ERR_HEAD_DIM;
+    if (c.dtype != XS_DTYPE_BF16 && c.dtype != XS_DTYPE_FP16) return XS_ERR_DTYPE;
+    int rc = check_page(c.page_size, c.n_pages);
+    if (rc != XS_OK) return rc;
+    if (c.Hkv < 1 || c.Hkv > 4096) return XS_ERR_SHAPE;
+    if ((rc = check_strides(c, c.k_strides, ks)) != XS_OK) return rc;
+    if ((rc = check_strides(c, c.v_strides, vs)) != XS_OK) return rc;
+    return aligned16(c.k) && aligned16(c.v) ? XS_OK : XS_ERR_ALIGNMENT;
 }
 
 Range cache_span(const void* p, const CacheStrides& c, int n_pages, int page_size, int Hkv, int D) {
@@ -114,8 +125,8 @@ void fill_rope(xs::RopeArgs* a, const xs_rope* rope, int T, int H, const int* po
 
 // [n_pages, page, Hkv, D] as the 5-D tensor (element, token % 8, panel, token / 8, page); the heads
 // lie along the first dimension, whatever their stride.  Box: `box_rows` tokens of one head.
-int encode_cache(CUtensorMap* m, const void* base, const CacheStrides& c, int n_pages, int page_size, int Hkv, int D,
-                 int box_rows, int dtype) {
+int encode_cache(CUtensorMap* m, const void* base, const CacheStrides& c, const xs_paged_cache& cache, int box_rows) {
+    const int n_pages = cache.n_pages, page_size = cache.page_size, Hkv = cache.Hkv, D = cache.D;
     PFN_cuTensorMapEncodeTiled_v12000 enc;
     int rc = get_encoder(&enc);
     if (rc != XS_OK) return rc;
@@ -126,7 +137,7 @@ int encode_cache(CUtensorMap* m, const void* base, const CacheStrides& c, int n_
     const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64), static_cast<cuuint32_t>(box_rows / 8), 1};
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUtensorMapDataType type =
-        dtype == XS_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        cache.dtype == XS_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     // A row of 64 channels is 128 B: fetching 256 B brings another head's or token's row along, which is gone
     // from L2 when its turn comes (64 x 8192 keys, 8 heads side by side: 4.2 TB/s against 5.4)
     const CUtensorMapL2promotion l2 = D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
@@ -295,40 +306,37 @@ int xs_rope_fwd(const void* x, const int* positions, void* out, int T, int H, lo
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
 
-int xs_rope_append_paged(const void* q, const void* k, const void* v, const int* positions, const long long* slots,
-                         void* q_out, void* k_cache, void* v_cache, int T, int H, int Hkv, long long q_stride,
-                         long long k_stride, long long v_stride, long long q_out_stride, int n_pages, int page_size,
-                         const long long* k_cache_strides, const long long* v_cache_strides, int dtype,
-                         const xs_rope* rope, void* stream) {
-    if (!q || !k || !v || !positions || !slots || !q_out || !k_cache || !v_cache) return XS_ERR_NULL;
-    int rc = check_rope(rope);
+int xs_rope_append_paged(const xs_rope_append_args* args, void* stream) {
+    if (!args) return XS_ERR_NULL;
+    const xs_rope_append_args& g = *args;
+    const xs_paged_cache& cache = g.cache;
+    if (!g.q || !g.k || !g.v || !g.positions || !g.slots || !g.q_out) return XS_ERR_NULL;
+    int rc = check_rope(g.rope);
     if (rc != XS_OK) return rc;
-    if (dtype != XS_DTYPE_BF16 && dtype != XS_DTYPE_FP16) return XS_ERR_DTYPE;
-    const int D = rope->D;
-    if ((rc = check_rows(T, H, D, q_stride)) != XS_OK) return rc;
-    if ((rc = check_rows(T, Hkv, D, k_stride)) != XS_OK) return rc;
-    if ((rc = check_rows(T, Hkv, D, v_stride)) != XS_OK) return rc;
-    if ((rc = check_rows(T, H, D, q_out_stride)) != XS_OK) return rc;
-    if ((rc = check_page(page_size, n_pages)) != XS_OK) return rc;
     CacheStrides ks, vs;
-    if ((rc = check_cache(k_cache_strides, n_pages, page_size, Hkv, D, &ks)) != XS_OK) return rc;
-    if ((rc = check_cache(v_cache_strides, n_pages, page_size, Hkv, D, &vs)) != XS_OK) return rc;
-    for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_cache),
-                          static_cast<const void*>(v_cache)})
-        if (!aligned16(p)) return XS_ERR_ALIGNMENT;
-    if (!aligned(positions, 4) || !aligned(slots, 8)) return XS_ERR_ALIGNMENT;
-    const Rows rq = rows_of(q, T, static_cast<int64_t>(H) * D, q_stride),
-               rk = rows_of(k, T, static_cast<int64_t>(Hkv) * D, k_stride),
-               rv = rows_of(v, T, static_cast<int64_t>(Hkv) * D, v_stride),
-               ro = rows_of(q_out, T, static_cast<int64_t>(H) * D, q_out_stride);
-    if (!(q == q_out && q_stride == q_out_stride) && rows_overlap(rq, ro)) return XS_ERR_OVERLAP;
+    if ((rc = check_cache(cache, &ks, &vs)) != XS_OK) return rc;
+    const int D = cache.D, T = g.T, H = g.H, Hkv = cache.Hkv;
+    if (g.rope->D != D) return XS_ERR_HEAD_DIM;
+    if ((rc = check_rows(T, H, D, g.q_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, Hkv, D, g.k_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, Hkv, D, g.v_stride)) != XS_OK) return rc;
+    if ((rc = check_rows(T, H, D, g.q_out_stride)) != XS_OK) return rc;
+    if (!aligned16(g.q) || !aligned16(g.k) || !aligned16(g.v) || !aligned16(g.q_out) || !aligned(g.positions, 4) ||
+        !aligned(g.slots, 8))
+        return XS_ERR_ALIGNMENT;
+    const Rows rq = rows_of(g.q, T, static_cast<int64_t>(H) * D, g.q_stride),
+               rk = rows_of(g.k, T, static_cast<int64_t>(Hkv) * D, g.k_stride),
+               rv = rows_of(g.v, T, static_cast<int64_t>(Hkv) * D, g.v_stride),
+               ro = rows_of(g.q_out, T, static_cast<int64_t>(H) * D, g.q_out_stride);
+    if (!(g.q == g.q_out && g.q_stride == g.q_out_stride) && rows_overlap(rq, ro)) return XS_ERR_OVERLAP;
     if (rows_overlap(rk, ro) || rows_overlap(rv, ro)) return XS_ERR_OVERLAP;
-    const Range kc = cache_span(k_cache, ks, n_pages, page_size, Hkv, D),
-                vc = cache_span(v_cache, vs, n_pages, page_size, Hkv, D);
-    // K and V may be interleaved in one buffer (equal strides, other heads or pages); which
-    // elements two strided caches share is the caller's to keep apart, equal pointers are refused
-    if (k_cache == v_cache) return XS_ERR_OVERLAP;
-    const Range pos = range_of(positions, static_cast<int64_t>(T) * 4), sl = range_of(slots, static_cast<int64_t>(T) * 8);
+    const Range kc = cache_span(cache.k, ks, cache.n_pages, cache.page_size, Hkv, D),
+                vc = cache_span(cache.v, vs, cache.n_pages, cache.page_size, Hkv, D);
+    // K and V may be interleaved in one buffer (other pages, tokens or heads); which elements two
+    // strided caches share is the caller's to keep apart, equal pointers are refused
+    if (cache.k == cache.v) return XS_ERR_OVERLAP;
+    const Range pos = range_of(g.positions, static_cast<int64_t>(T) * 4),
+                sl = range_of(g.slots, static_cast<int64_t>(T) * 8);
     for (const Range& c : {kc, vc}) {
         for (const Rows* r : {&rq, &rk, &rv, &ro})
             if (overlaps(c, span(*r))) return XS_ERR_OVERLAP;
@@ -338,26 +346,27 @@ int xs_rope_append_paged(const void* q, const void* k, const void* v, const int*
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != XS_OK) return rc;
     xs::RopeArgs a;
-    fill_rope(&a, rope, T, H, positions);
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.q_out = q_out;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.slots = slots;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.qo_stride = q_out_stride;
+    fill_rope(&a, g.rope, T, H, g.positions);
+    a.q = g.q;
+    a.k = g.k;
+    a.v = g.v;
+    a.q_out = g.q_out;
+    a.k_cache = cache.k;
+    a.v_cache = cache.v;
+    a.slots = g.slots;
+    a.q_stride = g.q_stride;
+    a.k_stride = g.k_stride;
+    a.v_stride = g.v_stride;
+    a.qo_stride = g.q_out_stride;
     for (int i = 0; i < 3; ++i) {
         a.ks[i] = ks.s[i];
         a.vs[i] = vs.s[i];
     }
-    a.n_slots = static_cast<long long>(n_pages) * page_size;
+    a.n_slots = static_cast<long long>(cache.n_pages) * cache.page_size;
     a.Hkv = Hkv;
-    a.page_shift = log2_of(page_size);
-    const cudaError_t e = xs::launch_rope(a, dtype, rope->layout, true, dev.sms, static_cast<cudaStream_t>(stream));
+    a.page_shift = log2_of(cache.page_size);
+    const cudaError_t e =
+        xs::launch_rope(a, cache.dtype, g.rope->layout, true, dev.sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
 
@@ -446,50 +455,46 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
 
-int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, const int* block_table, int layout,
-                      void* const* outs, float* lse, int T, int H, int Hkv, int D, int P, long long q_stride, int n,
-                      int table_width, long long table_stride, int n_pages, int page_size,
-                      const long long* k_cache_strides, const long long* v_cache_strides, int dtype, int max_q,
-                      int causal, int window, float scale, void* workspace, size_t workspace_bytes, void* stream) {
-    if (!q || !k_cache || !v_cache || !block_table || !outs || !workspace) return XS_ERR_NULL;
+int xs_attn_paged_fwd(const xs_attn_paged_args* args, void* stream) {
+    if (!args) return XS_ERR_NULL;
+    const xs_attn_paged_args& g = *args;
+    const xs_paged_cache& cache = g.cache;
+    const int T = g.T, H = g.H, Hkv = cache.Hkv, D = cache.D, P = g.P, n = g.n;
+    if (!g.q || !g.block_table || !g.workspace) return XS_ERR_NULL;
+    if (T < 1) return XS_ERR_SHAPE;
+    CacheStrides ks, vs;
+    int rc = check_cache(cache, &ks, &vs);
+    if (rc != XS_OK) return rc;
+    if ((rc = check_paged_shape(n, H, Hkv, D, g.max_q, g.causal, g.window)) != XS_OK) return rc;
     xs::PagedAttnArgs a;
     std::memset(&a, 0, sizeof a);
     int n_out = 0;
     int64_t out_bytes = 0;
     bool need_div = false;
-    if (T < 1) return XS_ERR_SHAPE;
-    int rc = check_paged_shape(n, H, Hkv, D, max_q, causal, window);
-    if (rc != XS_OK) return rc;
-    if ((rc = layout_epi(layout, outs, 1, T, H, D, P, &a.epi, &n_out, &out_bytes, &need_div)) != XS_OK) return rc;
-    if (layout != XS_LAYOUT_CONTIGUOUS) {
+    if ((rc = layout_epi(g.layout, g.outs, 1, T, H, D, P, &a.epi, &n_out, &out_bytes, &need_div)) != XS_OK) return rc;
+    if (need_div) {
         if (P < 1) return XS_ERR_SHAPE;
         if (P > XS_MAX_P) return XS_ERR_TOO_MANY_RANKS;
         if (T % P != 0 || H % P != 0) return XS_ERR_DIVISIBILITY;
     }
-    if (dtype != XS_DTYPE_BF16 && dtype != XS_DTYPE_FP16) return XS_ERR_DTYPE;
-    if ((rc = check_rows(T, H, D, q_stride)) != XS_OK) return rc;
-    if ((rc = check_page(page_size, n_pages)) != XS_OK) return rc;
-    if (table_width < 1 || table_stride < (n > 1 ? table_width : 0)) return XS_ERR_SHAPE;
-    CacheStrides ks, vs;
-    if ((rc = check_cache(k_cache_strides, n_pages, page_size, Hkv, D, &ks)) != XS_OK) return rc;
-    if ((rc = check_cache(v_cache_strides, n_pages, page_size, Hkv, D, &vs)) != XS_OK) return rc;
-    if ((rc = check_scale(scale)) != XS_OK) return rc;
     for (int i = 0; i < n_out; ++i)
-        if (!outs[i]) return XS_ERR_NULL;
-    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned(block_table, 4) || !aligned(lse, 4) ||
-        !aligned(workspace, 256))
+        if (!g.outs[i]) return XS_ERR_NULL;
+    if ((rc = check_rows(T, H, D, g.q_stride)) != XS_OK) return rc;
+    if (g.table_width < 1 || (n > 1 && g.table_stride < g.table_width) || g.table_stride > MAX_STRIDE) return XS_ERR_SHAPE;
+    if ((rc = check_scale(g.scale)) != XS_OK) return rc;
+    if (!aligned16(g.q) || !aligned(g.block_table, 4) || !aligned(g.lse, 4) || !aligned(g.workspace, 256))
         return XS_ERR_ALIGNMENT;
     for (int i = 0; i < n_out; ++i)
-        if (!aligned16(outs[i])) return XS_ERR_ALIGNMENT;
-    const Range ins[4] = {span(rows_of(q, T, static_cast<int64_t>(H) * D, q_stride)),
-                          cache_span(k_cache, ks, n_pages, page_size, Hkv, D),
-                          cache_span(v_cache, vs, n_pages, page_size, Hkv, D),
-                          range_of(block_table, ((n - 1) * static_cast<int64_t>(table_stride) + table_width) * 4)};
+        if (!aligned16(g.outs[i])) return XS_ERR_ALIGNMENT;
+    const Range ins[4] = {span(rows_of(g.q, T, static_cast<int64_t>(H) * D, g.q_stride)),
+                          cache_span(cache.k, ks, cache.n_pages, cache.page_size, Hkv, D),
+                          cache_span(cache.v, vs, cache.n_pages, cache.page_size, Hkv, D),
+                          range_of(g.block_table, ((n > 1 ? (n - 1) * static_cast<int64_t>(g.table_stride) : 0) + g.table_width) * 4)};
     Range o[XS_MAX_P + 2];
     int n_all = 0;
-    for (int i = 0; i < n_out; ++i) o[n_all++] = range_of(outs[i], out_bytes);
-    if (lse) o[n_all++] = range_of(lse, static_cast<int64_t>(T) * H * 4);
-    o[n_all++] = range_of(workspace, static_cast<int64_t>(workspace_bytes));
+    for (int i = 0; i < n_out; ++i) o[n_all++] = range_of(g.outs[i], out_bytes);
+    if (g.lse) o[n_all++] = range_of(g.lse, static_cast<int64_t>(T) * H * 4);
+    o[n_all++] = range_of(g.workspace, static_cast<int64_t>(g.workspace_bytes));
     for (int i = 0; i < n_all; ++i) {
         for (int j = i + 1; j < n_all; ++j)
             if (overlaps(o[i], o[j])) return XS_ERR_OVERLAP;
@@ -498,45 +503,46 @@ int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, c
     }
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != XS_OK) return rc;
-    if (workspace_bytes < paged_work(static_cast<char*>(workspace), n, D, dev.sms, &a.work)) return XS_ERR_WORKSPACE;
-    const Tiling tiling = make_tiling(H / Hkv, max_q, dev.sms);
-    a.q = q;
-    a.table = block_table;
-    a.lse = lse;
-    a.q_stride = q_stride;
-    a.table_stride = table_stride;
+    if (g.workspace_bytes < paged_work(static_cast<char*>(g.workspace), n, D, dev.sms, &a.work)) return XS_ERR_WORKSPACE;
+    const Tiling tiling = make_tiling(H / Hkv, g.max_q, dev.sms);
+    a.q = g.q;
+    a.table = g.block_table;
+    a.lse = g.lse;
+    a.q_stride = g.q_stride;
+    a.table_stride = n > 1 ? g.table_stride : 0;
     a.T = T;
     a.H = H;
     a.Hkv = Hkv;
     a.G = H / Hkv;
     a.D = D;
     a.n = n;
-    a.width = table_width;
-    a.page_shift = log2_of(page_size);
-    a.n_pages = n_pages;
+    a.width = g.table_width;
+    a.page_shift = log2_of(cache.page_size);
+    a.n_pages = cache.n_pages;
     a.k_head = static_cast<int>(ks.s[2]);
     a.v_head = static_cast<int>(vs.s[2]);
-    a.causal = causal ? 1 : 0;
-    a.window = window;
+    a.causal = g.causal ? 1 : 0;
+    a.window = g.window;
     // never 0: a masked score is -infinity and stays so
-    a.c = std::fmax(static_cast<float>(static_cast<double>(scale) * 1.4426950408889634), 1e-30f);
+    a.c = std::fmax(static_cast<float>(static_cast<double>(g.scale) * 1.4426950408889634), 1e-30f);
     a.tile = tiling.t;
     a.timeout_ns = timeout_ns();
     a.fd_G = xs::make_fastdiv(a.G);
     a.epi.fd_Sl = xs::make_fastdiv(a.epi.Sl);
     a.epi.fd_Hl = xs::make_fastdiv(a.epi.Hl);
-    const int box_max = tiling.rows == ROWS_TILE ? 128 : 32, box = page_size < box_max ? page_size : box_max;
+    const int box_max = tiling.rows == ROWS_TILE ? 128 : 32;
+    const int box = cache.page_size < box_max ? cache.page_size : box_max;
     CUtensorMap tk, tv;
-    if ((rc = encode_cache(&tk, k_cache, ks, n_pages, page_size, Hkv, D, box, dtype)) != XS_OK) return rc;
-    if ((rc = encode_cache(&tv, v_cache, vs, n_pages, page_size, Hkv, D, box, dtype)) != XS_OK) return rc;
+    if ((rc = encode_cache(&tk, cache.k, ks, cache, box)) != XS_OK) return rc;
+    if ((rc = encode_cache(&tv, cache.v, vs, cache, box)) != XS_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (tiling.rows == ROWS_TILE) {
         CUtensorMap tq;
-        if ((rc = encode_q(&tq, q, T, Hkv, a.G, D, q_stride, tiling.t.tokens, dtype)) != XS_OK) return rc;
-        e = xs::launch_attn_paged(tq, tk, tv, a, dtype, st);
+        if ((rc = encode_q(&tq, g.q, T, Hkv, a.G, D, g.q_stride, tiling.t.tokens, cache.dtype)) != XS_OK) return rc;
+        e = xs::launch_attn_paged(tq, tk, tv, a, cache.dtype, st);
     } else {
-        e = xs::launch_attn_paged_rows(tk, tv, a, dtype, tiling.rows, st);
+        e = xs::launch_attn_paged_rows(tk, tv, a, cache.dtype, tiling.rows, st);
     }
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }

@@ -474,22 +474,39 @@ int xs_rope_init(xs_rope* rope, int D, int rot, int layout, double base, int sca
 int xs_rope_fwd(const void* x, const int* positions, void* out, int T, int H, long long x_stride,
                 long long out_stride, int dtype, int grad, const xs_rope* rope, void* stream);
 
+/* A paged cache (plain data, host).  Strides in elements: between pages, between the
+ * tokens of a page, and between heads (one head, one page: not used). */
+typedef struct xs_paged_cache {
+    void* k;
+    void* v;                  /* device, D contiguous                                  */
+    long long k_strides[3];
+    long long v_strides[3];
+    int n_pages, page_size, Hkv, D;
+    int dtype;                /* XS_DTYPE_* of the cache, and of all tensors used with it */
+    int reserved;             /* 0 */
+} xs_paged_cache;
+
 /*
  * xs_rope_append_paged -- rotates the new tokens' q into q_out and their k into the K
  * cache, and copies v into the V cache, in one launch.  Row t goes to slot slots[t] =
  * page * page_size + offset; a slot outside [0, n_pages * page_size) (padding) stores
  * no K and V.  Rows with equal slots race.  Values as xs_rope_fwd's, bit for bit.
- *   q, q_out   [T, H, D]; k, v [T, Hkv, D], row strides as in xs_rope_fwd; q_out may be
- *              q itself (in place), and must not overlap k, v or a cache otherwise.
- *   positions  device int32 [T];  slots device int64 [T].
- *   k_cache_strides, v_cache_strides  host, 3 each: elements between pages, tokens of a
- *              page and heads.
  */
-int xs_rope_append_paged(const void* q, const void* k, const void* v, const int* positions, const long long* slots,
-                         void* q_out, void* k_cache, void* v_cache, int T, int H, int Hkv, long long q_stride,
-                         long long k_stride, long long v_stride, long long q_out_stride, int n_pages, int page_size,
-                         const long long* k_cache_strides, const long long* v_cache_strides, int dtype,
-                         const xs_rope* rope, void* stream);
+typedef struct xs_rope_append_args {
+    const void* q;            /* device, [T, H, D]                                     */
+    const void* k;            /* device, [T, Hkv, D]                                   */
+    const void* v;            /* device, [T, Hkv, D]                                   */
+    const int* positions;     /* device, [T]                                           */
+    const long long* slots;   /* device, [T]                                           */
+    void* q_out;              /* device, [T, H, D]; may be q itself with equal strides,
+                                 else no overlap with q, k, v or the cache             */
+    const xs_rope* rope;      /* host; its D is the cache's                            */
+    xs_paged_cache cache;
+    long long q_stride, k_stride, v_stride, q_out_stride;  /* between rows, as in xs_rope_fwd */
+    int T, H;
+} xs_rope_append_args;
+
+int xs_rope_append_paged(const xs_rope_append_args* args, void* stream);
 
 /*
  * xs_paged_step -- lays out one step on the device.  With c_i = cache_lens[i], a_i =
@@ -553,24 +570,34 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
  * Without `causal` a chunk's tokens see each other and the whole cache (the next chunk
  * of a video).  Query head h reads KV head h / (H / Hkv).  K, V and the probabilities
  * enter the products in `dtype`; sums, maxima and the accumulators are fp32.
- *   q            device, [T, H, D], rows q_stride elements apart (multiple of 8).
- *   outs, layout, P   the rows in one of the library's layouts (B = 1, S = T), as in
- *                xs_attn_varlen_fwd.  Rows from cu_q[n] on are left as they are.
- *   lse          device fp32 [T, H], or NULL.
- *   block_table  device int32, rows table_stride entries apart; the pages of a
- *                sequence's kv_len_i tokens (with a window: of those some row sees).  A page
- *                number outside [0, n_pages) and columns from table_width on read as zeros.
- *   n, H, Hkv, D, max_q, causal, window, workspace   as planned: a launch that does not
- *                match its plan computes nothing and xs_attn_get_device_error returns
- *                XS_ERR_DEVICE_BOUNDS.  H % Hkv == 0, H / Hkv <= 128.  window needs causal.
  * The sums of a tile that is cut among SMs are joined in a fixed order: equal calls on
  * equal plans give equal bits.  After XS_ERR_DEVICE_TIMEOUT plan again.
  */
-int xs_attn_paged_fwd(const void* q, const void* k_cache, const void* v_cache, const int* block_table, int layout,
-                      void* const* outs, float* lse, int T, int H, int Hkv, int D, int P, long long q_stride, int n,
-                      int table_width, long long table_stride, int n_pages, int page_size,
-                      const long long* k_cache_strides, const long long* v_cache_strides, int dtype, int max_q,
-                      int causal, int window, float scale, void* workspace, size_t workspace_bytes, void* stream);
+typedef struct xs_attn_paged_args {
+    const void* q;            /* device, [T, H, D], rows q_stride elements apart       */
+    const int* block_table;   /* device, [n] rows of table_width entries, table_stride
+                                 apart: the pages of a sequence's kv_len_i tokens (with a
+                                 window: of those that some row sees).  A page number
+                                 outside [0, n_pages) and columns from table_width on
+                                 read as zeros                                         */
+    float* lse;               /* device, [T, H], or NULL                               */
+    void* workspace;          /* as planned                                            */
+    size_t workspace_bytes;
+    void* outs[XS_MAX_P];     /* the rows in one of the library's layouts (B = 1, S = T),
+                                 as in xs_attn_varlen_fwd; rows from cu_q[n] on are left
+                                 as they are                                           */
+    xs_paged_cache cache;
+    long long q_stride, table_stride;
+    int layout, P;            /* XS_LAYOUT_*                                           */
+    int T, H;                 /* H % Hkv == 0, H / Hkv <= 128                          */
+    int n, table_width;       /* n, H, Hkv, D, max_q, causal, window as planned: a launch
+                                 that does not match its plan computes nothing, and
+                                 xs_attn_get_device_error returns XS_ERR_DEVICE_BOUNDS  */
+    int max_q, causal, window;   /* window > 0 needs causal                            */
+    float scale;              /* finite, >= 0                                          */
+} xs_attn_paged_args;
+
+int xs_attn_paged_fwd(const xs_attn_paged_args* args, void* stream);
 
 /*
  * xs_burst_gap -- Burst-Gap microbenchmark of the store path the fused epilogue

@@ -116,18 +116,48 @@ def test_rope_fwd_refusals(xs):
     assert xs.lib.xs_rope_fwd(A(0), A(1), A(2), 1, 1, 64, 64, 0, 0, ctypes.addressof(bad), None) == xs.XS_ERR_HEAD_DIM
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_longlong * 3),
+                ("vs", ctypes.c_longlong * 3), ("pages", ctypes.c_int), ("page", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "pos", "slots", "qo", "rope")] + [("cache", Cache)] + \
+               [(n, ctypes.c_longlong) for n in ("qs", "ks", "vs", "os_")] + [("T", ctypes.c_int), ("H", ctypes.c_int)]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "table", "lse", "ws")] + [("nbytes", ctypes.c_size_t)] + \
+               [("outs", ctypes.c_void_p * 16), ("cache", Cache), ("qs", ctypes.c_longlong), ("ts", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("layout", "P", "T", "H", "n", "width", "max_q", "causal", "window")] + \
+               [("scale", ctypes.c_float)]
+
+
+def test_the_binding_packs_the_structs(xs):
+    assert xs._APPEND_ARGS.size == ctypes.sizeof(AppendArgs)
+    assert {p.size for p in xs._ATTN_ARGS.values()} == {ctypes.sizeof(AttnArgs)} and set(xs._ATTN_ARGS) == set(range(1, 17))
+    assert Cache.dtype.offset == 80 and AttnArgs.cache.offset == 168 and AttnArgs.scale.offset == 308
+
+
 def _append(xs, **kw):
     a = dict(q=A(0), k=A(1), v=A(2), pos=A(3), slots=A(4), qo=A(5), kc=A(6), vc=A(7), T=10, H=4, Hkv=2, qs=512, ks=256,
-             vs=256, os_=512, pages=8, page=16, kst=S3(16 * 256, 256, 128), vst=S3(16 * 256, 256, 128), dtype=0)
+             vs=256, os_=512, pages=8, page=16, kst=S3(16 * 256, 256, 128), vst=S3(16 * 256, 256, 128), dtype=0, D=128)
+    keep = _init(xs)[1]
+    a["rope"] = ctypes.addressof(keep)
     a.update(kw)
-    s = _init(xs)[1]
-    return xs.lib.xs_rope_append_paged(*a.values(), ctypes.addressof(s), None)
+    c = Cache(a["kc"], a["vc"], a["kst"], a["vst"], a["pages"], a["page"], a["Hkv"], a["D"], a["dtype"], 0)
+    g = AppendArgs(*(a[n] for n in ("q", "k", "v", "pos", "slots", "qo", "rope")), c, a["qs"], a["ks"], a["vs"], a["os_"],
+                   a["T"], a["H"])
+    return xs.lib.xs_rope_append_paged(bytes(g), None)
 
 
 def test_append_refusals(xs):
     f = lambda **k: _append(xs, **k)   # noqa: E731
-    for name in ("q", "k", "v", "pos", "slots", "qo", "kc", "vc", "kst", "vst"):
+    for name in ("q", "k", "v", "pos", "slots", "qo", "kc", "vc", "rope"):
         assert f(**{name: None}) == xs.XS_ERR_NULL, name
+    assert xs.lib.xs_rope_append_paged(None, None) == xs.XS_ERR_NULL
+    assert f(D=64) == f(D=96) == xs.XS_ERR_HEAD_DIM      # not the rotation's
     assert f(page=8) == f(page=48) == f(page=2048) == f(page=0) == xs.XS_ERR_PAGE
     assert f(pages=0) == f(pages=2 ** 28) == f(Hkv=0) == f(ks=255) == f(kst=S3(4096, 120, 128)) == xs.XS_ERR_SHAPE
     assert f(kst=S3(4100, 256, 128)) == f(vst=S3(4096, 260, 128)) == f(slots=A(4) + 4) == f(kc=A(6) + 8) == xs.XS_ERR_ALIGNMENT
@@ -170,12 +200,15 @@ def _plan(xs, **kw):
 
 
 def _attn(xs, **kw):
-    a = dict(q=A(0), kc=A(1), vc=A(2), table=A(3), layout=1, outs=(ctypes.c_void_p * 16)(*(A(4) + (i << 28) for i in range(16))),
+    a = dict(q=A(0), kc=A(1), vc=A(2), table=A(3), layout=1, outs=[A(4) + (i << 28) for i in range(16)],
              lse=A(5), T=16, H=8, Hkv=2, D=128, P=1, qs=1024, n=4, width=10, ts=10, pages=64, page=16,
              kst=S3(4096, 256, 128), vst=S3(4096, 256, 128), dtype=0, max_q=1, causal=1, window=0, scale=0.1, ws=A(6),
              nbytes=1 << 30)
     a.update(kw)
-    return xs.lib.xs_attn_paged_fwd(*a.values(), None)
+    c = Cache(a["kc"], a["vc"], a["kst"], a["vst"], a["pages"], a["page"], a["Hkv"], a["D"], a["dtype"], 0)
+    g = AttnArgs(a["q"], a["table"], a["lse"], a["ws"], a["nbytes"], (ctypes.c_void_p * 16)(*a["outs"]), c, a["qs"], a["ts"],
+                 *(a[n] for n in ("layout", "P", "T", "H", "n", "width", "max_q", "causal", "window", "scale")))
+    return xs.lib.xs_attn_paged_fwd(bytes(g), None)
 
 
 def test_plan_refusals(xs):
@@ -192,9 +225,10 @@ def test_plan_refusals(xs):
 
 def test_attention_refusals(xs):
     f = lambda **k: _attn(xs, **k)   # noqa: E731
-    for name in ("q", "kc", "vc", "table", "outs", "ws", "kst", "vst"):
+    for name in ("q", "kc", "vc", "table", "ws"):
         assert f(**{name: None}) == xs.XS_ERR_NULL, name
-    assert f(outs=(ctypes.c_void_p * 1)(None)) == xs.XS_ERR_NULL
+    assert xs.lib.xs_attn_paged_fwd(None, None) == xs.XS_ERR_NULL
+    assert f(outs=[]) == f(outs=[A(4), A(7)], layout=0, P=4) == xs.XS_ERR_NULL
     assert f(T=0) == f(qs=1000) == f(width=0) == f(ts=9) == f(n=0) == f(max_q=0) == f(window=3, causal=0) == xs.XS_ERR_SHAPE
     assert f(pages=0) == f(pages=2 ** 28) == f(kst=S3(4096, 64, 128)) == xs.XS_ERR_SHAPE
     assert f(layout=3) == xs.XS_ERR_LAYOUT
@@ -205,7 +239,8 @@ def test_attention_refusals(xs):
     assert f(scale=float("nan")) == f(scale=-1.0) == xs.XS_ERR_SCALE
     assert f(q=A(0) + 8) == f(qs=1028) == f(kst=S3(4100, 256, 128)) == f(lse=A(5) + 2) == f(ws=A(6) + 16) == xs.XS_ERR_ALIGNMENT
     assert f(lse=A(4)) == f(ws=A(0)) == f(lse=A(1) + 64) == xs.XS_ERR_OVERLAP
-    assert f(outs=(ctypes.c_void_p * 1)(A(2) + 16)) == xs.XS_ERR_OVERLAP
+    assert f(outs=[A(2) + 16]) == f(outs=[A(4), A(4)], layout=0, P=2) == xs.XS_ERR_OVERLAP
+    assert f(D=96) == xs.XS_ERR_HEAD_DIM
     assert _passed(xs, f(lse=None)) and _passed(xs, f(layout=0, P=4)) and _passed(xs, f(n=1, ts=0))
 
 
