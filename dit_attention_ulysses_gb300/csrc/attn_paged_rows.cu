@@ -155,6 +155,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     float* join_o = reinterpret_cast<float*>(smem);                      // [WARPS][ROWS][O_STRIDE]
     float2* join_ml = reinterpret_cast<float2*>(smem + C::ML_OFF);       // [WARPS][ROWS]
 
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < WARPS * C::SLOTS; ++i) mbar_init(smem_addr(smem + C::BAR_OFF) + i * 8, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
     const PagedRange range = a.work.ranges[blockIdx.x];
     const int n_seqs = a.work.header->n_seqs;
     {
@@ -164,15 +171,6 @@ __global__ void __launch_bounds__(THREADS, 2)
             if (tid == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, h.n, h.tokens, h.grid);
             return;
         }
-    }
-    if (tid == 0) {
-        *abort_flag = 0;
-        for (int i = 0; i < WARPS * C::SLOTS; ++i) mbar_init(smem_addr(smem + C::BAR_OFF) + i * 8, 1);
-        fence_mbar_init();
-    }
-    if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
     }
     __syncthreads();
 

@@ -62,10 +62,14 @@ cudaError_t launch_paged_step(const StepArgs& a, int num_sms, cudaStream_t strea
 struct PagedTiling {
     int tokens;     // new tokens per tile
     int block;      // keys per block
-    int grid;       // CTAs, one contiguous range of the work each
+    int grid;       // CTAs
     int start_cost; // cost of a tile's start and end, in keys
     int snap;       // a cut leaves at least this many blocks on both sides
+    int whole;      // a tile of fewer blocks is not cut
+    int least;      // cost per CTA from which on another CTA takes part
     int waves;      // whole tiles are dealt out in up to this many waves before the rest is cut (0: all is cut)
+    // below few_keys keys per CTA on average (waves == 0) these replace start_cost and least
+    int few_keys, few_start_cost, few_least;
 };
 constexpr int MAX_PAGED_WAVES = 64;
 

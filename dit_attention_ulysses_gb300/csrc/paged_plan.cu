@@ -6,8 +6,7 @@
 //
 // Cut part: CTA c takes a contiguous range of the line such that all CTAs end together
 // however ragged the lengths are.  A range may start and end inside a tile; cuts fall on
-// key blocks and leave at least `snap` blocks on both sides, and a range is long enough
-// that no two cuts meet.
+// key blocks and leave at least `snap` blocks on both sides.
 //
 // Waves (tiles of 128 rows): before that, whole tiles are dealt out wave by wave, tile
 // w * grid + c (or the w * grid + c-th group of `slot` tiles) to CTA c, for as many waves
@@ -77,6 +76,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     __shared__ int waves_min;
     const int tid = threadIdx.x;
 
+    PagedTiling keys_only = a.tile;
+    keys_only.start_cost = 0;
     long long total = 0, all_tiles = 0;
     int kept = 0;
     for (int i0 = 0; i0 < a.n; i0 += PLAN_THREADS) {
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             s.kv_len = kv > 0 ? kv : 0;
         }
         const int mine = s.q_len > 0 ? paged_tiles(s, a.tile.tokens) : 0;
-        const long long cost = mine > 0 ? a.Hkv * paged_cost(s, mine, a.tile, a.causal, a.window) : 0;
+        const long long cost = mine > 0 ? a.Hkv * paged_cost(s, mine, keys_only, a.causal, a.window) : 0;
         long long cost_all, kept_all, tiles_all;
         const long long cost_at = block_scan(cost, warp_sums, cost_all);
         const long long tiles_at = block_scan(static_cast<long long>(mine) * a.Hkv, warp_sums, tiles_all);
@@ -104,18 +105,31 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         all_tiles += tiles_all;
         kept += static_cast<int>(kept_all);
     }
+    // Few keys per CTA: the time is latency, and short pieces of many CTAs beat long ones of some,
+    // though their parts take longer to join
+    PagedTiling tile = a.tile;
+    if (a.tile.waves == 0 && total < static_cast<long long>(a.tile.grid) * a.tile.few_keys) {
+        tile.start_cost = a.tile.few_start_cost;
+        tile.least = a.tile.few_least;
+    }
     if (tid == 0) {
         prefix[kept] = total;
         tiles[kept] = all_tiles;
         waves_min = a.tile.waves;
     }
+    total += all_tiles * tile.start_cost;
     __syncthreads();   // the prefix sums, and the sequences written by other threads of this CTA
+    for (int i = tid; i <= kept; i += PLAN_THREADS) prefix[i] += tiles[i] * tile.start_cost;
+    __syncthreads();
 
-    // every range at least twice the snap plus a start, so that cuts in one tile differ
-    const long long least = static_cast<long long>(2 * a.tile.snap + 1) * a.tile.block + a.tile.start_cost;
+    // As many CTAs as there is work for, but one per tile while there are CTAs.  At two blocks per range no two
+    // cuts fall on one block inside a tile (on a tile's start they may: a range is then empty).
     const int grid = a.tile.grid;
+    const long long least = tile.least;
     long long ranges = total / least;
+    if (ranges < all_tiles) ranges = all_tiles;
     if (ranges > grid) ranges = grid;
+    if (ranges > total / (2 * tile.block)) ranges = total / (2 * tile.block);
     if (ranges < 1) ranges = kept > 0 ? 1 : 0;
 
     // ---- waves
@@ -148,8 +162,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
                     slot.pos = p;
                     slot.seq = s;
                 }
-                cost += static_cast<double>(paged_cost(s, p.tile + n, a.tile, a.causal, a.window) -
-                                            paged_cost(s, p.tile, a.tile, a.causal, a.window));
+                cost += static_cast<double>(paged_cost(s, p.tile + n, tile, a.causal, a.window) -
+                                            paged_cost(s, p.tile, tile, a.causal, a.window));
                 t += n;
                 left -= n;
             }
@@ -180,8 +194,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             const PagedSeq s = a.work.seqs[q];
             const int of_head = paged_tiles(s, a.tile.tokens);
             const long long x = t - tiles[q], head = x / of_head;
-            x0 = prefix[q] + head * paged_cost(s, of_head, a.tile, a.causal, a.window) +
-                 paged_cost(s, x - head * of_head, a.tile, a.causal, a.window);
+            x0 = prefix[q] + head * paged_cost(s, of_head, tile, a.causal, a.window) +
+                 paged_cost(s, x - head * of_head, tile, a.causal, a.window);
         }
     }
     // grid <= PLAN_THREADS: one thread per CTA
@@ -201,7 +215,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
                                                 : static_cast<long long>(static_cast<double>(before) / shares * rest));
             if (x < total) {
                 const int q = find(prefix, kept, x);
-                p = paged_locate(a.work.seqs[q], q, x - prefix[q], (prefix[q + 1] - prefix[q]) / a.Hkv, a.tile, a.Hkv, a.causal,
+                p = paged_locate(a.work.seqs[q], q, x - prefix[q], (prefix[q + 1] - prefix[q]) / a.Hkv, tile, a.Hkv, a.causal,
                                  a.window);
             }
         }

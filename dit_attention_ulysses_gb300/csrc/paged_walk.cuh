@@ -97,7 +97,8 @@ __host__ __device__ __forceinline__ bool paged_before(const PagedPos& a, const P
 }
 
 // Where cost x of a sequence's cost * Hkv falls: a block of a tile.  Cuts closer than
-// `snap` blocks to a tile's end move to that end.
+// `snap` blocks to a tile's end move to that end, cuts in a tile of fewer than `whole`
+// blocks to the nearer one.
 __host__ __device__ __forceinline__ PagedPos paged_locate(const PagedSeq& s, int seq, long long x, long long seq_cost,
                                                           const PagedTiling& g, int Hkv, int causal, int window) {
     PagedPos p;
@@ -121,9 +122,10 @@ __host__ __device__ __forceinline__ PagedPos paged_locate(const PagedSeq& s, int
     paged_tile_blocks(s, lo, g, causal, window, first, count);
     const long long k = y > 0 ? (y + g.block / 2) / g.block : 0;
     p.k = k > count ? count : static_cast<int>(k);
-    if (p.k < g.snap) {
+    const bool whole = count < g.whole;
+    if (p.k < g.snap || (whole && 2 * p.k < count)) {
         p.k = 0;
-    } else if (count - p.k < g.snap) {
+    } else if (count - p.k < g.snap || whole) {
         paged_next(p, s, g.tokens, Hkv);
     }
     return p;

@@ -30,8 +30,9 @@
 namespace xs {
 namespace {
 
-constexpr int ROPE_THREADS = 256;
+constexpr int ROPE_THREADS = 128;
 constexpr int ROPE_UNROLL = 4;
+constexpr long long ROPE_LONG = 48ll << 20;   // bytes read, see launch_rope
 
 template <bool F16>
 __device__ __forceinline__ void widen(uint32_t w, float& lo, float& hi) {
@@ -85,10 +86,11 @@ __device__ __forceinline__ void turn(Chunk2& x, const float (&c)[8], const float
     }
 }
 
-// Block: 256 / units tokens (blockIdx.x) x one group of heads (blockIdx.y).
+// Block: 128 / units tokens (blockIdx.x) x one group of heads (blockIdx.y).
 // Heads are numbered q 0 .. H-1, then (APPEND) k H .. H+Hkv-1, v H+Hkv .. H+2Hkv-1.
-template <bool F16, bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeArgs g) {
+// LONG: no register limit (74 instead of 64), see launch_rope.
+template <bool F16, bool INTERLEAVED, bool APPEND, bool LONG>
+__global__ void __launch_bounds__(ROPE_THREADS, LONG ? 1 : 8) rope_kernel(const __grid_constant__ RopeArgs g) {
     const int units = g.D >> 4;
     const int tl = threadIdx.x / units, u = threadIdx.x - tl * units;
     const long long t = static_cast<long long>(blockIdx.x) * (ROPE_THREADS / units) + tl;
@@ -172,26 +174,41 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
 
 }  // namespace
 
-// Heads per thread: all of them when the tokens alone fill the SMs (1024 threads
-// each), fewer for short inputs, so that a single token still spreads its heads
-// over threads.
+template <bool F16, bool INTERLEAVED, bool APPEND>
+static void launch(const RopeArgs& a, dim3 grid, bool is_long, cudaStream_t stream) {
+    if (is_long)
+        rope_kernel<F16, INTERLEAVED, APPEND, true><<<grid, ROPE_THREADS, 0, stream>>>(a);
+    else
+        rope_kernel<F16, INTERLEAVED, APPEND, false><<<grid, ROPE_THREADS, 0, stream>>>(a);
+}
+
+// Heads per thread: all of them when the tokens alone fill the SMs (768 threads each),
+// fewer for short inputs, so that a single token still spreads its heads over threads.
+// Registers: below ROPE_LONG bytes 64 of them, which puts all blocks of a single wave side
+// by side (28 MB: 12.2 us against 13.2 without a limit); from there on no limit, whose
+// loads reach further ahead (128 MB: 44.7 us against 48.3; 776 MB: 231 against 236).
 cudaError_t launch_rope(const RopeArgs& args, int dtype, int layout, bool append, int num_sms, cudaStream_t stream) {
     RopeArgs a = args;
     const int units = a.D / 16, tokens = ROPE_THREADS / units;
     const int total = append ? a.H + 2 * a.Hkv : a.H;
-    const long long threads = static_cast<long long>(a.T) * units, want = static_cast<long long>(num_sms) * 1024;
+    const long long threads = static_cast<long long>(a.T) * units, want = static_cast<long long>(num_sms) * 768;
     long long groups = (want + threads - 1) / threads;
     if (groups > total) groups = total;
     a.heads_per = static_cast<int>((total + groups - 1) / groups);
     const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens),
                     static_cast<unsigned>((total + a.heads_per - 1) / a.heads_per));
-    using Kernel = void (*)(const RopeArgs);
-    static const Kernel kernels[2][2][2] = {
-        {{rope_kernel<false, false, false>, rope_kernel<false, false, true>},
-         {rope_kernel<false, true, false>, rope_kernel<false, true, true>}},
-        {{rope_kernel<true, false, false>, rope_kernel<true, false, true>},
-         {rope_kernel<true, true, false>, rope_kernel<true, true, true>}}};
-    kernels[dtype][layout][append ? 1 : 0]<<<grid, ROPE_THREADS, 0, stream>>>(a);
+    const bool is_long = static_cast<long long>(a.T) * total * a.D * 2 >= ROPE_LONG;
+    const int k = dtype * 4 + layout * 2 + (append ? 1 : 0);
+    switch (k) {
+        case 0: launch<false, false, false>(a, grid, is_long, stream); break;
+        case 1: launch<false, false, true>(a, grid, is_long, stream); break;
+        case 2: launch<false, true, false>(a, grid, is_long, stream); break;
+        case 3: launch<false, true, true>(a, grid, is_long, stream); break;
+        case 4: launch<true, false, false>(a, grid, is_long, stream); break;
+        case 5: launch<true, false, true>(a, grid, is_long, stream); break;
+        case 6: launch<true, true, false>(a, grid, is_long, stream); break;
+        default: launch<true, true, true>(a, grid, is_long, stream); break;
+    }
     return cudaGetLastError();
 }
 

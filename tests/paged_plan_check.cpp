@@ -1,5 +1,5 @@
 // Host check of the paged attention's division of work (csrc/paged_walk.cuh): reads
-// "tokens block grid start_cost snap Hkv causal window n" and n pairs "q_len kv_len",
+// "tokens block grid start_cost snap whole least Hkv causal window n" and n pairs "q_len kv_len",
 // plays the plan kernel, and checks every range.  Prints "ok <ranges> <longest> <mean>"
 // (cost of the longest range and the mean) or the first fault found.
 #include <cstdio>
@@ -20,8 +20,8 @@ static void fault(const char* what, long long a, long long b) {
 int main() {
     PagedTiling g;
     int Hkv, causal, window, n;
-    while (std::scanf("%d %d %d %d %d %d %d %d %d", &g.tokens, &g.block, &g.grid, &g.start_cost, &g.snap, &Hkv,
-                      &causal, &window, &n) == 9) {
+    while (std::scanf("%d %d %d %d %d %d %d %d %d %d %d", &g.tokens, &g.block, &g.grid, &g.start_cost, &g.snap, &g.whole,
+                      &g.least, &Hkv, &causal, &window, &n) == 11) {
         std::vector<PagedSeq> seqs;
         for (int i = 0; i < n; ++i) {
             PagedSeq s{0, 0, 0, i};
@@ -58,9 +58,12 @@ int main() {
             prefix[i + 1] = prefix[i] + Hkv * sum;
         }
         const long long total = prefix[kept];
-        const long long least = static_cast<long long>(2 * g.snap + 1) * g.block + g.start_cost;
-        long long ranges = total / least;
+        long long all_tiles = 0;
+        for (const PagedSeq& s : seqs) all_tiles += static_cast<long long>(Hkv) * paged_tiles(s, g.tokens);
+        long long ranges = total / g.least;
+        if (ranges < all_tiles) ranges = all_tiles;
         if (ranges > g.grid) ranges = g.grid;
+        if (ranges > total / (2 * g.block)) ranges = total / (2 * g.block);
         if (ranges < 1) ranges = kept > 0 ? 1 : 0;
         std::vector<PagedPos> cut(ranges + 1);
         for (int c = 0; c <= ranges && ranges > 0; ++c) {
@@ -112,7 +115,7 @@ int main() {
             int cta = std::get<2>(kv.second[0]);
             const int c_first = cta, c_last = std::get<2>(kv.second.back());
             for (auto& p : kv.second) {
-                if (std::get<0>(p) != at || std::get<2>(p) != cta) fault("pieces", i, t);
+                if (std::get<0>(p) != at || std::get<2>(p) != cta) fault("pieces", i, t);   // no CTA between has none
                 // what the range record says of the tile's CTAs
                 PagedPos q{i, h, t, 1};
                 if (at > 0 && first_at(q) - 1 != c_first) fault("c0", i, cta);

@@ -280,8 +280,9 @@ def test_division_of_work(tmp_path):
     cases = []
     for _ in range(1500):
         G = r.choice([1, 2, 3, 4, 5, 8, 16, 32])
-        rows, block, grid, cost, snap = r.choice([(16, 64, 304, 128, 1), (32, 64, 304, 128, 1), (128, 128, 152, 256, 2),
-                                                  (128, 128, 148, 512, 2), (128, 128, 152, 300, 1)])
+        rows, block, grid, cost, snap, whole, least = r.choice([
+            (16, 32, 304, 256, 4, 16, 512), (32, 32, 304, 64, 4, 16, 160), (128, 128, 152, 384, 2, 4, 1024),
+            (128, 128, 148, 0, 1, 0, 128), (16, 64, 304, 16, 1, 3, 64), (128, 128, 152, 300, 5, 2, 512)])
         causal = r.randint(0, 1)
         window = log(1, 5000) if causal and r.random() < 0.4 else 0
         n = log(1, 40)
@@ -289,7 +290,8 @@ def test_division_of_work(tmp_path):
         for _ in range(n):
             q = r.choice([0, 1, 1, log(1, 3000)])
             lens += [q, max(0, r.choice([q + log(1, 20000), q, q - r.randint(0, q), 0]))]
-        cases.append(" ".join(map(str, [max(1, rows // G), block, grid, cost, snap, r.choice([1, 2, 8, 24]), causal, window, n]
+        cases.append(" ".join(map(str, [max(1, rows // G), block, grid, cost, snap, whole, least, r.choice([1, 2, 8, 24]), causal, window,
+                                n]
                                   + lens)))
     p = subprocess.run([exe], input="\n".join(cases), capture_output=True, text=True)
     out = p.stdout.strip().split("\n")
