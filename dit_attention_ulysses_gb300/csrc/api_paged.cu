@@ -186,9 +186,9 @@ Tiling make_tiling(int G, int max_q, int sms) {
         x.t.tokens = ROWS_TILE / G;
         x.t.block = 128;
         x.t.grid = sms;
-        x.t.start_cost = 384;
-        x.t.snap = 2;
-        x.t.whole = 4;
+        x.t.start_cost = 512;
+        x.t.snap = 4;
+        x.t.whole = 12;
         x.t.least = 1024;
         x.t.waves = xs::MAX_PAGED_WAVES;
         return x;

@@ -506,23 +506,24 @@ __device__ __noinline__ bool part_epilogue(const PagedAttnArgs& a, const Piece& 
     using C = Cfg<D>;
     constexpr int DH = D / 2;
     auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
-    const bool live = row < d.n_rows;
-    {
-        const size_t at = static_cast<size_t>(d.part) * BLOCK_M + row;
-        float* po = a.work.part_o + at * D + half * DH;
+    // A part is laid out by threads: the k-th four channels of all 256, one after the other, so that
+    // every access is 512 contiguous bytes per warp (by rows, a join of two parts took 11 us)
+    constexpr int SOFTMAX_THREADS = NUM_SOFTMAX_WARPS * 32;
+    float4* const parts_o = reinterpret_cast<float4*>(a.work.part_o);
+    auto at_o = [&](int slot, int k) {
+        return (static_cast<size_t>(slot) * (DH / 4) + k) * SOFTMAX_THREADS + threadIdx.x;
+    };
+    auto at_ml = [&](int slot) { return static_cast<size_t>(slot) * BLOCK_M + row; };
 #pragma unroll 1
-        for (int q = 0; q < DH / 32; ++q) {
-            uint32_t orr[32];
-            tmem_ld16x2_32<DH>(o_base + q * 32, orr);
-            tmem_wait_ld();
-            if (live) {
+    for (int q = 0; q < DH / 32; ++q) {
+        uint32_t orr[32];
+        tmem_ld16x2_32<DH>(o_base + q * 32, orr);
+        tmem_wait_ld();
 #pragma unroll
-                for (int v4 = 0; v4 < 8; ++v4)
-                    st_global_v4(po + q * 32 + v4 * 4, orr[4 * v4], orr[4 * v4 + 1], orr[4 * v4 + 2], orr[4 * v4 + 3]);
-            }
-        }
-        if (live && half == 0) a.work.part_ml[at] = make_float2(m, l);
+        for (int v4 = 0; v4 < 8; ++v4)
+            st_global_v4(parts_o + at_o(d.part, q * 8 + v4), orr[4 * v4], orr[4 * v4 + 1], orr[4 * v4 + 2], orr[4 * v4 + 3]);
     }
+    if (half == 0) a.work.part_ml[at_ml(d.part)] = make_float2(m, l);
     tc_fence_before();
     __threadfence();
     warp_arrive(bar(C::B_O_FREE));
@@ -545,41 +546,42 @@ __device__ __noinline__ bool part_epilogue(const PagedAttnArgs& a, const Piece& 
     if (!*last) return true;
     __threadfence();   // the other CTAs' parts, published before their counts
     int token, head;
-    uint16_t* dst = dest_row(a, d, row, token, head);
+    uint16_t* const dst = dest_row(a, d, row, token, head);
     if (dst == nullptr) return true;
-    auto slot = [&](int c) { return (2 * static_cast<size_t>(c) + (c == d.c0 ? 1 : 0)) * BLOCK_M + row; };
+    float acc[DH];
+#pragma unroll
+    for (int i = 0; i < DH; ++i) acc[i] = 0.0f;
     float m_all = NO_MAX, l_all = 0.0f;
-    for (int c = d.c0; c <= d.c1; ++c) m_all = fmaxf(m_all, __ldcg(&a.work.part_ml[slot(c)]).x);
-    for (int c = d.c0; c <= d.c1; ++c) {
-        const float2 ml = __ldcg(&a.work.part_ml[slot(c)]);
-        l_all += ml.y * ex2_approx(ml.x - m_all);
+#pragma unroll 1
+    for (int c = d.c0; c <= d.c1; ++c) {   // in CTA order
+        const int slot = 2 * c + (c == d.c0 ? 1 : 0);
+        const float2 ml = __ldcg(a.work.part_ml + at_ml(slot));
+        float4 v[DH / 4];
+#pragma unroll
+        for (int k = 0; k < DH / 4; ++k) v[k] = __ldcg(parts_o + at_o(slot, k));
+        const float m_new = fmaxf(m_all, ml.x);
+        const float f0 = ex2_approx(m_all - m_new), f1 = ex2_approx(ml.x - m_new);
+        m_all = m_new;
+        l_all = l_all * f0 + ml.y * f1;
+#pragma unroll
+        for (int k = 0; k < DH / 4; ++k) {
+            acc[4 * k + 0] = acc[4 * k + 0] * f0 + v[k].x * f1;
+            acc[4 * k + 1] = acc[4 * k + 1] * f0 + v[k].y * f1;
+            acc[4 * k + 2] = acc[4 * k + 2] * f0 + v[k].z * f1;
+            acc[4 * k + 3] = acc[4 * k + 3] * f0 + v[k].w * f1;
+        }
     }
     const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
     if (half == 0 && a.lse != nullptr) a.lse[static_cast<size_t>(token) * a.H + head] = log_sum(m_all, l_all);
-#pragma unroll 1
-    for (int q = 0; q < DH / 16; ++q) {
-        float acc[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-        for (int c = d.c0; c <= d.c1; ++c) {
-            const float f = ex2_approx(__ldcg(&a.work.part_ml[slot(c)]).x - m_all);
-            const float4* po = reinterpret_cast<const float4*>(a.work.part_o + slot(c) * D + half * DH + q * 16);
+    for (int q = 0; q < DH / 8; ++q) {
+        uint32_t w[4];
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-                const float4 v = __ldcg(po + v4);
-                acc[4 * v4 + 0] += v.x * f;
-                acc[4 * v4 + 1] += v.y * f;
-                acc[4 * v4 + 2] += v.z * f;
-                acc[4 * v4 + 3] += v.w * f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float x = acc[8 * q + 2 * i] * inv, y = acc[8 * q + 2 * i + 1] * inv;
+            w[i] = F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
         }
-        uint32_t wv[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            wv[i] = F16 ? pack_f16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv)
-                        : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-        st_global_v4(dst + half * DH + q * 16, wv[0], wv[1], wv[2], wv[3]);
-        st_global_v4(dst + half * DH + q * 16 + 8, wv[4], wv[5], wv[6], wv[7]);
+        st_global_v4(dst + half * DH + q * 8, w[0], w[1], w[2], w[3]);
     }
     return true;
 }
