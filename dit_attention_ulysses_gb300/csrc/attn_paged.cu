@@ -263,6 +263,7 @@ __device__ void producer_k_role(const CUtensorMap* tq, const CUtensorMap* tk, co
             mbar_arrive(bar(C::B_PIECE + u % PIECES));   // release: the descriptor is visible to whoever waits
         }
         if (!more) break;
+        if (cut_end) pdl_launch();   // the CTA's last piece (a CTA that ends without one counts when it exits)
         if (lane == 0) {
             mbar_arrive_expect_tx(bar(C::B_Q_FULL + qb), static_cast<uint32_t>(tokens * a.G) * D * 2);
             for (int pnl = 0; pnl < C::PANELS; ++pnl)
@@ -794,6 +795,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    pdl_wait();
 
     if (warp < NUM_SOFTMAX_WARPS)
         softmax_role<D, F16>(args, smem, bar0, tmem_base, abort_flag);
@@ -824,8 +826,8 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
     auto kern = attn_paged_kernel<D, F16>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    kern<<<a.tile.grid, NUM_THREADS, Cfg<D>::SMEM_ALLOC, stream>>>(tq, tk, tv, a);
-    return cudaGetLastError();
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(a.tile.grid)), NUM_THREADS, Cfg<D>::SMEM_ALLOC, stream, tq, tk,
+                             tv, a);
 }
 
 }  // namespace

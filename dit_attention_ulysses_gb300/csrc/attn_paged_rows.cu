@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
+    pdl_wait();
     const PagedRange range = a.work.ranges[blockIdx.x];
     const int n_seqs = a.work.header->n_seqs;
     {
@@ -450,6 +451,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                 drain_wait(bars + ((item + i) % C::SLOTS) * 8, ((item + i) / C::SLOTS) & 1, 20000000ull);
         item += items;
 
+        if (cut_end) pdl_launch();   // the end is near
+
         // ---- join the warps
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -578,8 +581,7 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Page
     const int smem = RowsCfg<D, MT>::ALLOC;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.tile.grid, THREADS, smem, stream>>>(tk, tv, a);
-    return cudaGetLastError();
+    return launch_overlapped(kern, dim3(static_cast<unsigned>(a.tile.grid)), THREADS, smem, stream, tk, tv, a);
 }
 
 }  // namespace

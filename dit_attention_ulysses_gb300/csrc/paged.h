@@ -10,6 +10,24 @@
 
 namespace xs {
 
+// Launch whose prologue may overlap the end of the kernel before it on the stream; every
+// thread of the kernel calls pdl_wait (ptx.cuh) before it touches global memory.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                     const Args&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---- rotary positions, and their fusion with the cache append (rope.cu)
 struct RopeArgs {
     const void* q;            // [T, H, D], rows q_stride elements apart

@@ -24,6 +24,7 @@
 
 #include "paged.h"
 #include "paged_walk.cuh"
+#include "ptx.cuh"
 
 namespace xs {
 namespace {
@@ -76,6 +77,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     __shared__ int waves_min;
     const int tid = threadIdx.x;
 
+    pdl_launch();
+    pdl_wait();
     PagedTiling keys_only = a.tile;
     keys_only.start_cost = 0;
     long long total = 0, all_tiles = 0;
@@ -287,8 +290,7 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    paged_plan_kernel<<<1, PLAN_THREADS, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(paged_plan_kernel, dim3(1), PLAN_THREADS, smem, stream, a);
 }
 
 }  // namespace xs

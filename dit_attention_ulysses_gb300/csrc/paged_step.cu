@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace xs {
 namespace {
@@ -100,6 +101,8 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const __grid_consta
     const int shift = a.page_shift;
     auto pages_of = [&](long long tokens) -> long long { return (tokens + (1ll << shift) - 1) >> shift; };
 
+    pdl_launch();
+    pdl_wait();
     const int list = min(max(*a.free_count, 0), a.n_pages);   // entries of the free list
     int c[K], stat[K], rows_of[K], need_of[K];
     Sums sum{0, 0, 0};
@@ -240,8 +243,7 @@ static cudaError_t launch(const StepArgs& a, int num_sms, cudaStream_t stream) {
     const long long work = a.rows > a.n ? a.rows : a.n;
     long long grid = (work + THREADS - 1) / THREADS;
     if (grid > num_sms) grid = num_sms;
-    paged_step_kernel<THREADS, K><<<static_cast<unsigned>(grid), THREADS, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(paged_step_kernel<THREADS, K>, dim3(static_cast<unsigned>(grid)), THREADS, smem, stream, a);
 }
 
 // One CTA per 512 or 1024 rows, at most one per SM: a single one for a decoding batch.

@@ -348,6 +348,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Programmatic dependent launch: pdl_wait returns once every kernel launched before on the
+// stream has finished and its stores are visible (at once in an ordinary launch); nothing
+// that such a kernel may write is read, and nothing at all written, before it, by any
+// thread.  pdl_launch allows the next kernel to start its own prologue.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // GPU-scope release store / acquire load of a 32-bit flag in global memory.
 __device__ __forceinline__ void st_release_gpu(unsigned* p, unsigned v) {
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");

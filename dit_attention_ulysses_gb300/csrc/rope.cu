@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace xs {
 namespace {
@@ -91,6 +92,8 @@ __device__ __forceinline__ void turn(Chunk2& x, const float (&c)[8], const float
 // LONG: no register limit (74 instead of 64), see launch_rope.
 template <bool F16, bool INTERLEAVED, bool APPEND, bool LONG>
 __global__ void __launch_bounds__(ROPE_THREADS, LONG ? 1 : 8) rope_kernel(const __grid_constant__ RopeArgs g) {
+    pdl_launch();
+    pdl_wait();
     const int units = g.D >> 4;
     const int tl = threadIdx.x / units, u = threadIdx.x - tl * units;
     const long long t = static_cast<long long>(blockIdx.x) * (ROPE_THREADS / units) + tl;
@@ -175,11 +178,9 @@ __global__ void __launch_bounds__(ROPE_THREADS, LONG ? 1 : 8) rope_kernel(const 
 }  // namespace
 
 template <bool F16, bool INTERLEAVED, bool APPEND>
-static void launch(const RopeArgs& a, dim3 grid, bool is_long, cudaStream_t stream) {
-    if (is_long)
-        rope_kernel<F16, INTERLEAVED, APPEND, true><<<grid, ROPE_THREADS, 0, stream>>>(a);
-    else
-        rope_kernel<F16, INTERLEAVED, APPEND, false><<<grid, ROPE_THREADS, 0, stream>>>(a);
+static cudaError_t launch(const RopeArgs& a, dim3 grid, bool is_long, cudaStream_t stream) {
+    return is_long ? launch_overlapped(rope_kernel<F16, INTERLEAVED, APPEND, true>, grid, ROPE_THREADS, 0, stream, a)
+                   : launch_overlapped(rope_kernel<F16, INTERLEAVED, APPEND, false>, grid, ROPE_THREADS, 0, stream, a);
 }
 
 // Heads per thread: all of them when the tokens alone fill the SMs (768 threads each),
@@ -200,16 +201,15 @@ cudaError_t launch_rope(const RopeArgs& args, int dtype, int layout, bool append
     const bool is_long = static_cast<long long>(a.T) * total * a.D * 2 >= ROPE_LONG;
     const int k = dtype * 4 + layout * 2 + (append ? 1 : 0);
     switch (k) {
-        case 0: launch<false, false, false>(a, grid, is_long, stream); break;
-        case 1: launch<false, false, true>(a, grid, is_long, stream); break;
-        case 2: launch<false, true, false>(a, grid, is_long, stream); break;
-        case 3: launch<false, true, true>(a, grid, is_long, stream); break;
-        case 4: launch<true, false, false>(a, grid, is_long, stream); break;
-        case 5: launch<true, false, true>(a, grid, is_long, stream); break;
-        case 6: launch<true, true, false>(a, grid, is_long, stream); break;
-        default: launch<true, true, true>(a, grid, is_long, stream); break;
+        case 0: return launch<false, false, false>(a, grid, is_long, stream);
+        case 1: return launch<false, false, true>(a, grid, is_long, stream);
+        case 2: return launch<false, true, false>(a, grid, is_long, stream);
+        case 3: return launch<false, true, true>(a, grid, is_long, stream);
+        case 4: return launch<true, false, false>(a, grid, is_long, stream);
+        case 5: return launch<true, false, true>(a, grid, is_long, stream);
+        case 6: return launch<true, true, false>(a, grid, is_long, stream);
+        default: return launch<true, true, true>(a, grid, is_long, stream);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace xs
