@@ -422,7 +422,11 @@ class Rope:
         self._struct = _RopeStruct()
         self.ptr = ctypes.addressof(self._struct)
         self.D, self.rot = D, D if rot is None else rot
-        xs_rope_init(self, D, self.rot, layout, base, scaling, factor, context, low, high, magnitude)
+        self._args = (D, self.rot, layout, base, scaling, factor, context, low, high, magnitude)
+        xs_rope_init(self, *self._args)
+
+    def __reduce__(self):   # copies have a table of their own
+        return Rope, self._args
 
 
 def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling: int, factor: float,
@@ -603,6 +607,9 @@ class PagedWorkspace:
         self._buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.ptr = (self._buf.data_ptr() + 255) & ~255
         self.planned = None   # (max_q, causal, window) of the plan
+
+    def __reduce__(self):   # a copy is a new workspace without a plan
+        return PagedWorkspace, (self.n, self.H, self.Hkv, self.D, self._buf.device)
 
 
 def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, causal: bool = True, window: int = 0,

@@ -95,6 +95,30 @@ Range cache_span(const void* p, const CacheStrides& c, int n_pages, int page_siz
     return range_of(p, last * 2);
 }
 
+// Whether K and V of a cache share no element: apart in memory, or (one buffer for both, with
+// equal strides) apart within every page, every token or every head, whatever holds both.
+bool kv_apart(const xs_paged_cache& c, const CacheStrides& ks, const CacheStrides& vs, const Range& k, const Range& v) {
+    if (!overlaps(k, v)) return true;
+    const int dims[3] = {c.n_pages, c.page_size, c.Hkv};
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i] > 1 && ks.s[i] != vs.s[i]) return false;
+    }
+    const uintptr_t lo = k.lo < v.lo ? k.lo : v.lo, hi = k.lo < v.lo ? v.lo : k.lo;
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i] == 1) continue;
+        int64_t width = c.D;   // span of the dimensions with smaller strides
+        bool nested = true;
+        for (int j = 0; j < 3; ++j) {
+            if (j == i || dims[j] == 1) continue;
+            if (ks.s[j] < ks.s[i]) width += (dims[j] - 1) * static_cast<int64_t>(ks.s[j]);
+            else if (ks.s[j] % ks.s[i] != 0) nested = false;   // larger strides keep the offset's place
+        }
+        const int64_t stride = ks.s[i] * 2, d = static_cast<int64_t>((hi - lo) % static_cast<uintptr_t>(stride));
+        if (nested && d >= width * 2 && stride - d >= width * 2) return true;
+    }
+    return false;
+}
+
 int check_rope(const xs_rope* rope) {
     if (!rope) return XS_ERR_NULL;
     if (rope->D != 64 && rope->D != 128) return XS_ERR_HEAD_DIM;
@@ -340,9 +364,7 @@ int xs_rope_append_paged(const xs_rope_append_args* args, void* stream) {
     if (rows_overlap(rk, ro) || rows_overlap(rv, ro)) return XS_ERR_OVERLAP;
     const Range kc = cache_span(cache.k, ks, cache.n_pages, cache.page_size, Hkv, D),
                 vc = cache_span(cache.v, vs, cache.n_pages, cache.page_size, Hkv, D);
-    // K and V may be interleaved in one buffer (other pages, tokens or heads); which elements two
-    // strided caches share is the caller's to keep apart, equal pointers are refused
-    if (cache.k == cache.v) return XS_ERR_OVERLAP;
+    if (!kv_apart(cache, ks, vs, kc, vc)) return XS_ERR_OVERLAP;
     const Range pos = range_of(g.positions, static_cast<int64_t>(T) * 4),
                 sl = range_of(g.slots, static_cast<int64_t>(T) * 8);
     for (const Range& c : {kc, vc}) {

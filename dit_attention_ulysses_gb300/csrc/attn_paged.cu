@@ -55,7 +55,7 @@ constexpr uint32_t S_COL = 0;     // + 128 * buffer; P(g) over the first 64 colu
 constexpr int S_BUFS = 3;
 constexpr uint32_t O_COL = 384;
 constexpr float RESCALE_THRESHOLD = 8.0f;   // log2 units
-constexpr float NO_MAX = -1e30f;            // running maximum of a row that has seen nothing
+constexpr float NO_MAX = -3.402823466e38f;            // running maximum of a row that has seen nothing
 constexpr int PIECES = 4;                   // descriptors in flight (see producer_k_role)
 
 // One piece of work: key blocks of one tile, written by the producer.

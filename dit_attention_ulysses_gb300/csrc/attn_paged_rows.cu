@@ -41,7 +41,7 @@ constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int GROUP = 32;                  // keys of a ring slot
 constexpr int JOIN_BATCH = 16;             // parts of a cut tile read at once
-constexpr float NO_MAX = -1e30f;           // running maximum of a row that has seen nothing
+constexpr float NO_MAX = -3.402823466e38f;           // running maximum of a row that has seen nothing
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units; P stays below 2^8
 
 template <int D, int MT>

@@ -569,7 +569,9 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
  * a row that sees no key (kv_len_i < q_len_i, say) gets O = 0 and lse = -infinity.
  * Without `causal` a chunk's tokens see each other and the whole cache (the next chunk
  * of a video).  Query head h reads KV head h / (H / Hkv).  K, V and the probabilities
- * enter the products in `dtype`; sums, maxima and the accumulators are fp32.
+ * enter the products in `dtype`; sums, maxima and the accumulators are fp32.  Scores x_t
+ * stay below 1e9 in magnitude (a chunk's exponents are formed in one fused step, whose
+ * rounding is a common factor of a row up to there).
  * The sums of a tile that is cut among SMs are joined in a fixed order: equal calls on
  * equal plans give equal bits.  After XS_ERR_DEVICE_TIMEOUT plan again.
  */

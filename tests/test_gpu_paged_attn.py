@@ -149,6 +149,66 @@ def test_rising_scores_move_the_maximum(xs, q):
     assert (np.abs(lse.double().cpu().numpy() - z) <= 5e-4 + 2.0 ** -22 * np.abs(z)).all()
 
 
+@pytest.mark.parametrize("q,power", [(1, 55), (200, 12)], ids=["few", "chunk"])
+def test_scores_far_from_zero(xs, q, power):
+    """All scores alike far below zero (a row that sees keys, however low), and one key far above the
+    others: no overflow on the way, the mean and that key's values.  A chunk's exponents subtract the
+    rounded maximum from the exact product, so its scores stay below 1e9; a few tokens' may be any."""
+    c = pg.PagedCase([q], [700], 2, 2, 64, 16, seed=6)
+    big = 2.0 ** power
+    score = 64 * big * big / 8
+    c.q.fill_(big)
+    c.k.fill_(-big)
+    out, lse = _run(xs, c, causal=False)
+    v = np.mean(c.values[0], axis=0)
+    a = np.mean(np.abs(c.values[0]), axis=0)
+    assert (np.abs(out.double().cpu().numpy() - v) <= 2.0 ** -8 * (a + np.abs(v)) * 1.01 + 2e-4 * a).all()
+    # log2(e), ln 2 and their products in fp32: four steps; the logarithm of 700 is below one
+    assert ((lse.double() / -score - 1).abs() <= 2.0 ** -21).all()
+    c.k[c.table[0, 30].long(), 5] = big
+    out, lse = _run(xs, c, causal=False)
+    one = torch.from_numpy(c.values[0][30 * 16 + 5]).cuda()
+    # a chunk's only probability is a power of two near 1, rounded to the type: half a step, and the output's
+    assert ((out.double() - one).abs() <= (2.0 ** -8 * 2.02 if q > 1 else 0.0) * one.abs()).all()
+    assert ((lse.double() / score - 1).abs() <= 2.0 ** -21).all()
+
+
+def test_nan_rows_of_q_behind_the_last_sequence(xs):
+    """Padding rows may hold anything."""
+    for q in ([1, 1], [70, 30]):
+        c = pg.PagedCase(q, [300, 200], 6, 2, 128, 16, seed=6, extra_rows=40)
+        c.q[sum(q):] = float("nan")
+        out, lse = _run(xs, c)
+        c.check(out, lse, True, 0, c.D ** -0.5)
+
+
+@pytest.mark.parametrize("q", [1, 300])
+def test_workspace_of_more_sequences_and_used_again(xs, q):
+    """A workspace serves one step after the other, of other lengths, causal or not, few or many."""
+    ws = xs.PagedWorkspace(3, 4, 2, 128)
+    for kv, causal, window in (((500, 0, 90), True, 0), ((1, 3000, 700), False, 0), ((800, 900, 1000), True, 64)):
+        c = pg.PagedCase([q, 1, 0], [max(kv[0], q), kv[1], kv[2]], 4, 2, 128, 32, seed=q)
+        out, lse = _run(xs, c, causal, window, ws=ws)
+        c.check(out, lse, causal, window, c.D ** -0.5)
+
+
+def test_lengths_that_are_not_the_caches(xs):
+    """Nonsense on the device reads and writes nothing out of range; the next step is right."""
+    c = pg.PagedCase([2, 3], [60, 70], 4, 2, 64, 16, seed=1)
+    ws = xs.PagedWorkspace(2, 4, 2, 64)
+    guard = torch.full((c.T + 64, 4, 64), 5.0, dtype=c.dtype, device="cuda")
+    for cu, kv in (([5, 1, 3], [60, 70]), ([-7, 3, 9], [-1, 5000]), ([0, 2, 4000], [60, 20]), ([100, 101, 102], [10, 10]),
+                   ([0, 0, 0], [2 ** 20, 2 ** 20]), ([2, 5, 5], [0, 0])):
+        for max_q in (1, 100):
+            xs.xs_attn_paged_plan(torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                  torch.tensor(kv, dtype=torch.int32, device="cuda"), max_q, ws)
+            xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table, xs.XS_LAYOUT_CONTIGUOUS, [guard[32:32 + c.T]], 0.1, ws)
+            xs.xs_attn_get_device_error()
+            assert (guard[:32] == 5.0).all() and (guard[32 + c.T:] == 5.0).all()
+    out, lse = _run(xs, c, ws=ws)
+    c.check(out, lse, True, 0, c.D ** -0.5)
+
+
 def test_long_split_is_repeatable(xs):
     """One sequence cut over many SMs; ten calls on one plan give the same bits, and a plan made
     anew does too."""

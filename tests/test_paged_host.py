@@ -167,7 +167,14 @@ def test_append_refusals(xs):
     assert _passed(xs, f(qo=A(0)))
     assert _passed(xs, f(k=A(0) + 1024, v=A(0) + 1536, qo=A(0), qs=1024, ks=1024, vs=1024, os_=1024))   # a fused projection
     both = S3(2 * 16 * 256, 256, 128)
-    assert _passed(xs, f(vc=A(6) + 2 * 16 * 256, kst=both, vst=both))                                   # K and V in one buffer
+    assert _passed(xs, f(vc=A(6) + 2 * 16 * 256, kst=both, vst=both))                                   # one buffer, by pages
+    assert f(vc=A(6) + 2 * 16 * 256 - 16, kst=both, vst=both) == f(vc=A(6) + 16 * 256, kst=both, vst=both) == xs.XS_ERR_OVERLAP
+    tok = S3(16 * 512, 512, 128)
+    assert _passed(xs, f(vc=A(6) + 512, kst=tok, vst=tok)) and _passed(xs, f(kc=A(6) + 512, vc=A(6), kst=tok, vst=tok))
+    assert f(vc=A(6) + 256, kst=tok, vst=tok) == f(vc=A(6) + 16 * 1024, kst=tok, vst=tok) == xs.XS_ERR_OVERLAP
+    head = S3(16 * 512, 512, 256)
+    assert _passed(xs, f(vc=A(6) + 256, kst=head, vst=head)) and f(vc=A(6) + 512, kst=head, vst=head) == xs.XS_ERR_OVERLAP
+    assert f(vc=A(6) + 512, kst=tok, vst=S3(16 * 512, 512, 136)) == xs.XS_ERR_OVERLAP                   # unlike strides: not told apart
     assert _passed(xs, f(Hkv=1, ks=128, vs=128, kst=S3(2048, 128, 1), vst=S3(2048, 128, 0)))            # one head: its stride is not used
 
 
@@ -262,6 +269,15 @@ def test_python_refuses_host_tensors_and_wrong_types(xs):
         xs.xs_rope_fwd(x, pos, x, xs.Rope(128))
     with pytest.raises(TypeError):
         xs.xs_paged_step(*([pos] * 5), 16, *([pos] * 6))
+
+
+def test_copies_of_a_rope_stand_alone(xs):
+    import copy
+    import pickle
+    a = xs.Rope(128, 48, base=5e5, scaling=xs.XS_ROPE_LINEAR, factor=2.0)
+    want = bytes(a._struct)
+    for b in (copy.copy(a), copy.deepcopy(a), pickle.loads(pickle.dumps(a))):
+        assert b.ptr != a.ptr and bytes(b._struct) == want and ctypes.addressof(b._struct) == b.ptr
 
 
 # ------------------------------------------------------------------- division of work
