@@ -228,7 +228,7 @@ Tiling make_tiling(int G, int max_q, int sms) {
     x.t.least = 512;
     x.t.few_keys = 512;
     x.t.few_start_cost = 128;
-    x.t.few_least = 160;
+    x.t.few_least = 128;
     x.t.waves = 0;   // one tile per sequence and KV head: no keys to share in L2
     return x;
 }
