@@ -34,10 +34,8 @@ struct Sums {
     long long rows, need, give;
 };
 
-template <int THREADS>
-__device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sums x = v;
+__device__ __forceinline__ Sums warp_scan(Sums x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long r = __shfl_up_sync(0xffffffffu, x.rows, d), n = __shfl_up_sync(0xffffffffu, x.need, d),
@@ -48,28 +46,28 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total)
             x.give += g;
         }
     }
-    if (lane == 31) warp_sums[warp] = x;
+    return x;
+}
+
+// sums: [2 THREADS / 32 + 1].  One warp scans the warps' sums for all (32 warps each doing it for
+// itself spent 2 us in shuffles).
+template <int THREADS>
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* sums, Sums& total) {
+    constexpr int WARPS = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Sums x = warp_scan(v);
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
-    // lane w holds the sums of warp w
-    Sums s = lane < THREADS / 32 ? warp_sums[lane] : Sums{0, 0, 0}, before = s;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long r = __shfl_up_sync(0xffffffffu, before.rows, d), n = __shfl_up_sync(0xffffffffu, before.need, d),
-                        g = __shfl_up_sync(0xffffffffu, before.give, d);
-        if (lane >= d) {
-            before.rows += r;
-            before.need += n;
-            before.give += g;
-        }
+    if (warp == 0) {
+        const Sums s = lane < WARPS ? sums[lane] : Sums{0, 0, 0};
+        const Sums y = warp_scan(s);
+        if (lane < WARPS) sums[WARPS + lane] = Sums{y.rows - s.rows, y.need - s.need, y.give - s.give};
+        if (lane == 31) sums[2 * WARPS] = y;
     }
-    total.rows = __shfl_sync(0xffffffffu, before.rows, 31);
-    total.need = __shfl_sync(0xffffffffu, before.need, 31);
-    total.give = __shfl_sync(0xffffffffu, before.give, 31);
-    const long long wr = __shfl_sync(0xffffffffu, before.rows - s.rows, warp);
-    const long long wn = __shfl_sync(0xffffffffu, before.need - s.need, warp);
-    const long long wg = __shfl_sync(0xffffffffu, before.give - s.give, warp);
-    __syncthreads();   // warp_sums may be written again
-    return Sums{wr + x.rows - v.rows, wn + x.need - v.need, wg + x.give - v.give};
+    __syncthreads();
+    const Sums before = sums[WARPS + warp];
+    total = sums[2 * WARPS];
+    return Sums{before.rows + x.rows - v.rows, before.need + x.need - v.need, before.give + x.give - v.give};
 }
 
 // The request whose part [p[i], p[i+1]) of a prefix sum holds x (0 <= x < p[n]).
@@ -91,7 +89,7 @@ __device__ __forceinline__ int clamp_int(long long x) { return x > 0x7fffffffll 
 template <int THREADS, int K>
 __global__ void __launch_bounds__(THREADS) paged_step_kernel(const __grid_constant__ StepArgs a) {
     extern __shared__ int smem[];
-    __shared__ Sums warp_sums[THREADS / 32];
+    __shared__ Sums warp_sums[THREADS / 16 + 1];
     __shared__ int taken_max;
     const int n = a.n, tid = threadIdx.x;
     int* len = smem;           // [n] cached tokens (not negative)
@@ -201,15 +199,17 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const __grid_consta
         return a.table[static_cast<long long>(q) * a.width + (e - list - give[q])];
     };
     const int gtid = blockIdx.x * THREADS + tid, gsize = gridDim.x * THREADS;
-    // pages given back, behind the list's own
-    for (int e = list + gtid; e < avail; e += gsize) {
-        const int q = find(give, n, e - list);
-        a.free_pages[e] = a.table[static_cast<long long>(q) * a.width + (e - list - give[q])];
-    }
-    // pages taken, behind the request's own
-    for (int k = gtid; k < taken; k += gsize) {
-        const int q = find(need, n, k);
-        a.table[static_cast<long long>(q) * a.width + pages_of(len[q]) + (k - need[q])] = page_at(k);
+    // Pages given back, behind the list's own, then pages taken, behind the request's own: from the last
+    // thread on, which has no row (a thread that had all three took the steps one after the other)
+    const int given = avail - list;
+    for (int z = gsize - 1 - gtid; z < given + taken; z += gsize) {
+        if (z < given) {
+            const int q = find(give, n, z);
+            a.free_pages[list + z] = a.table[static_cast<long long>(q) * a.width + (z - give[q])];
+        } else {
+            const int k = z - given, q = find(need, n, k);
+            a.table[static_cast<long long>(q) * a.width + pages_of(len[q]) + (k - need[q])] = page_at(k);
+        }
     }
     // positions and slots
     for (long long r = gtid; r < a.rows; r += gsize) {
@@ -240,13 +240,14 @@ static cudaError_t launch(const StepArgs& a, int num_sms, cudaStream_t stream) {
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    const long long work = a.rows > a.n ? a.rows : a.n;
+    long long work = a.rows > a.n ? a.rows : a.n;
+    if (work < a.n_pages / 8) work = a.n_pages / 8;   // ended requests may give that many pages back
     long long grid = (work + THREADS - 1) / THREADS;
     if (grid > num_sms) grid = num_sms;
     return launch_overlapped(paged_step_kernel<THREADS, K>, dim3(static_cast<unsigned>(grid)), THREADS, smem, stream, a);
 }
 
-// One CTA per 512 or 1024 rows, at most one per SM: a single one for a decoding batch.
+// One CTA per 512 or 1024 rows, or pages that may come back, at most one per SM.
 cudaError_t launch_paged_step(const StepArgs& a, int num_sms, cudaStream_t stream) {
     if (a.n <= 512) return launch<512, 1>(a, num_sms, stream);
     if (a.n <= 2048) return launch<1024, 2>(a, num_sms, stream);
