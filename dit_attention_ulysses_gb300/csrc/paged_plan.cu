@@ -31,27 +31,43 @@ namespace {
 
 constexpr int PLAN_THREADS = 512;
 
-// Exclusive prefix sum over the block's threads, and the total.
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = v;
+// Sums over the threads before this one, and over all.
+struct Sums {
+    long long cost, tiles, kept;
+};
+
+__device__ __forceinline__ Sums warp_scan(Sums x) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+        const long long c = __shfl_up_sync(0xffffffffu, x.cost, d), t = __shfl_up_sync(0xffffffffu, x.tiles, d);
+        const int k = __shfl_up_sync(0xffffffffu, static_cast<int>(x.kept), d);
+        if (lane >= d) {
+            x.cost += c;
+            x.tiles += t;
+            x.kept += k;
+        }
     }
-    if (lane == 31) warp_sums[warp] = x;
+    return x;
+}
+
+// sums: [2 PLAN_THREADS / 32 + 1]
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* sums, Sums& total) {
+    constexpr int WARPS = PLAN_THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Sums x = warp_scan(v);
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
-    long long before = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-        const long long s = warp_sums[w];
-        if (w < warp) before += s;
-        sum += s;
+    if (warp == 0) {
+        const Sums s = lane < WARPS ? sums[lane] : Sums{0, 0, 0};
+        const Sums y = warp_scan(s);
+        if (lane < WARPS) sums[WARPS + lane] = Sums{y.cost - s.cost, y.tiles - s.tiles, y.kept - s.kept};
+        if (lane == 31) sums[2 * WARPS] = y;
     }
-    __syncthreads();   // warp_sums may be written again
-    total = sum;
-    return before + x - v;
+    __syncthreads();
+    const Sums before = sums[WARPS + warp];
+    total = sums[2 * WARPS];
+    return Sums{before.cost + x.cost - v.cost, before.tiles + x.tiles - v.tiles, before.kept + x.kept - v.kept};
 }
 
 // Last i in [0, n) with p[i] <= x.
@@ -73,7 +89,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     long long* tiles = prefix + a.n + 1;                  // [n + 1] tiles before it
     PagedPos* cut = reinterpret_cast<PagedPos*>(tiles + a.n + 1);      // [grid + 1]
     float* slot_cost = reinterpret_cast<float*>(cut + a.tile.grid + 1);   // [grid][waves]
-    __shared__ long long warp_sums[PLAN_THREADS / 32];
+    __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
     __shared__ int waves_min;
     const int tid = threadIdx.x;
 
@@ -94,19 +110,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         }
         const int mine = s.q_len > 0 ? paged_tiles(s, a.tile.tokens) : 0;
         const long long cost = mine > 0 ? a.Hkv * paged_cost(s, mine, keys_only, a.causal, a.window) : 0;
-        long long cost_all, kept_all, tiles_all;
-        const long long cost_at = block_scan(cost, warp_sums, cost_all);
-        const long long tiles_at = block_scan(static_cast<long long>(mine) * a.Hkv, warp_sums, tiles_all);
-        const long long kept_at = block_scan(mine > 0 ? 1 : 0, warp_sums, kept_all);
+        Sums all;
+        const Sums before = block_scan(Sums{cost, static_cast<long long>(mine) * a.Hkv, mine > 0 ? 1 : 0}, warp_sums, all);
         if (mine > 0) {
-            const int at = kept + static_cast<int>(kept_at);
-            prefix[at] = total + cost_at;
-            tiles[at] = all_tiles + tiles_at;
+            const int at = kept + static_cast<int>(before.kept);
+            prefix[at] = total + before.cost;
+            tiles[at] = all_tiles + before.tiles;
             a.work.seqs[at] = s;
         }
-        total += cost_all;
-        all_tiles += tiles_all;
-        kept += static_cast<int>(kept_all);
+        total += all.cost;
+        all_tiles += all.tiles;
+        kept += static_cast<int>(all.kept);
     }
     // Few keys per CTA: the time is latency, and short pieces of many CTAs beat long ones of some,
     // though their parts take longer to join
@@ -206,8 +220,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     if (tid < ranges)
         for (int w = 0; w < waves; ++w) spent += slot_cost[w * grid + tid];
     const long long mine = tid < ranges ? share - static_cast<long long>(spent) : 0;
-    long long shares;
-    const long long before = block_scan(mine > 0 ? mine : 0, warp_sums, shares);
+    Sums all;
+    const long long before = block_scan(Sums{mine > 0 ? mine : 0, 0, 0}, warp_sums, all).cost, shares = all.cost;
     if (tid <= ranges && ranges > 0) {
         PagedPos p{kept, 0, 0, 0};
         if (tid < ranges && shares > 0) {
