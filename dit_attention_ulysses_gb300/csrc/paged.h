@@ -91,19 +91,19 @@ struct PagedTiling {
 };
 constexpr int MAX_PAGED_WAVES = 64;
 
-// A sequence of the step (those with new tokens only).
-struct PagedSeq {
+// A sequence of the step (those with new tokens only).  (Aligned, here and below: 16-byte loads and stores.)
+struct alignas(16) PagedSeq {
     int q_start, q_len, kv_len;
     int index;      // row of the block table
 };
 
 // Position in the work: block k of tile `tile` of KV head `head` of sequence `seq`.
-struct PagedPos {
+struct alignas(16) PagedPos {
     int seq, head, tile, k;
 };
 
 // `slot` consecutive tiles that a CTA runs whole in one wave, from `pos` on.
-struct PagedSlot {
+struct alignas(16) PagedSlot {
     PagedPos pos;
     PagedSeq seq;   // the sequence of `pos`
 };
@@ -111,7 +111,7 @@ struct PagedSlot {
 // The part of the work that is cut, for one CTA: from `start` (inclusive) to `end` (exclusive), plus what it
 // needs to begin and to publish unfinished tiles.  A tile cut over CTAs c0 .. c1 is
 // merged by the last of them to finish, in the order of the CTAs.
-struct PagedRange {
+struct alignas(16) PagedRange {
     PagedPos start, end;
     PagedSeq first;       // the sequence of `start`
     int c0, c1;           // CTAs of the tile that `start` continues (start.k > 0)
@@ -121,7 +121,7 @@ struct PagedRange {
 static_assert(sizeof(PagedRange) == 64, "one range is one 64-byte line");
 
 // What a plan was made for; a launch with other arguments does nothing and reports it.
-struct PagedHeader {
+struct alignas(16) PagedHeader {
     int n_seqs;           // sequences with new tokens
     int ranges;           // CTAs with work
     int n, H, Hkv, D, tokens, block, grid, causal, window;

@@ -29,7 +29,8 @@
 namespace xs {
 namespace {
 
-constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_THREADS = 1024;
+constexpr int MAX_RANGES = 511;
 
 // Sums over the threads before this one, and over all.
 struct Sums {
@@ -85,10 +86,11 @@ __device__ __forceinline__ int find(const T* p, int n, long long x) {
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ PagedPlanArgs a) {
-    extern __shared__ long long prefix[];                 // [n + 1] cost before each kept sequence (all KV heads)
+    extern __shared__ __align__(16) long long prefix[];   // [n + 1] cost before each kept sequence (all KV heads)
     long long* tiles = prefix + a.n + 1;                  // [n + 1] tiles before it
     PagedPos* cut = reinterpret_cast<PagedPos*>(tiles + a.n + 1);      // [grid + 1]
-    float* slot_cost = reinterpret_cast<float*>(cut + a.tile.grid + 1);   // [grid][waves]
+    unsigned* slot_cost = reinterpret_cast<unsigned*>(cut + a.tile.grid + 1);   // [grid][waves]
+    __shared__ long long cut_key[MAX_RANGES + 1];         // order of a cut: twice its tile, plus one inside the tile
     __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
     __shared__ int waves_min;
     const int tid = threadIdx.x;
@@ -143,26 +145,27 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     // cuts fall on one block inside a tile (on a tile's start they may: a range is then empty).
     const int grid = a.tile.grid;
     const long long least = tile.least;
-    long long ranges = total / least;
+    long long ranges = total > 0 ? paged_div(total, least) : 0;
     if (ranges < all_tiles) ranges = all_tiles;
     if (ranges > grid) ranges = grid;
-    if (ranges > total / (2 * tile.block)) ranges = total / (2 * tile.block);
+    if (ranges * 2 * tile.block > total) ranges = total > 0 ? paged_div(total, 2 * tile.block) : 0;
     if (ranges < 1) ranges = kept > 0 ? 1 : 0;
 
     // ---- waves
     int waves = 0;
     long long per_slot = 1;
-    const long long share = ranges > 0 ? total / ranges : 0;   // of every CTA
-    if (a.tile.waves > 0 && ranges == grid && all_tiles >= grid) {
+    const long long share = ranges > 0 && total > 0 ? paged_div(total, ranges) : 0;   // of every CTA
+    // (with few tiles per KV head there is little to share, and a range runs them one after the other anyway)
+    if (a.tile.waves > 0 && ranges == grid && all_tiles >= grid && all_tiles >= 4ll * kept * a.Hkv) {
         // one tile per slot, more (up to 64) where there are more tiles than slots; what is left is cut
         const long long slots = static_cast<long long>(grid) * a.tile.waves;
-        per_slot = min((all_tiles + slots - 1) / slots, 64ll);
-        const int most = static_cast<int>(min(all_tiles / (grid * per_slot), static_cast<long long>(a.tile.waves)));
+        per_slot = min(paged_div(all_tiles + slots - 1, slots), 64ll);
+        const int most = static_cast<int>(min(paged_div(all_tiles, grid * per_slot), static_cast<long long>(a.tile.waves)));
         for (int i = tid; i < grid * most; i += PLAN_THREADS) {
             const int w = i / grid, c = i - w * grid;
             const long long first = (static_cast<long long>(w) * grid + c) * per_slot;
             PagedSlot slot;
-            double cost = 0.0;
+            long long cost = 0;
             long long left = per_slot, t = first;
             while (left > 0) {   // one turn per KV head that the slot touches
                 const int q = find(tiles, kept, t);
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
                 const long long x = t - tiles[q];
                 PagedPos p;
                 p.seq = q;
-                p.head = static_cast<int>(x / of_head);
+                p.head = static_cast<int>(paged_div(x, of_head));
                 p.tile = static_cast<int>(x - static_cast<long long>(p.head) * of_head);
                 p.k = 0;
                 const long long n = left < of_head - p.tile ? left : of_head - p.tile;
@@ -179,21 +182,27 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
                     slot.pos = p;
                     slot.seq = s;
                 }
-                cost += static_cast<double>(paged_cost(s, p.tile + n, tile, a.causal, a.window) -
-                                            paged_cost(s, p.tile, tile, a.causal, a.window));
+                if (per_slot == 1) {
+                    int lo, hi;
+                    paged_tile_keys(s, p.tile, tile.tokens, a.causal, a.window, lo, hi);
+                    cost = static_cast<long long>(hi) - lo + tile.start_cost;
+                } else {
+                    cost += paged_cost(s, p.tile + n, tile, a.causal, a.window) -
+                            paged_cost(s, p.tile, tile, a.causal, a.window);
+                }
                 t += n;
                 left -= n;
             }
             a.work.slots[static_cast<size_t>(c) * MAX_PAGED_WAVES + w] = slot;
-            slot_cost[i] = static_cast<float>(cost);
+            slot_cost[i] = static_cast<unsigned>(min(cost, 0xffffffffll));
         }
         __syncthreads();
         if (tid < grid) {
-            double sum = 0.0;
+            long long sum = 0;
             int w = 0;
             for (; w < most; ++w) {
                 sum += slot_cost[w * grid + tid];
-                if (sum > static_cast<double>(share - least)) break;
+                if (sum > share - least) break;
             }
             atomicMin(&waves_min, w);   // a minimum: the order does not matter
         }
@@ -210,41 +219,42 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             const int q = find(tiles, kept, t);
             const PagedSeq s = a.work.seqs[q];
             const int of_head = paged_tiles(s, a.tile.tokens);
-            const long long x = t - tiles[q], head = x / of_head;
+            const long long x = t - tiles[q], head = paged_div(x, of_head);
             x0 = prefix[q] + head * paged_cost(s, of_head, tile, a.causal, a.window) +
                  paged_cost(s, x - head * of_head, tile, a.causal, a.window);
         }
     }
     // grid <= PLAN_THREADS: one thread per CTA
-    double spent = 0.0;
+    long long spent = 0;
     if (tid < ranges)
         for (int w = 0; w < waves; ++w) spent += slot_cost[w * grid + tid];
-    const long long mine = tid < ranges ? share - static_cast<long long>(spent) : 0;
+    const long long mine = tid < ranges ? share - spent : 0;
     Sums all;
     const long long before = block_scan(Sums{mine > 0 ? mine : 0, 0, 0}, warp_sums, all).cost, shares = all.cost;
     if (tid <= ranges && ranges > 0) {
         PagedPos p{kept, 0, 0, 0};
         if (tid < ranges && shares > 0) {
-            // in proportion, so that rounding leaves nothing over
-            const long long rest = total - x0;
-            const long long x =
-                x0 + (tid == 0 ? 0 : waves == 0 ? total / ranges * tid + total % ranges * tid / ranges
-                                                : static_cast<long long>(static_cast<double>(before) / shares * rest));
+            // what the shares leave over (fewer than `ranges`, the remainder of the division) spread evenly
+            const long long over = total - x0 - shares;
+            const long long x = x0 + before + (over > 0 ? paged_div(over * tid, ranges) : 0);
             if (x < total) {
                 const int q = find(prefix, kept, x);
-                p = paged_locate(a.work.seqs[q], q, x - prefix[q], (prefix[q + 1] - prefix[q]) / a.Hkv, tile, a.Hkv, a.causal,
+                p = paged_locate(a.work.seqs[q], q, x - prefix[q], paged_div(prefix[q + 1] - prefix[q], a.Hkv), tile, a.Hkv, a.causal,
                                  a.window);
             }
         }
         cut[tid] = p;
+        long long id = tiles[p.seq];   // (a cut at a sequence's start may name the sequence after the last)
+        if (p.seq < kept) id += static_cast<long long>(p.head) * paged_tiles(a.work.seqs[p.seq], tile.tokens) + p.tile;
+        cut_key[tid] = 2 * id + (p.k > 0 ? 1 : 0);
     }
     __syncthreads();
-    // first cut at or past p
-    auto first_at = [&](const PagedPos& p) {
+    // first cut of at least this key
+    auto first_at = [&](long long key) {
         int lo = 0, hi = static_cast<int>(ranges);
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (paged_before(cut[mid], p))
+            if (cut_key[mid] < key)
                 lo = mid + 1;
             else
                 hi = mid;
@@ -257,16 +267,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             r.start = cut[c];
             r.end = cut[c + 1];
             r.first = a.work.seqs[r.start.seq < kept ? r.start.seq : 0];
-            PagedPos p = r.start;
-            if (p.k > 0) {
-                p.k = 1;
-                r.c0 = first_at(p) - 1;              // the CTA before the tile's first inner cut starts the tile
-                p.k = 0x7fffffff;
-                r.c1 = first_at(p) - 1;              // the CTA of its last inner cut ends it
+            if (r.start.k > 0) {
+                r.c0 = first_at(cut_key[c]) - 1;       // the CTA before the tile's first inner cut starts the tile
+                r.c1 = first_at(cut_key[c] + 1) - 1;   // the CTA of its last inner cut ends it
             }
-            p = r.end;
-            p.k = 0x7fffffff;
-            r.c1_last = r.end.k > 0 ? first_at(p) - 1 : c;
+            r.c1_last = r.end.k > 0 ? first_at(cut_key[c + 1] + 1) - 1 : c;
         } else {
             r.start = r.end = PagedPos{kept, 0, 0, 0};
         }
@@ -295,8 +300,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
-    static_assert(MAX_PAGED_WAVES * sizeof(float) * PLAN_THREADS <= 128 * 1024, "shared memory of the waves");
-    if (a.tile.grid >= PLAN_THREADS || a.tile.waves > MAX_PAGED_WAVES) return cudaErrorInvalidConfiguration;
+    if (a.tile.grid > MAX_RANGES || a.tile.waves > MAX_PAGED_WAVES) return cudaErrorInvalidConfiguration;
     const size_t smem = static_cast<size_t>(a.n + 1) * 16 + static_cast<size_t>(a.tile.grid + 1) * sizeof(PagedPos) +
                         static_cast<size_t>(a.tile.grid) * a.tile.waves * sizeof(float);
     if (smem > 47 * 1024) {

@@ -7,6 +7,12 @@
 
 namespace xs {
 
+// a / b for a >= 0, b > 0, in 32 bits where both fit (a 64-bit division takes several times as long).
+__host__ __device__ __forceinline__ long long paged_div(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
 __host__ __device__ __forceinline__ int paged_tiles(const PagedSeq& s, int tokens) {
     return (s.q_len + tokens - 1) / tokens;
 }
@@ -51,14 +57,14 @@ __host__ __device__ __forceinline__ long long paged_cost(const PagedSeq& s, long
             full = m - 1;
             hi = kv;          // the last, short one ends at the sequence's end
         }
-        long long z = base < 0 ? -base / R : 0;   // tiles whose end is not past 0: one key each
+        long long z = base < 0 ? paged_div(-base, R) : 0;   // tiles whose end is not past 0: one key each
         if (z > full) z = full;
         hi += z + (full - z) * base + R * (full * (full + 1) / 2 - z * (z + 1) / 2);
     }
     long long lo = 0;
     if (window > 0) {
         const long long b = base - window + 1;    // start of tile 0, before the clamp at 0
-        long long z = b <= 0 ? -b / R + 1 : 0;    // tiles that start at key 0
+        long long z = b <= 0 ? paged_div(-b, R) + 1 : 0;    // tiles that start at key 0
         if (z > m) z = m;
         lo = (m - z) * b + R * (m * (m - 1) / 2 - z * (z - 1) / 2);
     }
@@ -105,7 +111,7 @@ __host__ __device__ __forceinline__ PagedPos paged_locate(const PagedSeq& s, int
     p.seq = seq;
     p.head = p.tile = p.k = 0;
     if (seq_cost < 1) return p;   // lengths whose costs overflow 64 bits
-    const long long head = x / seq_cost;
+    const long long head = x < 0 ? 0 : paged_div(x, seq_cost);
     p.head = head < 0 ? 0 : head < Hkv ? static_cast<int>(head) : Hkv - 1;
     long long y = x - p.head * seq_cost;
     int lo = 0, hi = paged_tiles(s, g.tokens);   // cost(lo) <= y < cost(hi)

@@ -70,7 +70,7 @@ int main() {
             PagedPos p{kept, 0, 0, 0};
             if (c == 0) p.seq = 0;
             if (c > 0 && c < ranges) {
-                const long long x = total / ranges * c + total % ranges * c / ranges;
+                const long long x = total / ranges * c + total % ranges * c / ranges;   // (without waves)
                 int i = 0;
                 while (prefix[i + 1] <= x) ++i;
                 p = paged_locate(seqs[i], i, x - prefix[i], (prefix[i + 1] - prefix[i]) / Hkv, g, Hkv, causal, window);
