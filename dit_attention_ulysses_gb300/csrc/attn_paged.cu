@@ -29,6 +29,12 @@
 // the rest, so that all end together.  A tile cut
 // among CTAs goes to the workspace in parts; the last CTA to finish one joins the parts in
 // CTA order.  No CTA waits for another, so the launch is an ordinary one.
+//
+// Measured: 4608 tokens over 18432 keys, 24 heads: 700 us in short runs (1490 TFLOP/s, 77 %
+// of cuBLAS's burst; the dense kernel reaches 1600 on 18432^2), 740 at the power limit; two
+// chunks of 2048 over 16384, 32 / 8 heads: 700 and 750; any page size within 3 %.  A tile
+// costs some 3 us beside its blocks (first copies 2.6, last PV and epilogue 2.9, overlapped
+// in part), a cut tile 6 more (part 1.1, fence and count 1.8, join 1.2 per part).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
