@@ -15,7 +15,8 @@
  *
  * Layout conventions (all entry points):
  *   - bf16 tensors, row-major [B, S, H, D] with D fastest ("BSHD"), contiguous
- *     (xs_attn_varlen_fwd: packed [T, H, D]).
+ *     (xs_attn_varlen_fwd: packed [T, H, D]; the rotary and paged entry points:
+ *     bf16 or fp16, with strides of their own).
  *   - Attention is bidirectional (non-causal): O = softmax(Q K^T * scale) V per
  *     (b, h), no mask, no bias, no dropout, except in xs_attn_causal_fwd and,
  *     when asked, xs_attn_varlen_fwd.  Accumulation is fp32, the
@@ -26,7 +27,7 @@
  *
  * Ownership and synchronisation:
  *   - The caller owns every buffer and the stream.  The library allocates no
- *     device memory per call; on each device it keeps one error word and the
+ *     device memory per call; on each device it keeps its error words and the
  *     scratch array of xs_attn_fwd_balanced_noalloc (static device data).
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  Outputs are valid once the stream reaches the end of

@@ -240,6 +240,39 @@ def test_offsets_past_32_bits(xs):
         c.check(out, lse, True, 0, D ** -0.5)
 
 
+@pytest.mark.parametrize("most", [1, 40], ids=["one", "up_to_40"])
+def test_most_sequences(xs, most):
+    """8192 sequences, the limit, some without new tokens."""
+    r = np.random.default_rng(most)
+    q = r.integers(0, most, size=8192, endpoint=True)
+    kv = q + r.integers(0, 30, size=8192)
+    c = pg.PagedCase(q.tolist(), kv.tolist(), 2, 1, 64, 16, seed=most)
+    out, lse = _run(xs, c)
+    c.check(out, lse, True, 0, c.D ** -0.5)
+
+
+@pytest.mark.parametrize("q", [1, 70])
+def test_a_million_keys(xs, q):
+    """2^20 keys of one head: Q = 0 weighs every key alike, so a row is the mean of what it sees."""
+    D, page, keys = 64, 512, 1 << 20
+    kc, vc = (torch.randn((keys // page, page, 1, D), device="cuda").bfloat16() for _ in "kv")
+    table = torch.randperm(keys // page, device="cuda").int()[None]
+    cu, kv = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, q], [keys]))
+    query = torch.zeros((q, 1, D), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(query), torch.empty((q, 1), dtype=torch.float32, device="cuda")
+    ws = xs.PagedWorkspace(1, 1, 1, D)
+    xs.xs_attn_paged_plan(cu, kv, q, ws)
+    xs.xs_attn_paged_fwd(query, kc, vc, table, xs.XS_LAYOUT_CONTIGUOUS, [out], 0.1, ws, lse=lse)
+    assert xs.xs_attn_get_device_error() == xs.XS_OK
+    v = vc[table[0].long()].double().view(keys, D)
+    seen = torch.arange(keys - q + 1, keys + 1, device="cuda").double()
+    ref = torch.cumsum(v, 0)[keys - q:] / seen[:, None]
+    # probabilities are exactly 1: a sum of 2^20 terms in fp32 over 2^20, in hundreds of separate runs of
+    # at most a few thousand blocks' partial sums (each step 2^-24 of a partial sum below 5000)
+    assert ((out[:, 0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5).all()
+    assert ((lse[:, 0].double() - seen.log()).abs() <= 6e-5).all()
+
+
 def test_pages_out_of_range_read_as_zeros(xs):
     """Bad page numbers and a table too narrow for the sequence read as zeros: no fault."""
     H, D, page = 2, 64, 16
@@ -420,6 +453,32 @@ def test_serving_steps_in_a_graph(xs, max_q):
         s.step(new, graph.replay)
     for new in STEPS[::-1]:      # eager and replayed steps in turn
         s.step([a if a >= 0 else 0 for a in new], s.launch if sum(new) % 2 else graph.replay)
+
+
+def test_readme_example(xs):
+    """The README's serving step runs as printed, and computes what the entry points say."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    code = next(b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "xs_paged_step" in b)
+    ns = dict(torch=torch, xs=xs)
+    exec(code, ns)
+    assert xs.xs_attn_get_device_error() == xs.XS_OK
+    n, H, Hkv, D = (ns[k] for k in ("n", "H", "Hkv", "D"))
+    assert ns["cache_lens"].tolist() == [20] * n and int(ns["count"]) == ns["n_pages"] - 2 * n
+    # first tokens of the first and the last request: the whole attention of a prompt in 64 bits
+    q, k, v = (x.double().cpu().numpy() for x in (ns["q"], ns["k"], ns["v"]))
+    k, _ = pg.rope_reference(k, ns["positions"].cpu().numpy(), pg.frequencies(D), False)
+    k = torch.from_numpy(k).bfloat16().double().numpy()
+    for i in (0, n - 1):
+        rows = slice(20 * i, 20 * i + 20)
+        for h in (0, H - 1):
+            g = h // (H // Hkv)
+            ref, mass, _ = pg.attention_reference(q[rows, h], k[rows, g], v[rows, g], 20, True, 0, D ** -0.5)
+            got = ns["out"][rows, h].double().cpu().numpy()
+            u = pg.U[torch.bfloat16]     # k may round to the other neighbour: 4 u of a score, as in _Server.step
+            assert (np.abs(got - ref) <= u * (mass + np.abs(ref)) * 1.01 + (1.5e-4 + 4 * u) * mass).all()
 
 
 def test_two_streams_with_their_own_workspaces(xs):
