@@ -215,6 +215,8 @@ Tiling make_tiling(int G, int max_q, int sms) {
         x.t.whole = 12;
         x.t.least = 1024;
         x.t.waves = xs::MAX_PAGED_WAVES;
+        x.t.one_each = 1280;      // a cut tile costs as much time as ten blocks (8 us)
+        x.t.l2_bytes = 64 << 20;
         return x;
     }
     x.rows = need <= ROWS_SMALL ? ROWS_SMALL : ROWS_WIDE;

@@ -193,7 +193,7 @@ __device__ void producer_k_role(const CUtensorMap* tq, const CUtensorMap* tk, co
     PagedRange range = a.work.ranges[blockIdx.x];
     const PagedHeader& h = *a.work.header;
     const int n_seqs = h.n_seqs, per_slot = h.slot;
-    int waves = h.waves;
+    int waves = h.waves - (static_cast<int>(blockIdx.x) >= h.slot_ctas ? 1 : 0);
     if (h.n != a.n || h.H != a.H || h.Hkv != a.Hkv || h.D != D || h.tokens != tokens || h.block != BLOCK_N ||
         h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window) {
         if (lane == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, h.n, h.tokens, h.grid);

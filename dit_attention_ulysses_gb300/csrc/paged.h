@@ -86,6 +86,8 @@ struct PagedTiling {
     int whole;      // a tile of fewer blocks is not cut
     int least;      // cost per CTA from which on another CTA takes part
     int waves;      // whole tiles are dealt out in up to this many waves before the rest is cut (0: all is cut)
+    int one_each;   // (waves) all tiles run whole if no CTA's cost more than this beyond its share
+    int l2_bytes;   // (waves) keys and values beyond this do not stay in L2 for long
     // below few_keys keys per CTA on average (waves == 0) these replace start_cost and least
     int few_keys, few_start_cost, few_least;
 };
@@ -127,7 +129,8 @@ struct alignas(16) PagedHeader {
     int n, H, Hkv, D, tokens, block, grid, causal, window;
     int waves;            // slots of every CTA before its range
     int slot;             // tiles per slot
-    int unused[3];
+    int slot_ctas;        // CTAs that have a slot in the last wave
+    int unused[2];
 };
 constexpr int PAGED_MAGIC_SITE = 3;   // error record: the plan does not match the call
 

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     unsigned* slot_cost = reinterpret_cast<unsigned*>(cut + a.tile.grid + 1);   // [grid][waves]
     __shared__ long long cut_key[MAX_RANGES + 1];         // order of a cut: twice its tile, plus one inside the tile
     __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
-    __shared__ int waves_min;
+    __shared__ int waves_min, longest;
     const int tid = threadIdx.x;
 
     pdl_launch();
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     keys_only.start_cost = 0;
     long long total = 0, all_tiles = 0;
     int kept = 0;
+    if (tid == 0) longest = 0;
     for (int i0 = 0; i0 < a.n; i0 += PLAN_THREADS) {
         const int i = i0 + tid;
         PagedSeq s{0, 0, 0, i};
@@ -138,6 +139,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         tiles[kept] = all_tiles;
         waves_min = a.tile.waves;
     }
+    const long long keys = total, heads = static_cast<long long>(kept) * a.Hkv;
     total += all_tiles * tile.start_cost;
     __syncthreads();   // the prefix sums, and the sequences written by other threads of this CTA
     for (int i = tid; i <= kept; i += PLAN_THREADS) prefix[i] += tiles[i] * tile.start_cost;
@@ -154,16 +156,24 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     if (ranges < 1) ranges = kept > 0 ? 1 : 0;
 
     // ---- waves
-    int waves = 0;
+    // They pay where several tiles share a head's keys: four and more, or two if all keys together do not stay
+    // in L2 anyway (with few tiles and few keys a range runs a head's tiles one after the other).  The rest is
+    // cut, or runs whole as a last, partial wave, if that takes a CTA little longer than its share: a cut tile
+    // costs 8 us, and CTAs at other places of more keys than L2 holds wait for DRAM (8 x 64 new tokens over 8192
+    // keys, 32 / 8 heads, two tiles to a head: 87 us cut, 74 whole; 8 x 96: 142 and 101).
+    int waves = 0, slot_ctas = grid;
     long long per_slot = 1;
     const long long share = ranges > 0 && total > 0 ? paged_div(total, ranges) : 0;   // of every CTA
-    // (with few tiles per KV head there is little to share, and a range runs them one after the other anyway)
-    if (a.tile.waves > 0 && ranges == grid && all_tiles >= grid && all_tiles >= 4ll * kept * a.Hkv) {
+    const bool spilling = all_tiles > 0 && paged_div(keys, all_tiles) * heads * a.D * 4 > a.tile.l2_bytes;
+    const bool shared = all_tiles >= 4 * heads || (spilling && all_tiles >= 2 * heads);
+    if (a.tile.waves > 0 && kept > 0 && (shared || all_tiles <= grid)) {
         // one tile per slot, more (up to 64) where there are more tiles than slots; what is left is cut
         const long long slots = static_cast<long long>(grid) * a.tile.waves;
         per_slot = min(paged_div(all_tiles + slots - 1, slots), 64ll);
         const int most = static_cast<int>(min(paged_div(all_tiles, grid * per_slot), static_cast<long long>(a.tile.waves)));
-        for (int i = tid; i < grid * most; i += PLAN_THREADS) {
+        // per_slot == 1: all tiles, those of the partial wave too (all_tiles <= slots then)
+        const int extra = per_slot == 1 ? static_cast<int>(all_tiles - static_cast<long long>(most) * grid) : 0;
+        for (int i = tid; i < grid * most + extra; i += PLAN_THREADS) {
             const int w = i / grid, c = i - w * grid;
             const long long first = (static_cast<long long>(w) * grid + c) * per_slot;
             PagedSlot slot;
@@ -201,19 +211,29 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         __syncthreads();
         if (tid < grid) {
             long long sum = 0;
-            int w = 0;
-            for (; w < most; ++w) {
+            int fit = most;   // waves that leave this CTA below its share
+            for (int w = 0; w < most; ++w) {
                 sum += slot_cost[w * grid + tid];
-                if (sum > share - least) break;
+                if (sum > share - least && fit == most) fit = w;
             }
-            atomicMin(&waves_min, w);   // a minimum: the order does not matter
+            if (tid < extra) sum += slot_cost[most * grid + tid];
+            atomicMin(&waves_min, fit);   // a minimum and a maximum: the order does not matter
+            atomicMax(&longest, static_cast<int>(min(sum, 0x7fffffffll)));
         }
         __syncthreads();
-        waves = waves_min;
+        const long long rest = paged_div(share * extra, all_tiles);
+        const long long spare = max(static_cast<long long>(tile.one_each), shared && spilling ? 3 * rest / 8 : 0ll);
+        if (per_slot == 1 && most + (extra > 0 ? 1 : 0) <= a.tile.waves && longest <= share + spare) {
+            waves = most + (extra > 0 ? 1 : 0);
+            if (extra > 0) slot_ctas = extra;
+            ranges = 0;   // nothing is left to cut
+        } else if (shared && ranges == grid && all_tiles >= grid) {
+            waves = waves_min;
+        }
     }
     // ---- cuts: CTA c gets its share less what its waves cost, along the rest of the line
     long long x0 = 0;   // cost of the waves' tiles
-    if (waves > 0) {
+    if (waves > 0 && ranges > 0) {
         const long long t = static_cast<long long>(waves) * grid * per_slot;
         if (t >= all_tiles) {
             x0 = total;
@@ -295,6 +315,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         h.window = a.window;
         h.waves = waves;
         h.slot = static_cast<int>(per_slot);
+        h.slot_ctas = slot_ctas;
         *a.work.header = h;
     }
 }
