@@ -10,7 +10,8 @@
 //
 // Waves (tiles of 128 rows): before that, whole tiles are dealt out wave by wave, tile
 // w * grid + c (or the w * grid + c-th group of `slot` tiles) to CTA c, for as many waves
-// as leave every CTA below its share of the whole; the ranges make up the difference.
+// as leave every CTA below its share of the whole; the ranges make up the difference, or
+// the last tiles run whole too where that costs less than cutting them.
 // The CTAs then walk the keys of the same one or few KV heads at the same time, from the
 // same end, and share them in L2.  One range each over the whole line had every CTA at
 // another place of all heads' keys: 226 MB of them at 24 heads of 18432 keys, read at 9
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     // in L2 anyway (with few tiles and few keys a range runs a head's tiles one after the other).  The rest is
     // cut, or runs whole as a last, partial wave, if that takes a CTA little longer than its share: a cut tile
     // costs 8 us, and CTAs at other places of more keys than L2 holds wait for DRAM (8 x 64 new tokens over 8192
-    // keys, 32 / 8 heads, two tiles to a head: 87 us cut, 74 whole; 8 x 96: 142 and 101).
+    // keys, 32 / 8 heads, two tiles to a head: 87 us cut, 74 whole; 8 x 96: 142 and 101; 8 x 128, whose last
+    // wave is nearly empty: 131 and 135).
     int waves = 0, slot_ctas = grid;
     long long per_slot = 1;
     const long long share = ranges > 0 && total > 0 ? paged_div(total, ranges) : 0;   // of every CTA
