@@ -494,3 +494,27 @@ def test_two_streams_with_their_own_workspaces(xs):
     torch.cuda.synchronize()
     for c, o in zip(cases, outs):
         c.check(o, None, True, 0, 0.1)
+
+
+PLANS_IN_TURN = """
+import torch
+import dit_attention_ulysses_gb300 as xs
+for n in (1, 2, 31, 64, 100, 130, 131, 200, 300, 400, 420, 421, 422, 500, 1000, 2000, 2500, 2700, 3000, 5000, 8192):
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda") * 2
+    kv = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    for max_q in (1, 300):
+        xs.xs_attn_paged_plan(cu, kv, max_q, xs.PagedWorkspace(n, 8, 2, 64))
+torch.cuda.synchronize()
+assert xs.xs_attn_get_device_error() == xs.XS_OK
+print("planned")
+"""
+
+
+def test_plans_of_growing_batches_in_a_new_process(xs):
+    """The plan's shared memory grows with the sequences: each size launches, whatever ran before."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", PLANS_IN_TURN], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.strip() == "planned", r.stderr[-2000:]
