@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     __shared__ long long cut_key[MAX_RANGES + 1];         // order of a cut: twice its tile, plus one inside the tile
     __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
     __shared__ int waves_min, longest;
+    __shared__ unsigned short sorter[PLAN_THREADS];       // [warp][step of cost]
     const int tid = threadIdx.x;
 
     pdl_launch();
@@ -162,24 +163,25 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     // cut, or runs whole as a last, partial wave, if that takes a CTA little longer than its share: a cut tile
     // costs 8 us, and CTAs at other places of more keys than L2 holds wait for DRAM (8 x 64 new tokens over 8192
     // keys, 32 / 8 heads, two tiles to a head: 87 us cut, 74 whole; 8 x 96: 142 and 101; 8 x 128, whose last
-    // wave is nearly empty: 131 and 135).
+    // wave is nearly empty: 131 and 135).  Up to PLAN_THREADS tiles, one per thread, are tried whole whatever they
+    // share.
     int waves = 0, slot_ctas = grid;
     long long per_slot = 1;
     const long long share = ranges > 0 && total > 0 ? paged_div(total, ranges) : 0;   // of every CTA
     const bool spilling = all_tiles > 0 && paged_div(keys, all_tiles) * heads * a.D * 4 > a.tile.l2_bytes;
     const bool shared = all_tiles >= 4 * heads || (spilling && all_tiles >= 2 * heads);
-    if (a.tile.waves > 0 && kept > 0 && (shared || all_tiles <= grid)) {
+    if (a.tile.waves > 0 && kept > 0 && (shared || all_tiles <= PLAN_THREADS)) {
         // one tile per slot, more (up to 64) where there are more tiles than slots; what is left is cut
         const long long slots = static_cast<long long>(grid) * a.tile.waves;
         per_slot = min(paged_div(all_tiles + slots - 1, slots), 64ll);
         const int most = static_cast<int>(min(paged_div(all_tiles, grid * per_slot), static_cast<long long>(a.tile.waves)));
         // per_slot == 1: all tiles, those of the partial wave too (all_tiles <= slots then)
         const int extra = per_slot == 1 ? static_cast<int>(all_tiles - static_cast<long long>(most) * grid) : 0;
-        for (int i = tid; i < grid * most + extra; i += PLAN_THREADS) {
-            const int w = i / grid, c = i - w * grid;
-            const long long first = (static_cast<long long>(w) * grid + c) * per_slot;
+        const int last = most - (extra > 0 ? 0 : 1);   // the last wave of all tiles
+        // slot of `per_slot` tiles from tile `first` on, and its cost
+        auto describe = [&](long long first, long long& cost) {
             PagedSlot slot;
-            long long cost = 0;
+            cost = 0;
             long long left = per_slot, t = first;
             while (left > 0) {   // one turn per KV head that the slot touches
                 const int q = find(tiles, kept, t);
@@ -207,26 +209,94 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
                 t += n;
                 left -= n;
             }
+            return slot;
+        };
+        auto put = [&](const PagedSlot& slot, long long cost, int w, int c) {
             a.work.slots[static_cast<size_t>(c) * MAX_PAGED_WAVES + w] = slot;
-            slot_cost[i] = static_cast<unsigned>(min(cost, 0xffffffffll));
-        }
-        __syncthreads();
-        if (tid < grid) {
-            long long sum = 0;
-            int fit = most;   // waves that leave this CTA below its share
-            for (int w = 0; w < most; ++w) {
-                sum += slot_cost[w * grid + tid];
-                if (sum > share - least && fit == most) fit = w;
+            slot_cost[w * grid + c] = static_cast<unsigned>(min(cost, 0xffffffffll));
+        };
+        auto sum_up = [&]() {   // the longest CTA, and the waves that leave every CTA below its share
+            __syncthreads();
+            if (tid < grid) {
+                long long sum = 0;
+                int fit = most;
+                for (int w = 0; w < most; ++w) {
+                    sum += slot_cost[w * grid + tid];
+                    if (sum > share - least && fit == most) fit = w;
+                }
+                if (tid < extra) sum += slot_cost[most * grid + tid];
+                atomicMin(&waves_min, fit);   // a minimum and a maximum: the order does not matter
+                atomicMax(&longest, static_cast<int>(min(sum, 0x7fffffffll)));
             }
-            if (tid < extra) sum += slot_cost[most * grid + tid];
-            atomicMin(&waves_min, fit);   // a minimum and a maximum: the order does not matter
-            atomicMax(&longest, static_cast<int>(min(sum, 0x7fffffffll)));
-        }
-        __syncthreads();
+            __syncthreads();
+        };
         const long long rest = paged_div(share * extra, all_tiles);
         const long long spare = max(static_cast<long long>(tile.one_each), shared && spilling ? 3 * rest / 8 : 0ll);
-        if (per_slot == 1 && most + (extra > 0 ? 1 : 0) <= a.tile.waves && longest <= share + spare) {
-            waves = most + (extra > 0 ? 1 : 0);
+        bool whole = per_slot == 1 && last < a.tile.waves;
+        if (whole && all_tiles <= PLAN_THREADS) {
+            // Few tiles: by falling cost (in 32 steps of the greatest, stable), the waves in turn from the first and
+            // from the last CTA on, so that a CTA's long and short tiles even out.  24 ragged chunks of up to 9
+            // blocks a tile, two tiles to a CTA: 17 us, 23 as cut ranges; causal prompts of 1024 / 2048 / 4608
+            // tokens: 17.5 / 40 / 112 us, in the line's order with cuts 21 / 49 / 124.
+            long long cost = 0;
+            PagedSlot slot;
+            if (tid < all_tiles) {
+                slot = describe(tid, cost);
+                atomicMax(&longest, static_cast<int>(min(cost, 0x7fffffffll)));
+            }
+            sorter[tid] = 0;
+            __syncthreads();
+            const int warp = tid >> 5, lane = tid & 31;
+            const int key = tid < all_tiles ? 31 - static_cast<int>(paged_div(31 * min(cost, 0x7fffffffll), longest)) : 32;
+            const unsigned peers = __match_any_sync(0xffffffffu, key);
+            const int before = __popc(peers & ((1u << lane) - 1));
+            if (key < 32 && before == 0) sorter[warp * 32 + key] = static_cast<unsigned short>(__popc(peers));
+            __syncthreads();
+            if (warp == 0) {   // lane b: tiles before those of step b in warp w
+                int n = 0;
+                for (int w = 0; w < PLAN_THREADS / 32; ++w) n += sorter[w * 32 + lane];
+                int at = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, at, d);
+                    if (lane >= d) at += y;
+                }
+                at -= n;
+                for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+                    const int y = sorter[w * 32 + lane];
+                    sorter[w * 32 + lane] = static_cast<unsigned short>(at);
+                    at += y;
+                }
+                if (lane == 0) longest = 0;
+            }
+            __syncthreads();
+            if (tid < all_tiles) {
+                const int rank = sorter[warp * 32 + key] + before, w = rank / grid, i = rank - w * grid;
+                put(slot, cost, w, ((last - w) & 1) ? grid - 1 - i : i);
+            }
+            sum_up();
+            whole = longest <= share + spare;
+            if (!whole && shared) {
+                __syncthreads();
+                if (tid == 0) {
+                    longest = 0;
+                    waves_min = a.tile.waves;
+                }
+                if (tid < all_tiles) put(slot, cost, tid / grid, tid % grid);
+                sum_up();
+            }
+        } else {
+            for (int i = tid; i < grid * most + extra; i += PLAN_THREADS) {
+                const int w = i / grid, c = i - w * grid;
+                long long cost;
+                const PagedSlot slot = describe((static_cast<long long>(w) * grid + c) * per_slot, cost);
+                put(slot, cost, w, c);
+            }
+            sum_up();
+            whole = whole && longest <= share + spare;
+        }
+        if (whole) {
+            waves = last + 1;
             if (extra > 0) slot_ctas = extra;
             ranges = 0;   // nothing is left to cut
         } else if (shared && ranges == grid && all_tiles >= grid) {

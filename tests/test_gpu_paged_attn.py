@@ -95,6 +95,21 @@ def test_chunks(xs, case, dtype):
     assert out[rows:].isnan().all() and lse[rows:].isnan().all()
 
 
+@pytest.mark.parametrize("n", [38, 39, 76, 77, 130, 255, 256, 257])
+def test_many_ragged_tiles(xs, n):
+    """Four tiles per sequence: one to seven tiles per CTA, some CTAs with one fewer, and both sides of the
+    number up to which the plan sorts them."""
+    r = np.random.default_rng(n)
+    q_lens = r.integers(1, 41, size=n).tolist()
+    c = pg.PagedCase(q_lens, [q + int(r.integers(0, 400)) for q in q_lens], 8, 4, 64, 16, seed=n, extra_rows=1)
+    ws = xs.PagedWorkspace(n, 8, 4, 64)
+    out, lse = _run(xs, c, ws=ws, max_q=64)
+    c.check(out, lse, True, 0, c.D ** -0.5)
+    rows = sum(q_lens)
+    out2, lse2 = _run(xs, c, ws=ws, max_q=64)      # a plan of the same lengths is the same plan
+    assert torch.equal(out2[:rows], out[:rows]) and torch.equal(lse2[:rows], lse[:rows])
+
+
 @pytest.mark.parametrize("max_q", [1, 3, 8, 5000])
 def test_max_q_is_only_an_estimate(xs, max_q):
     c = pg.PagedCase([5, 150, 1], [400, 300, 90], 4, 2, 128, 16, seed=9)
