@@ -34,6 +34,8 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int MAX_RANGES = 511;
+constexpr int SORTED = 4 * PLAN_THREADS;      // tiles that a plan sorts, four per thread
+constexpr int SORT_ROWS = SORTED / 32;        // one per warp and turn
 
 // Sums over the threads before this one, and over all.
 struct Sums {
@@ -96,7 +98,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     __shared__ long long cut_key[MAX_RANGES + 1];         // order of a cut: twice its tile, plus one inside the tile
     __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
     __shared__ int waves_min, longest;
-    __shared__ unsigned short sorter[PLAN_THREADS];       // [warp][step of cost]
+    __shared__ __align__(16) unsigned short sorter[32 * SORT_ROWS];   // [step of cost][row]: tiles before a row's
+    __shared__ int step_tiles[32];
     const int tid = threadIdx.x;
 
     pdl_launch();
@@ -163,14 +166,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     // cut, or runs whole as a last, partial wave, if that takes a CTA little longer than its share: a cut tile
     // costs 8 us, and CTAs at other places of more keys than L2 holds wait for DRAM (8 x 64 new tokens over 8192
     // keys, 32 / 8 heads, two tiles to a head: 87 us cut, 74 whole; 8 x 96: 142 and 101; 8 x 128, whose last
-    // wave is nearly empty: 131 and 135).  Up to PLAN_THREADS tiles, one per thread, are tried whole whatever they
-    // share.
+    // wave is nearly empty: 131 and 135).  Up to SORTED tiles are tried whole whatever they share.
     int waves = 0, slot_ctas = grid;
     long long per_slot = 1;
     const long long share = ranges > 0 && total > 0 ? paged_div(total, ranges) : 0;   // of every CTA
     const bool spilling = all_tiles > 0 && paged_div(keys, all_tiles) * heads * a.D * 4 > a.tile.l2_bytes;
     const bool shared = all_tiles >= 4 * heads || (spilling && all_tiles >= 2 * heads);
-    if (a.tile.waves > 0 && kept > 0 && (shared || all_tiles <= PLAN_THREADS)) {
+    if (a.tile.waves > 0 && kept > 0 && (shared || all_tiles <= SORTED)) {
         // one tile per slot, more (up to 64) where there are more tiles than slots; what is left is cut
         const long long slots = static_cast<long long>(grid) * a.tile.waves;
         per_slot = min(paged_div(all_tiles + slots - 1, slots), 64ll);
@@ -211,10 +213,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             }
             return slot;
         };
-        auto put = [&](const PagedSlot& slot, long long cost, int w, int c) {
-            a.work.slots[static_cast<size_t>(c) * MAX_PAGED_WAVES + w] = slot;
-            slot_cost[w * grid + c] = static_cast<unsigned>(min(cost, 0xffffffffll));
-        };
         auto sum_up = [&]() {   // the longest CTA, and the waves that leave every CTA below its share
             __syncthreads();
             if (tid < grid) {
@@ -233,64 +231,114 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         const long long rest = paged_div(share * extra, all_tiles);
         const long long spare = max(static_cast<long long>(tile.one_each), shared && spilling ? 3 * rest / 8 : 0ll);
         bool whole = per_slot == 1 && last < a.tile.waves;
-        if (whole && all_tiles <= PLAN_THREADS) {
+        if (whole && all_tiles <= SORTED) {
             // Few tiles: by falling cost (in 32 steps of the greatest, stable), the waves in turn from the first and
             // from the last CTA on, so that a CTA's long and short tiles even out.  24 ragged chunks of up to 9
             // blocks a tile, two tiles to a CTA: 17 us, 23 as cut ranges; causal prompts of 1024 / 2048 / 4608
-            // tokens: 17.5 / 40 / 112 us, in the line's order with cuts 21 / 49 / 124.
-            long long cost = 0;
-            PagedSlot slot;
-            if (tid < all_tiles) {
-                slot = describe(tid, cost);
-                atomicMax(&longest, static_cast<int>(min(cost, 0x7fffffffll)));
+            // tokens: 17.5 / 40 / 112 us, in the line's order with cuts 21 / 49 / 124; four of 2048: 141 and 152.
+            const int warp = tid >> 5, lane = tid & 31, count = static_cast<int>(all_tiles);
+#pragma unroll 1
+            for (int i = tid; i < count; i += PLAN_THREADS) {
+                long long cost;
+                describe(i, cost);
+                slot_cost[i] = static_cast<unsigned>(min(cost, 0x7fffffffll));
+                atomicMax(&longest, static_cast<int>(slot_cost[i]));
             }
-            sorter[tid] = 0;
+            for (int i = tid; i < 32 * SORT_ROWS / 2; i += PLAN_THREADS) reinterpret_cast<unsigned*>(sorter)[i] = 0;
             __syncthreads();
-            const int warp = tid >> 5, lane = tid & 31;
-            const int key = tid < all_tiles ? 31 - static_cast<int>(paged_div(31 * min(cost, 0x7fffffffll), longest)) : 32;
-            const unsigned peers = __match_any_sync(0xffffffffu, key);
-            const int before = __popc(peers & ((1u << lane) - 1));
-            if (key < 32 && before == 0) sorter[warp * 32 + key] = static_cast<unsigned short>(__popc(peers));
+            constexpr int EACH = SORTED / PLAN_THREADS;
+            unsigned cost[EACH];
+            int place[EACH];   // first step and tiles before this one in its warp, then the slot
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) {
+                const int i = tid + j * PLAN_THREADS;
+                cost[j] = i < count ? slot_cost[i] : 0;
+                const int key = i < count ? 31 - static_cast<int>(paged_div(31ll * cost[j], longest)) : 32;
+                const unsigned peers = __match_any_sync(0xffffffffu, key);
+                const int before = __popc(peers & ((1u << lane) - 1));
+                if (key < 32 && before == 0)
+                    sorter[key * SORT_ROWS + j * 32 + warp] = static_cast<unsigned short>(__popc(peers));
+                place[j] = key << 8 | before;
+            }
             __syncthreads();
-            if (warp == 0) {   // lane b: tiles before those of step b in warp w
-                int n = 0;
-                for (int w = 0; w < PLAN_THREADS / 32; ++w) n += sorter[w * 32 + lane];
+            {   // warp b: step b, from row to row
+                unsigned short* const row = sorter + warp * SORT_ROWS + lane * EACH;
+                int n[EACH], sum = 0;
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) sum += n[j] = row[j];
+                int at = sum;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, at, d);
+                    if (lane >= d) at += y;
+                }
+                if (lane == 31) step_tiles[warp] = at;
+                at -= sum;
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) {
+                    row[j] = static_cast<unsigned short>(at);
+                    at += n[j];
+                }
+            }
+            __syncthreads();
+            if (warp == 0) {
+                const int n = step_tiles[lane];
                 int at = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const int y = __shfl_up_sync(0xffffffffu, at, d);
                     if (lane >= d) at += y;
                 }
-                at -= n;
-                for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-                    const int y = sorter[w * 32 + lane];
-                    sorter[w * 32 + lane] = static_cast<unsigned short>(at);
-                    at += y;
-                }
+                step_tiles[lane] = at - n;
                 if (lane == 0) longest = 0;
             }
             __syncthreads();
-            if (tid < all_tiles) {
-                const int rank = sorter[warp * 32 + key] + before, w = rank / grid, i = rank - w * grid;
-                put(slot, cost, w, ((last - w) & 1) ? grid - 1 - i : i);
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) {
+                if (tid + j * PLAN_THREADS >= count) continue;
+                const int key = place[j] >> 8;
+                const int rank = step_tiles[key] + sorter[key * SORT_ROWS + j * 32 + warp] + (place[j] & 255);
+                const int w = rank / grid, i = rank - w * grid;
+                place[j] = w * grid + (((last - w) & 1) ? grid - 1 - i : i);
+                slot_cost[place[j]] = cost[j];
             }
             sum_up();
             whole = longest <= share + spare;
-            if (!whole && shared) {
+            if (!whole && shared) {   // back to the line
                 __syncthreads();
                 if (tid == 0) {
                     longest = 0;
                     waves_min = a.tile.waves;
                 }
-                if (tid < all_tiles) put(slot, cost, tid / grid, tid % grid);
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) {
+                    const int i = tid + j * PLAN_THREADS;
+                    if (i < count) slot_cost[i] = cost[j];
+                }
                 sum_up();
+            }
+            if (whole) {   // the costs have done their work
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) {
+                    const int i = tid + j * PLAN_THREADS;
+                    if (i < count) slot_cost[i] = static_cast<unsigned>(place[j]);
+                }
+            }
+            if (whole || shared) {
+#pragma unroll 1
+                for (int i = tid; i < count; i += PLAN_THREADS) {
+                    const int at = whole ? static_cast<int>(slot_cost[i]) : i, w = at / grid;
+                    long long unused;
+                    a.work.slots[static_cast<size_t>(at - w * grid) * MAX_PAGED_WAVES + w] = describe(i, unused);
+                }
             }
         } else {
             for (int i = tid; i < grid * most + extra; i += PLAN_THREADS) {
                 const int w = i / grid, c = i - w * grid;
                 long long cost;
-                const PagedSlot slot = describe((static_cast<long long>(w) * grid + c) * per_slot, cost);
-                put(slot, cost, w, c);
+                a.work.slots[static_cast<size_t>(c) * MAX_PAGED_WAVES + w] = describe(i * per_slot, cost);
+                slot_cost[i] = static_cast<unsigned>(min(cost, 0xffffffffll));
             }
             sum_up();
             whole = whole && longest <= share + spare;
@@ -398,7 +446,7 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
     if (a.tile.grid > MAX_RANGES || a.tile.waves > MAX_PAGED_WAVES) return cudaErrorInvalidConfiguration;
     const size_t smem = static_cast<size_t>(a.n + 1) * 16 + static_cast<size_t>(a.tile.grid + 1) * sizeof(PagedPos) +
                         static_cast<size_t>(a.tile.grid) * a.tile.waves * sizeof(float);
-    if (smem > 40 * 1024) {   // (the kernel has 8 KB of its own beside these)
+    if (smem > 32 * 1024) {   // (the kernel has 14 KB of its own beside these)
         const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) return e;

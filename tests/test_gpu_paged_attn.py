@@ -95,9 +95,9 @@ def test_chunks(xs, case, dtype):
     assert out[rows:].isnan().all() and lse[rows:].isnan().all()
 
 
-@pytest.mark.parametrize("n", [38, 39, 76, 77, 130, 255, 256, 257])
+@pytest.mark.parametrize("n", [38, 39, 76, 77, 130, 257, 1024, 1025])
 def test_many_ragged_tiles(xs, n):
-    """Four tiles per sequence: one to seven tiles per CTA, some CTAs with one fewer, and both sides of the
+    """Four tiles per sequence: one to 27 tiles per CTA, some CTAs with one fewer, and both sides of the
     number up to which the plan sorts them."""
     r = np.random.default_rng(n)
     q_lens = r.integers(1, 41, size=n).tolist()
