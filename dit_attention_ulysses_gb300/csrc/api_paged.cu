@@ -202,7 +202,7 @@ struct Tiling {
     xs::PagedTiling t;
 };
 
-Tiling make_tiling(int G, int max_q, int sms) {
+Tiling make_tiling(int G, int D, int max_q, int sms) {
     Tiling x{};
     const int64_t need = static_cast<int64_t>(G) * max_q;
     if (need > ROWS_WIDE) {
@@ -214,6 +214,8 @@ Tiling make_tiling(int G, int max_q, int sms) {
         x.t.snap = 4;
         x.t.whole = 12;
         x.t.least = 1024;
+        x.t.join = 150;           // 40 new tokens over 20000 keys, 8 / 1 heads: 50 us at 0, 35 at 150, 42 at 500
+        x.t.join_rows = ROWS_TILE;
         x.t.waves = xs::MAX_PAGED_WAVES;
         x.t.one_each = 1280;      // a cut tile costs as much time as ten blocks (8 us)
         x.t.l2_bytes = 64 << 20;
@@ -228,6 +230,10 @@ Tiling make_tiling(int G, int max_q, int sms) {
     x.t.snap = 4;
     x.t.whole = 20;
     x.t.least = 512;
+    // 6 tokens over 19550 keys, 12 / 3 heads: 53 us at 0, 28 at 4, 35 at 12; one over 131072, 8 / 1: 43, 29, 28;
+    // 4 x 2 over 1527, 8 / 1: 12.2, 12.7, 13.3
+    x.t.join = 4;
+    x.t.join_rows = 512 / D;   // four channels to a thread
     x.t.few_keys = 512;
     x.t.few_start_cost = 128;
     x.t.few_least = 128;
@@ -482,7 +488,7 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
     a.D = D;
     a.causal = causal ? 1 : 0;
     a.window = window;
-    a.tile = make_tiling(H / Hkv, max_q, dev.sms).t;
+    a.tile = make_tiling(H / Hkv, D, max_q, dev.sms).t;
     const cudaError_t e = xs::launch_paged_plan(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
@@ -536,7 +542,7 @@ int xs_attn_paged_fwd(const xs_attn_paged_args* args, void* stream) {
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != XS_OK) return rc;
     if (g.workspace_bytes < paged_work(static_cast<char*>(g.workspace), n, D, dev.sms, &a.work)) return XS_ERR_WORKSPACE;
-    const Tiling tiling = make_tiling(H / Hkv, g.max_q, dev.sms);
+    const Tiling tiling = make_tiling(H / Hkv, D, g.max_q, dev.sms);
     a.q = g.q;
     a.table = g.block_table;
     a.lse = g.lse;

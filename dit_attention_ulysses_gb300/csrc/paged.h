@@ -85,6 +85,7 @@ struct PagedTiling {
     int snap;       // a cut leaves at least this many blocks on both sides
     int whole;      // a tile of fewer blocks is not cut
     int least;      // cost per CTA from which on another CTA takes part
+    int join, join_rows;   // time that a part takes in the join of its tile, in keys, per join_rows rows
     int waves;      // whole tiles are dealt out in up to this many waves before the rest is cut (0: all is cut)
     int one_each;   // (waves) all tiles run whole if no CTA's cost more than this beyond its share
     int l2_bytes;   // (waves) keys and values beyond this do not stay in L2 for long

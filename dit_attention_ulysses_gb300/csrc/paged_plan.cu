@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     unsigned* slot_cost = reinterpret_cast<unsigned*>(cut + a.tile.grid + 1);   // [grid][waves]
     __shared__ long long cut_key[MAX_RANGES + 1];         // order of a cut: twice its tile, plus one inside the tile
     __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
-    __shared__ int waves_min, longest;
+    __shared__ int waves_min, longest, tile_keys, tile_rows;
     __shared__ __align__(16) unsigned short sorter[32 * SORT_ROWS];   // [step of cost][row]: tiles before a row's
     __shared__ int step_tiles[32];
     const int tid = threadIdx.x;
@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     keys_only.start_cost = 0;
     long long total = 0, all_tiles = 0;
     int kept = 0;
-    if (tid == 0) longest = 0;
+    if (tid == 0) longest = tile_keys = tile_rows = 0;
+    __syncthreads();
     for (int i0 = 0; i0 < a.n; i0 += PLAN_THREADS) {
         const int i = i0 + tid;
         PagedSeq s{0, 0, 0, i};
@@ -127,6 +128,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             prefix[at] = total + before.cost;
             tiles[at] = all_tiles + before.tiles;
             a.work.seqs[at] = s;
+            int lo, hi;
+            paged_tile_keys(s, mine - 1, a.tile.tokens, a.causal, a.window, lo, hi);
+            atomicMax(&tile_keys, hi - lo);
+            atomicMax(&tile_rows, min(s.q_len, a.tile.tokens) * (a.H / a.Hkv));
         }
         total += all.cost;
         all_tiles += all.tiles;
@@ -154,7 +159,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     // cuts fall on one block inside a tile (on a tile's start they may: a range is then empty).
     const int grid = a.tile.grid;
     const long long least = tile.least;
-    long long ranges = total > 0 ? paged_div(total, least) : 0;
+    // A CTA's part of the longest tile takes time as its keys do, the join of that tile as the parts do: the sum
+    // is least at sqrt(join * keys) keys to a part
+    const int join = a.tile.join * ((tile_rows + a.tile.join_rows - 1) / a.tile.join_rows);
+    const long long part = static_cast<long long>(sqrtf(static_cast<float>(join) * static_cast<float>(tile_keys)));
+    long long ranges = total > 0 ? paged_div(total, max(least, part)) : 0;
     if (ranges < all_tiles) ranges = all_tiles;
     if (ranges > grid) ranges = grid;
     if (ranges * 2 * tile.block > total) ranges = total > 0 ? paged_div(total, 2 * tile.block) : 0;
