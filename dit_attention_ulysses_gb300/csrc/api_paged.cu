@@ -196,6 +196,7 @@ int encode_q(CUtensorMap* m, const void* base, int T, int Hkv, int G, int D, lon
 // ---- tiling of the paged attention, a function of the shape alone
 // rows 16 and 32: attn_paged_rows.cu; 128: attn_paged.cu
 constexpr int ROWS_SMALL = 16, ROWS_WIDE = 32, ROWS_TILE = 128;
+constexpr int ROWS_FEW = 24;   // packed rows of a sequence and KV head up to which the first is taken
 
 struct Tiling {
     int rows;   // packed query rows of a tile
@@ -205,7 +206,10 @@ struct Tiling {
 Tiling make_tiling(int G, int D, int max_q, int sms) {
     Tiling x{};
     const int64_t need = static_cast<int64_t>(G) * max_q;
-    if (need > ROWS_WIDE) {
+    // 32 rows, 32 / 8 heads, few-tokens kernel against the chunk kernel: 32 x 8192 keys 196 / 180 us, 8 x 8192 69 / 60,
+    // one of 500 keys 13.5 / 9.2 (but 62 / 75 for one of 131072 and a single KV head); 20 rows: 189 / 180, 64 / 60,
+    // one of 32768 keys 46 / 55; 16 rows: 177 / 179, 56 / 60
+    if (need > ROWS_FEW) {
         x.rows = ROWS_TILE;
         x.t.tokens = ROWS_TILE / G;
         x.t.block = 128;
