@@ -19,8 +19,8 @@
 //
 // Costs are arithmetic series (paged_walk.cuh), so nothing per tile is stored but the
 // waves' slots: one CTA scans the sequences, then its threads bisect for slots and cuts.
-// What bounds it is that chain, once per step: 7.3 us for a decoding batch, 11 .. 12 for
-// chunks with waves, 22 for 8192 sequences.
+// What bounds it is that chain, once per step: 8.1 us for a decoding batch, 10 for 24 short
+// chunks, 14 .. 16 for long ones, 23 for 8192 sequences.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     unsigned* slot_cost = reinterpret_cast<unsigned*>(cut + a.tile.grid + 1);   // [grid][waves]
     __shared__ long long cut_key[MAX_RANGES + 1];         // order of a cut: twice its tile, plus one inside the tile
     __shared__ Sums warp_sums[PLAN_THREADS / 16 + 1];
-    __shared__ int waves_min, longest, tile_keys, tile_rows;
+    __shared__ int waves_min, longest, most_keys, most_new;
     __shared__ __align__(16) unsigned short sorter[32 * SORT_ROWS];   // [step of cost][row]: tiles before a row's
     __shared__ int step_tiles[32];
     const int tid = threadIdx.x;
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     keys_only.start_cost = 0;
     long long total = 0, all_tiles = 0;
     int kept = 0;
-    if (tid == 0) longest = tile_keys = tile_rows = 0;
-    __syncthreads();
+    int my_keys = 0, my_new = 0;
+    if (tid == 0) longest = most_keys = most_new = 0;
     for (int i0 = 0; i0 < a.n; i0 += PLAN_THREADS) {
         const int i = i0 + tid;
         PagedSeq s{0, 0, 0, i};
@@ -128,14 +128,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             prefix[at] = total + before.cost;
             tiles[at] = all_tiles + before.tiles;
             a.work.seqs[at] = s;
-            int lo, hi;
-            paged_tile_keys(s, mine - 1, a.tile.tokens, a.causal, a.window, lo, hi);
-            atomicMax(&tile_keys, hi - lo);
-            atomicMax(&tile_rows, min(s.q_len, a.tile.tokens) * (a.H / a.Hkv));
+            my_keys = max(my_keys, s.kv_len);
+            my_new = max(my_new, s.q_len);
         }
         total += all.cost;
         all_tiles += all.tiles;
         kept += static_cast<int>(all.kept);
+    }
+    my_keys = __reduce_max_sync(0xffffffffu, my_keys);
+    my_new = __reduce_max_sync(0xffffffffu, my_new);
+    if ((tid & 31) == 0) {   // (the scans have synchronised; the threads meet again before these are read)
+        atomicMax(&most_keys, my_keys);
+        atomicMax(&most_new, my_new);
     }
     // Few keys per CTA: the time is latency, and short pieces of many CTAs beat long ones of some,
     // though their parts take longer to join
@@ -161,8 +165,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     const long long least = tile.least;
     // A CTA's part of the longest tile takes time as its keys do, the join of that tile as the parts do: the sum
     // is least at sqrt(join * keys) keys to a part
-    const int join = a.tile.join * ((tile_rows + a.tile.join_rows - 1) / a.tile.join_rows);
-    const long long part = static_cast<long long>(sqrtf(static_cast<float>(join) * static_cast<float>(tile_keys)));
+    const int rows = min(most_new, a.tile.tokens) * (a.H / a.Hkv);
+    const int join = a.tile.join * ((rows + a.tile.join_rows - 1) / a.tile.join_rows);
+    const float span = static_cast<float>(a.window > 0 ? min(most_keys, a.window) : most_keys);
+    const long long part = static_cast<long long>(sqrtf(static_cast<float>(join) * span));
     long long ranges = total > 0 ? paged_div(total, max(least, part)) : 0;
     if (ranges < all_tiles) ranges = all_tiles;
     if (ranges > grid) ranges = grid;
@@ -246,13 +252,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
             // blocks a tile, two tiles to a CTA: 17 us, 23 as cut ranges; causal prompts of 1024 / 2048 / 4608
             // tokens: 17.5 / 40 / 112 us, in the line's order with cuts 21 / 49 / 124; four of 2048: 141 and 152.
             const int warp = tid >> 5, lane = tid & 31, count = static_cast<int>(all_tiles);
+            int most_cost = 0;
 #pragma unroll 1
             for (int i = tid; i < count; i += PLAN_THREADS) {
                 long long cost;
                 describe(i, cost);
                 slot_cost[i] = static_cast<unsigned>(min(cost, 0x7fffffffll));
-                atomicMax(&longest, static_cast<int>(slot_cost[i]));
+                most_cost = max(most_cost, static_cast<int>(slot_cost[i]));
             }
+            most_cost = __reduce_max_sync(0xffffffffu, most_cost);
+            if (lane == 0) atomicMax(&longest, most_cost);
             for (int i = tid; i < 32 * SORT_ROWS / 2; i += PLAN_THREADS) reinterpret_cast<unsigned*>(sorter)[i] = 0;
             __syncthreads();
             constexpr int EACH = SORTED / PLAN_THREADS;
