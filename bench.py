@@ -36,7 +36,8 @@ DEFAULT_WORKLOAD = "video_large"
 SIDE_WORKLOAD = "image"   # timed as an extra key of the default line
 D64_WORKLOAD = "video_small_d64"   # the head-dimension-64 kernel, another extra key
 METRIC = "fused attn+A2A-layout TFLOP/s and % of GB300 dense BF16 peak; fused-store overhead %"
-KERNEL_SOURCES = ["dit_attention_ulysses_gb300/csrc/attn_fwd.cu", "dit_attention_ulysses_gb300/csrc/ptx.cuh",
+KERNEL_SOURCES = ["dit_attention_ulysses_gb300/csrc/attn_fwd.cu", "dit_attention_ulysses_gb300/csrc/attn_tile.cuh",
+                  "dit_attention_ulysses_gb300/csrc/device_wait.cuh", "dit_attention_ulysses_gb300/csrc/ptx.cuh",
                   "dit_attention_ulysses_gb300/csrc/kernels.h"]
 PROFILES = os.path.join(ROOT, "profiles")
 
