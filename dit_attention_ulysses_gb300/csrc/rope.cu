@@ -19,9 +19,9 @@
 // 8 sines and cosines once and walks the heads with them in registers, four heads
 // in flight.  Eight (D = 128) or four (D = 64) threads hold a head, so a load
 // instruction of a warp covers 128-byte segments.  75776 x 40 x 128: 230 us, 6.76 TB/s,
-// as fast as the card copies; 4608 x 24 x 128: 12.4 us from DRAM (8.3 at that rate, the
+// as fast as the card copies; 4608 x 24 x 128: 11.7 us from DRAM (8.3 at that rate, the
 // rest is the start and end of one wave); the append of 8192 tokens, 32 + 8 + 8 heads:
-// 36 us, 5.5 TB/s; a single small launch: 2.1 us.
+// 34 us, 5.85 TB/s; a single small launch: 2.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,7 +36,7 @@ namespace {
 
 constexpr int ROPE_THREADS = 128;
 constexpr int ROPE_UNROLL = 4;
-constexpr long long ROPE_LONG = 48ll << 20;   // bytes read, see launch_rope
+constexpr int ROPE_RESIDENT = 5;   // blocks that an SM holds (88 .. 96 registers)
 
 template <bool F16>
 __device__ __forceinline__ void widen(uint32_t w, float& lo, float& hi) {
@@ -92,9 +92,8 @@ __device__ __forceinline__ void turn(Chunk2& x, const float (&c)[8], const float
 
 // Block: 128 / units tokens (blockIdx.x) x one group of heads (blockIdx.y).
 // Heads are numbered q 0 .. H-1, then (APPEND) k H .. H+Hkv-1, v H+Hkv .. H+2Hkv-1.
-// LONG: no register limit (88 .. 96 instead of 64), see launch_rope.
-template <bool F16, bool INTERLEAVED, bool APPEND, bool LONG>
-__global__ void __launch_bounds__(ROPE_THREADS, LONG ? 1 : 8) rope_kernel(const __grid_constant__ RopeArgs g) {
+template <bool F16, bool INTERLEAVED, bool APPEND>
+__global__ void __launch_bounds__(ROPE_THREADS, 1) rope_kernel(const __grid_constant__ RopeArgs g) {
     pdl_launch();
     pdl_wait();
     const int units = g.D >> 4;
@@ -180,38 +179,35 @@ __global__ void __launch_bounds__(ROPE_THREADS, LONG ? 1 : 8) rope_kernel(const 
 
 }  // namespace
 
-template <bool F16, bool INTERLEAVED, bool APPEND>
-static cudaError_t launch(const RopeArgs& a, dim3 grid, bool is_long, cudaStream_t stream) {
-    return is_long ? launch_overlapped(rope_kernel<F16, INTERLEAVED, APPEND, true>, grid, ROPE_THREADS, 0, stream, a)
-                   : launch_overlapped(rope_kernel<F16, INTERLEAVED, APPEND, false>, grid, ROPE_THREADS, 0, stream, a);
-}
-
-// Heads per thread: all of them when the tokens alone fill the SMs (768 threads each),
-// fewer for short inputs, so that a single token still spreads its heads over threads.
-// Registers: below ROPE_LONG bytes 64 of them, which puts all blocks of a single wave side
-// by side (28 MB: 12.2 us against 13.2 without a limit); from there on no limit, whose
-// loads reach further ahead (128 MB: 44.7 us against 48.3; 776 MB: 231 against 236).
+// Heads per thread: as few as four (the loads in flight), at most twelve, and in between the fewest with which all
+// blocks run side by side; eight where they do not anyway, twelve again from four rounds on.  Few tokens spread
+// their heads further.  Append of 512 / 2048 / 8192 / 32768 tokens, 32 + 8 + 8 heads: 4.8 us (4 heads per thread; 5.4
+// with 12), 11.5 (12; 12.3 with 8), 34.4 (8; 36 with 48), 123.4 (12; 125.5 with 8); 64 tokens: 2.7 (2; 3.0 with 4);
+// 4608 x 24 x 128: 11.7 (12; 12.4 with 8).  With registers limited to 64, for eight blocks per SM: 6.1, 12.1, 38,
+// 131; 3.1; 12.0.
 cudaError_t launch_rope(const RopeArgs& args, int dtype, int layout, bool append, int num_sms, cudaStream_t stream) {
     RopeArgs a = args;
     const int units = a.D / 16, tokens = ROPE_THREADS / units;
     const int total = append ? a.H + 2 * a.Hkv : a.H;
-    const long long threads = static_cast<long long>(a.T) * units, want = static_cast<long long>(num_sms) * 768;
-    long long groups = (want + threads - 1) / threads;
-    if (groups > total) groups = total;
-    a.heads_per = static_cast<int>((total + groups - 1) / groups);
-    const dim3 grid(static_cast<unsigned>((a.T + tokens - 1) / tokens),
-                    static_cast<unsigned>((total + a.heads_per - 1) / a.heads_per));
-    const bool is_long = static_cast<long long>(a.T) * total * a.D * 2 >= ROPE_LONG;
-    const int k = dtype * 4 + layout * 2 + (append ? 1 : 0);
-    switch (k) {
-        case 0: return launch<false, false, false>(a, grid, is_long, stream);
-        case 1: return launch<false, false, true>(a, grid, is_long, stream);
-        case 2: return launch<false, true, false>(a, grid, is_long, stream);
-        case 3: return launch<false, true, true>(a, grid, is_long, stream);
-        case 4: return launch<true, false, false>(a, grid, is_long, stream);
-        case 5: return launch<true, false, true>(a, grid, is_long, stream);
-        case 6: return launch<true, true, false>(a, grid, is_long, stream);
-        default: return launch<true, true, true>(a, grid, is_long, stream);
+    const long long rows = (static_cast<long long>(a.T) + tokens - 1) / tokens;
+    auto blocks = [&](int heads) { return rows * ((total + heads - 1) / heads); };
+    int heads = 4;
+    while (heads < 12 && blocks(heads) > static_cast<long long>(num_sms) * ROPE_RESIDENT) heads += 4;
+    if (blocks(heads) > static_cast<long long>(num_sms) * ROPE_RESIDENT)
+        heads = blocks(heads) > 4ll * num_sms * ROPE_RESIDENT ? 12 : 8;
+    while (heads > 1 && blocks(heads) < num_sms / 2) heads /= 2;
+    a.heads_per = heads;
+    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>((total + heads - 1) / heads));
+    auto launch = [&](auto kernel) { return launch_overlapped(kernel, grid, ROPE_THREADS, 0, stream, a); };
+    switch (dtype * 4 + layout * 2 + (append ? 1 : 0)) {
+        case 0: return launch(rope_kernel<false, false, false>);
+        case 1: return launch(rope_kernel<false, false, true>);
+        case 2: return launch(rope_kernel<false, true, false>);
+        case 3: return launch(rope_kernel<false, true, true>);
+        case 4: return launch(rope_kernel<true, false, false>);
+        case 5: return launch(rope_kernel<true, false, true>);
+        case 6: return launch(rope_kernel<true, true, false>);
+        default: return launch(rope_kernel<true, true, true>);
     }
 }
 
