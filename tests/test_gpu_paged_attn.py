@@ -511,6 +511,33 @@ def test_two_streams_with_their_own_workspaces(xs):
         c.check(o, None, True, 0, 0.1)
 
 
+def test_two_graphs_share_a_workspace(xs):
+    """Each captured plan and attention replayed in turn, the two kernels and cut tiles among them."""
+    cases = [pg.PagedCase([1] * 6, [5000, 10, 900, 4000, 77, 1], 8, 2, 128, 16, seed=1),
+             pg.PagedCase([90, 0, 1, 40, 7, 200], [2500, 3, 1, 4000, 77, 230], 8, 2, 128, 32, seed=2)]
+    ws = xs.PagedWorkspace(6, 8, 2, 128)
+    outs = [torch.empty((c.T, 8, 128), dtype=c.dtype, device="cuda") for c in cases]
+
+    def launch(c, o):
+        xs.xs_attn_paged_plan(c.cu, c.kv, max(c.q_lens), ws)
+        xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table, xs.XS_LAYOUT_CONTIGUOUS, [o], 0.1, ws)
+
+    graphs = []
+    for c, o in zip(cases, outs):
+        launch(c, o)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            launch(c, o)
+    for turn in range(3):
+        for g, c, o in zip(graphs, cases, outs):
+            o.fill_(float("nan"))
+            g.replay()
+            c.check(o, None, True, 0, 0.1)
+    assert xs.xs_attn_get_device_error() == xs.XS_OK
+
+
 PLANS_IN_TURN = """
 import torch
 import dit_attention_ulysses_gb300 as xs
