@@ -19,7 +19,7 @@
 //
 // Costs are arithmetic series (paged_walk.cuh), so nothing per tile is stored but the
 // waves' slots: one CTA scans the sequences, then its threads bisect for slots and cuts.
-// What bounds it is that chain, once per step: 8.1 us for a decoding batch, 10 for 24 short
+// What bounds it is that chain, once per step: 8.5 us for a decoding batch, 10 for 24 short
 // chunks, 14 .. 16 for long ones, 23 for 8192 sequences.
 #include <cuda_runtime.h>
 
@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     // Few keys per CTA: the time is latency, and short pieces of many CTAs beat long ones of some,
     // though their parts take longer to join
     PagedTiling tile = a.tile;
-    if (a.tile.waves == 0 && total < static_cast<long long>(a.tile.grid) * a.tile.few_keys) {
+    const bool few = a.tile.waves == 0 && total < static_cast<long long>(a.tile.grid) * a.tile.few_keys;
+    if (few) {
         tile.start_cost = a.tile.few_start_cost;
         tile.least = a.tile.few_least;
     }
@@ -172,6 +173,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     long long ranges = total > 0 ? paged_div(total, max(least, part)) : 0;
     if (ranges < all_tiles) ranges = all_tiles;
     if (ranges > grid) ranges = grid;
+    // Few keys in tiles of about one length: parts that do not straddle tiles, in the whole batches that a join reads
+    // when there are many (1 x 6000 keys, 32 / 8 heads: 11.5 us with 304 parts, 10.5 with 256; 8 x 2048: 14.5 and
+    // 13.4; ragged batches lose 3 .. 10 % by it)
+    if (few && ranges >= 3 * all_tiles && all_tiles > 0 && 16.0f * span * all_tiles <= 17.0f * keys) {
+        const long long of_tile = ranges / all_tiles;
+        if (of_tile < 16) {
+            ranges = of_tile * all_tiles;
+        } else {
+            ranges = (ranges + 8 * all_tiles) / (16 * all_tiles) * (16 * all_tiles);
+            while (ranges > grid) ranges -= 16 * all_tiles;
+        }
+    }
     if (ranges * 2 * tile.block > total) ranges = total > 0 ? paged_div(total, 2 * tile.block) : 0;
     if (ranges < 1) ranges = kept > 0 ? 1 : 0;
 
