@@ -173,16 +173,21 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     long long ranges = total > 0 ? paged_div(total, max(least, part)) : 0;
     if (ranges < all_tiles) ranges = all_tiles;
     if (ranges > grid) ranges = grid;
-    // Few keys in tiles of about one length: parts that do not straddle tiles, in the whole batches that a join reads
-    // when there are many (1 x 6000 keys, 32 / 8 heads: 11.5 us with 304 parts, 10.5 with 256; 8 x 2048: 14.5 and
-    // 13.4; ragged batches lose 3 .. 10 % by it)
-    if (few && ranges >= 3 * all_tiles && all_tiles > 0 && 16.0f * span * all_tiles <= 17.0f * keys) {
-        const long long of_tile = ranges / all_tiles;
-        if (of_tile < 16) {
-            ranges = of_tile * all_tiles;
-        } else {
+    // Tiles of about one length: parts that do not straddle tiles, if that leaves few enough CTAs out.  Few tokens and
+    // few keys: always, in the whole batches that a join reads when there are many (1 x 6000 keys, 32 / 8 heads: 11.5
+    // us with 304 parts, 10.4 with 256; 8 x 2048: 14.5 and 13.2; ragged batches lose 3 .. 10 % by it).  Chunks: if no
+    // CTA gets more work than half a cut costs (64 tokens over 16384 keys, 32 / 8 heads: 36 .. 38 us with 152 parts,
+    // 33 .. 37.4 with 144; 100 over 30100, 16 / 2, two sequences: 59 and 57; but 1000 over 21000, 4 / 4: 48 and,
+    // with 128, 51)
+    if (all_tiles > 0 && ranges >= 2 * all_tiles && 16.0f * span * all_tiles <= 17.0f * keys) {
+        const long long even = ranges / all_tiles * all_tiles;
+        if (a.tile.waves > 0) {
+            if (paged_div(total, even) - paged_div(total, ranges) <= tile.one_each / 2) ranges = even;
+        } else if (few && ranges >= 16 * all_tiles) {
             ranges = (ranges + 8 * all_tiles) / (16 * all_tiles) * (16 * all_tiles);
             while (ranges > grid) ranges -= 16 * all_tiles;
+        } else if (few && ranges >= 3 * all_tiles) {
+            ranges = even;
         }
     }
     if (ranges * 2 * tile.block > total) ranges = total > 0 ? paged_div(total, 2 * tile.block) : 0;
