@@ -438,15 +438,31 @@ def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling
 
 # The checks below run on every call of a decoding loop, where they cost more than the
 # kernels: the accepted case takes a few attribute reads per tensor, and the reason of a
-# refusal is worked out only once there is one.
+# refusal is worked out only once there is one.  Where the native binding (csrc/binding.cpp)
+# has been built for this torch, it reads the tensors and makes the call itself; what it does
+# not accept (it returns None) goes through the checks here.
 _I32 = _I64 = _F32 = None
 _DTYPES = {}
 _current_device = _raw_stream = None
+_native = None
+
+
+def _bind_native(torch):
+    try:
+        from . import _binding
+    except ImportError:     # not built here, or for another torch
+        return None
+    if _binding.torch_version != torch.__version__.partition("+")[0]:
+        return None
+    names = ("xs_rope_fwd", "xs_rope_append_paged", "xs_paged_step", "xs_attn_paged_plan", "xs_attn_paged_fwd")
+    _binding.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in names))
+    return _binding
 
 
 def _bind_torch():
-    global _I32, _I64, _F32, _current_device, _raw_stream
+    global _I32, _I64, _F32, _current_device, _raw_stream, _native
     import torch
+    _native = _bind_native(torch)
     _DTYPES.update({torch.bfloat16: XS_DTYPE_BF16, torch.float16: XS_DTYPE_FP16})
     if torch.cuda.is_available():
         torch.cuda.init()
@@ -465,6 +481,10 @@ def _device():
 
 def _stream_of(stream, dev):
     return _raw_stream(dev) if stream is None else _stream_handle(stream)
+
+
+def _handle(stream):
+    return None if stream is None else _stream_handle(stream)
 
 
 def _dtype_of(t, name):
@@ -526,6 +546,10 @@ def xs_rope_fwd(x, positions, out, rope: Rope, grad: bool = False, stream=None) 
     """Rotary positions of ``x`` [T, H, D] (bf16 or fp16; rows may be slices of a wider matrix)
     into ``out`` (``out`` may be ``x``); ``grad=True`` applies the transposed map, which takes
     the gradient of ``out`` to the gradient of ``x``.  ``positions``: int32 [T]."""
+    if _native is not None:
+        code = _native.rope(x, positions, out, rope.ptr, rope.D, 1 if grad else 0, _handle(stream))
+        if code is not None:
+            return _check(code, "xs_rope_fwd") if code else None
     dev, D, dt = _device(), rope.D, x.dtype
     dtype = _dtype_of(x, "x")
     T, H, x_stride = _rows(x, "x", dt, D, dev)
@@ -542,6 +566,10 @@ def xs_rope_append_paged(q, k, v, positions, slots, q_out, k_cache, v_cache, rop
     """Rotate the new tokens' ``q`` [T, H, D] into ``q_out`` and their ``k`` [T, Hkv, D] into the
     slots of ``k_cache`` [n_pages, page_size, Hkv, D], and copy ``v`` into those of ``v_cache``.
     ``positions`` int32 [T], ``slots`` int64 [T] (outside the cache: not stored)."""
+    if _native is not None:
+        code = _native.append(q, k, v, positions, slots, q_out, k_cache, v_cache, rope.ptr, rope.D, _handle(stream))
+        if code is not None:
+            return _check(code, "xs_rope_append_paged") if code else None
     dev, D, dt = _device(), rope.D, q.dtype
     dtype = _dtype_of(q, "q")
     T, H, qs = _rows(q, "q", dt, D, dev)
@@ -570,6 +598,11 @@ def xs_paged_step(cache_lens, new_lens, block_table, free_pages, free_count, pag
     ended requests (``new_lens < 0``) back to the list, and ``kv_lens``, ``cu_q``, ``positions``,
     ``slots``, ``free_count_out`` and ``status`` (include/xsattn.h has the rules).  All int32
     device tensors, ``slots`` int64; ``free_pages`` has one entry per page of the cache."""
+    if _native is not None:
+        code = _native.step(cache_lens, new_lens, block_table, free_pages, free_count, page_size, kv_lens, cu_q,
+                            positions, slots, free_count_out, status, _handle(stream))
+        if code is not None:
+            return _check(code, "xs_paged_step") if code else None
     dev, i32 = _device(), _I32
     if block_table.dim() != 2 or block_table.dtype is not i32 or not block_table.is_contiguous():
         raise TypeError(f"block_table must be a contiguous {i32} tensor [n, width]")
@@ -606,6 +639,7 @@ class PagedWorkspace:
         self.nbytes = xs_attn_paged_workspace_bytes(n, H, Hkv, D)
         self._buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.ptr = (self._buf.data_ptr() + 255) & ~255
+        self._dims = (n, H, Hkv, D, self.ptr, self.nbytes)
         self.planned = None   # (max_q, causal, window) of the plan
 
     def __reduce__(self):   # a copy is a new workspace without a plan
@@ -617,11 +651,16 @@ def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, cau
     """Divide the attention of a step among the SMs: ``cu_q`` int32 [n + 1], ``kv_lens`` int32 [n]
     on the device; ``max_q`` an upper estimate of a sequence's new tokens; ``causal`` and
     ``window`` (0: none) as the attention is to use them."""
-    w, dev = workspace, _device()
-    _on_device(w._buf, "workspace", dev)
-    causal = 1 if causal else 0
-    code = lib.xs_attn_paged_plan(_vec(cu_q, "cu_q", _I32, w.n + 1, dev), _vec(kv_lens, "kv_lens", _I32, w.n, dev), w.n,
-                                  w.H, w.Hkv, w.D, max_q, causal, window, w.ptr, w.nbytes, _stream_of(stream, dev))
+    w, causal = workspace, 1 if causal else 0
+    code = None
+    if _native is not None:
+        code = _native.plan(cu_q, kv_lens, max_q, w._buf, w._dims, causal, window, _handle(stream))
+    if code is None:
+        dev = _device()
+        _on_device(w._buf, "workspace", dev)
+        code = lib.xs_attn_paged_plan(_vec(cu_q, "cu_q", _I32, w.n + 1, dev), _vec(kv_lens, "kv_lens", _I32, w.n, dev),
+                                      w.n, w.H, w.Hkv, w.D, max_q, causal, window, w.ptr, w.nbytes,
+                                      _stream_of(stream, dev))
     if code:
         _check(code, "xs_attn_paged_plan")
     w.planned = (max_q, causal, window)
@@ -633,6 +672,11 @@ def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale
     each, any strides with D contiguous) as ``workspace`` plans it.  ``block_table`` int32 [n, width];
     ``layout`` XS_LAYOUT_A2A (P shards [T/P, H, D]), XS_LAYOUT_CONTIGUOUS (one [T, H, D] tensor) or
     XS_LAYOUT_HEADS (P head shards [T, H/P, D]); ``lse``: fp32 [T, H] or None."""
+    if _native is not None:
+        code = _native.attn(q, k_cache, v_cache, block_table, layout, outs, scale, workspace._buf, workspace._dims,
+                            workspace.planned, lse, _handle(stream))
+        if code is not None:
+            return _check(code, "xs_attn_paged_fwd") if code else None
     w, dev, dt = workspace, _device(), q.dtype
     if w.planned is None:
         raise ValueError("xs_attn_paged_fwd: the workspace has no plan (call xs_attn_paged_plan first)")

@@ -3,12 +3,18 @@
 The translation units are compiled in parallel and linked into one shared
 library next to this file.  Only nvcc and the CUDA runtime are needed; no
 PyTorch headers are involved (the C ABI takes plain pointers).
+
+Beside it, where Python's and PyTorch's headers are there, g++ compiles the
+binding of the serving calls (_binding.so, csrc/binding.cpp); without it their
+arguments are checked in Python.
 """
 from __future__ import annotations
 
 import os
+import importlib.util
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,11 +56,49 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def _binding_headers() -> str | None:
+    """PyTorch's directory, if its headers and Python's are installed."""
+    spec = importlib.util.find_spec("torch")
+    torch_dir = os.path.dirname(spec.origin) if spec and spec.origin else ""
+    found = [os.path.join(torch_dir, "include", "torch", "csrc", "autograd", "python_variable.h"),
+             os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+    return torch_dir if torch_dir and all(map(os.path.exists, found)) and shutil.which("g++") else None
+
+
+def build_binding(force: bool = False) -> str | None:
+    """Compile the binding (if stale) and return its path; None without the headers."""
+    torch_dir = _binding_headers()
+    if torch_dir is None:
+        return None
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = [src, os.path.join(CSRC, "..", "..", "include", "xsattn.h"), __file__,
+            os.path.join(torch_dir, "version.py")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps
+                                                     if os.path.exists(d)):
+        return BINDING
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w", src, "-o", tmp]
+    for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+              os.path.join(cuda_home(), "include")):
+        cmd += ["-I", d]
+    cmd += ["-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
     """Compile (if stale) and return the path of libxsattn.so (or of a variant)."""
     defines, lib_name, build_dir = VARIANTS[variant]
     LIB = os.path.join(HERE, lib_name)
     if not force and not _stale(LIB):
+        build_binding()
         return LIB
     bdir = os.path.join(HERE, build_dir)
     os.makedirs(bdir, exist_ok=True)
@@ -70,8 +114,10 @@ def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose:
         for _, log in results:
             if log:

@@ -560,3 +560,50 @@ def test_plans_of_growing_batches_in_a_new_process(xs):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", PLANS_IN_TURN], cwd=root, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and r.stdout.strip() == "planned", r.stderr[-2000:]
+
+
+def test_native_binding_and_python_checks_make_the_same_calls(xs, monkeypatch):
+    """One step through the binding and through the checks in Python: the same bits, and the same refusals."""
+    xs._device()
+    if xs._native is None:
+        pytest.skip("the binding needs PyTorch's and Python's headers")
+    seen = []
+
+    class Spy:
+        def __getattr__(self, name):
+            def f(*args):
+                seen.append((name, getattr(native, name)(*args)))
+                return seen[-1][1]
+            return f
+
+    native, outs = xs._native, []
+    side = torch.cuda.Stream()
+    for binding in (Spy(), None):
+        monkeypatch.setattr(xs, "_native", binding)
+        s = _Server(xs, 4, 8, 2, 128, 16, 40, 100, seed=1)
+        for new in STEPS:
+            s.step(new, s.launch)
+        c = pg.PagedCase([90, 1, 7], [300, 200, 7], 8, 2, 128, 16, seed=2, q_pad=3, table_pad=2)
+        ws, lse = xs.PagedWorkspace(3, 8, 2, 128), torch.empty((c.T, 8), device="cuda")
+        shards = [torch.empty((c.T, 4, 128), dtype=c.dtype, device="cuda") for _ in range(2)]
+        turned = torch.empty((c.T, 8, 128), dtype=c.dtype, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        xs.xs_attn_paged_plan(c.cu, c.kv, 90, ws, stream=side)
+        xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table, xs.XS_LAYOUT_HEADS, shards, 0.1, ws, lse=lse, stream=side.cuda_stream)
+        xs.xs_rope_fwd(c.q, torch.arange(c.T, device="cuda").int(), turned, xs.Rope(128, 64), grad=True)
+        torch.cuda.synchronize()
+        outs.append([*shards, lse, turned])
+        with pytest.raises(TypeError, match="contiguous"):
+            xs.xs_attn_paged_plan(torch.zeros(8, dtype=torch.int32, device="cuda")[::2], c.kv, 90, ws)
+        with pytest.raises(TypeError, match="shapes do not match|shape"):
+            xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table, xs.XS_LAYOUT_HEADS, shards[:1], 0.1, ws)
+        with pytest.raises(TypeError, match="current device"):
+            xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table.cpu(), xs.XS_LAYOUT_HEADS, shards, 0.1, ws)
+        with pytest.raises(xs.XsError) as e:
+            xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table, xs.XS_LAYOUT_HEADS, shards, -1.0, ws)
+        assert e.value.code == xs.XS_ERR_SCALE
+        with pytest.raises(ValueError, match="no plan"):
+            xs.xs_attn_paged_fwd(c.q, c.k, c.v, c.table, xs.XS_LAYOUT_HEADS, shards, 0.1, xs.PagedWorkspace(3, 8, 2, 128))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    taken = {name for name, code in seen if code == xs.XS_OK}
+    assert taken == {"rope", "append", "step", "plan", "attn"}
