@@ -1,3 +1,4 @@
+import glob
 import os
 import sys
 
@@ -8,7 +9,27 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 
+# Calls with made-up addresses: the accepted ones would reach a GPU if the process saw one.
+NO_GPU_FILES = ("test_abi_host.py", "test_paged_host.py")
+
+
+def _sees_a_gpu():
+    return os.environ.get("CUDA_VISIBLE_DEVICES") != "" and bool(glob.glob("/dev/nvidia[0-9]*"))
+
+
+def pytest_collection_modifyitems(config, items):
+    """Those files run in processes that see no GPU only: not beside GPU tests on a machine with one
+    (``-m "not gpu"`` hides it)."""
+    if _sees_a_gpu():
+        out = [i for i in items if os.path.basename(str(i.fspath)) in NO_GPU_FILES and not i.get_closest_marker("gpu")]
+        if out:
+            config.hook.pytest_deselected(items=out)
+            items[:] = [i for i in items if i not in out]
+
+
 def pytest_configure(config):
+    if config.option.markexpr.strip() == "not gpu":     # before anything starts CUDA
+        os.environ["CUDA_VISIBLE_DEVICES"] = ""
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a); run with -m gpu")
     config.addinivalue_line("markers", "slow: long-running CPU oracle case")
 

@@ -1,5 +1,5 @@
-"""The paged-cache entry points without a GPU: refusals of the C ABI (fake pointers, nothing
-is dereferenced) and of the Python binding, the frequencies of xs_rope_init, the division of
+"""The paged-cache entry points without a GPU (a process that sees one does not run this file):
+refusals of the C ABI (fake pointers, nothing is dereferenced) and of the Python binding, the frequencies of xs_rope_init, the division of
 the attention's work (host program over the kernels' own geometry), and the references of the
 GPU tests on hand-worked cases."""
 import ctypes
@@ -24,6 +24,9 @@ def xs():
     from conftest import build_library
     build_library()
     import dit_attention_ulysses_gb300 as xs
+    # the calls that pass the checks below must not reach a GPU with their made-up addresses
+    nbytes = ctypes.c_size_t(0)
+    assert xs.lib.xs_attn_paged_workspace_bytes(1, 1, 1, 64, ctypes.byref(nbytes)) != xs.XS_OK, "run this file without a GPU"
     return xs
 
 
@@ -32,7 +35,7 @@ def A(i):
     return 0x10_0000_0000 * (i + 1)
 
 
-REFUSED_LATER = ("XS_ERR_CUDA", "XS_ERR_UNSUPPORTED_DEVICE", "XS_OK")   # the checks passed
+REFUSED_LATER = ("XS_ERR_CUDA", "XS_ERR_UNSUPPORTED_DEVICE")   # the checks passed, and there is no GPU
 
 
 def _passed(xs, code):
@@ -269,6 +272,25 @@ def test_python_refuses_host_tensors_and_wrong_types(xs):
         xs.xs_rope_fwd(x, pos, x, xs.Rope(128))
     with pytest.raises(TypeError):
         xs.xs_paged_step(*([pos] * 5), 16, *([pos] * 6))
+
+
+def test_native_binding_leaves_host_tensors_to_python(xs):
+    xs._device()
+    if xs._native is None:
+        from importlib import util
+        assert util.find_spec("torch") is None or xs.__file__ is None or not os.path.exists(
+            os.path.join(os.path.dirname(xs.__file__), "_binding.so"))
+        return
+    x, pos = torch.zeros((4, 2, 64), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    rope, n = xs.Rope(64), xs._native
+    assert n.rope(x, pos, x, rope.ptr, 64, 0, None) is None
+    assert n.rope(x, pos) is None and n.rope(None, 1, 2, 3, 4, 5, 6) is None         # too few; not tensors
+    assert n.step(*([pos] * 5), 16, *([pos] * 6), None) is None
+    assert n.plan(pos, pos, 1, pos, (1, 1, 1, 64, 0, 0), 1, 0, None) is None
+    assert n.append(x, x, x, pos, pos, x, x, x, rope.ptr, 64, None) is None
+    assert n.attn(x, x, x, pos, 1, [x], 0.1, pos, (), (1, 1, 0), None, None) is None
+    with pytest.raises(ValueError):
+        n.bind(1, 2, 3, 4, 0)
 
 
 def test_copies_of_a_rope_stand_alone(xs):
