@@ -218,8 +218,9 @@ Tiling make_tiling(int G, int D, int max_q, int sms) {
         x.t.snap = 4;
         x.t.whole = 12;
         x.t.least = 1024;
-        x.t.join = 150;           // 40 new tokens over 20000 keys, 8 / 1 heads: 50 us at 0, 35 at 150, 42 at 500
-        x.t.join_rows = ROWS_TILE;
+        // (per 32 rows) 40 new tokens over 20000 keys, 8 / 1 heads: 50 us at 0, 35 at 38, 42 at 125
+        x.t.join = 38;
+        x.t.join_rows = 32;
         x.t.waves = xs::MAX_PAGED_WAVES;
         x.t.one_each = 1280;      // a cut tile costs as much time as ten blocks (8 us)
         x.t.l2_bytes = 64 << 20;

@@ -503,6 +503,70 @@ __device__ __forceinline__ float log_sum(float m, float l) {
     return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
 }
 
+// The join of a tile of up to 128 / SHARE rows: SHARE warps for every 16 rows, each with a share of the channels of
+// both half rows and SHARE parts in flight, in CTA order (past the last: the last, at weight 0).
+template <int D, bool F16, int SHARE>
+__device__ __forceinline__ bool join_few_rows(const PagedAttnArgs& a, const Piece& d, int warp) {
+    constexpr int CHUNKS = D / 8 / SHARE;   // four channels each
+    constexpr int SOFTMAX_THREADS = NUM_SOFTMAX_WARPS * 32;
+    const int lane = static_cast<int>(lane_id());
+    const int owner = (warp & 4) | (warp & (4 / SHARE - 1)), sub = (warp & 3) / (4 / SHARE);
+    const int row = (owner & 3) * 32 + (owner >> 2) * 16 + (lane & 15);
+    int token, head;
+    uint16_t* const dst = dest_row(a, d, row, token, head);
+    if (dst == nullptr) return true;
+    const float4* const from = reinterpret_cast<const float4*>(a.work.part_o) + owner * 32 + lane;
+    float4 acc[CHUNKS];
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float m_all = NO_MAX, l_all = 0.0f;
+#pragma unroll 1
+    for (int c = d.c0; c <= d.c1; c += SHARE) {
+        float2 ml[SHARE];
+        float4 v[SHARE][CHUNKS];
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j) {
+            const int cj = c + j <= d.c1 ? c + j : d.c1, slot = 2 * cj + (cj == d.c0 ? 1 : 0);
+            ml[j] = __ldcg(a.work.part_ml + static_cast<size_t>(slot) * BLOCK_M + row);
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k)
+                v[j][k] = __ldcg(from + (static_cast<size_t>(slot) * (D / 8) + sub * CHUNKS + k) * SOFTMAX_THREADS);
+            if (c + j > d.c1) ml[j] = make_float2(NO_MAX, 0.0f);
+        }
+        float m_new = m_all;
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j) m_new = fmaxf(m_new, ml[j].x);
+        const float f0 = ex2_approx(m_all - m_new);
+        m_all = m_new;
+        l_all *= f0;
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) acc[k] = make_float4(acc[k].x * f0, acc[k].y * f0, acc[k].z * f0, acc[k].w * f0);
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j) {
+            const float f = c + j <= d.c1 ? ex2_approx(ml[j].x - m_all) : 0.0f;
+            l_all += ml[j].y * f;
+#pragma unroll
+            for (int k = 0; k < CHUNKS; ++k) {
+                acc[k].x += v[j][k].x * f;
+                acc[k].y += v[j][k].y * f;
+                acc[k].z += v[j][k].z * f;
+                acc[k].w += v[j][k].w * f;
+            }
+        }
+    }
+    const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
+    if (sub == 0 && lane < 16 && a.lse != nullptr) a.lse[static_cast<size_t>(token) * a.H + head] = log_sum(m_all, l_all);
+    uint16_t* const out = dst + (lane >> 4) * (D / 2) + sub * CHUNKS * 4;
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+        uint2 w;
+        w.x = F16 ? pack_f16x2(acc[k].x * inv, acc[k].y * inv) : pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
+        w.y = F16 ? pack_f16x2(acc[k].z * inv, acc[k].w * inv) : pack_bf16x2(acc[k].z * inv, acc[k].w * inv);
+        *reinterpret_cast<uint2*>(out + k * 4) = w;
+    }
+    return true;
+}
+
 // Publishes this thread's half row of an unfinished tile (its O accumulator, maximum and
 // sum), and, in the CTA that finishes last, joins the parts in CTA order and stores the
 // row.  Out of line: at most twice per CTA and launch.
@@ -522,7 +586,7 @@ __device__ __noinline__ bool part_epilogue(const PagedAttnArgs& a, const Piece& 
     };
     auto at_ml = [&](int slot) { return static_cast<size_t>(slot) * BLOCK_M + row; };
 #pragma unroll 1
-    for (int q = 0; q < DH / 32; ++q) {
+    for (int q = 0; q < (row - (threadIdx.x & 15) < d.n_rows ? DH / 32 : 0); ++q) {   // (a warp without rows: none)
         uint32_t orr[32];
         tmem_ld16x2_32<DH>(o_base + q * 32, orr);
         tmem_wait_ld();
@@ -552,6 +616,8 @@ __device__ __noinline__ bool part_epilogue(const PagedAttnArgs& a, const Piece& 
     if (!warp_wait(bar(C::B_JOIN), parity, abort_flag, a.timeout_ns)) return false;
     if (!*last) return true;
     __threadfence();   // the other CTAs' parts, published before their counts
+    if (d.n_rows <= 32) return join_few_rows<D, F16, 4>(a, d, warp);
+    if (d.n_rows <= 64) return join_few_rows<D, F16, 2>(a, d, warp);
     int token, head;
     uint16_t* const dst = dest_row(a, d, row, token, head);
     if (dst == nullptr) return true;
