@@ -194,9 +194,8 @@ int encode_q(CUtensorMap* m, const void* base, int T, int Hkv, int G, int D, lon
 }
 
 // ---- tiling of the paged attention, a function of the shape alone
-// rows 16 and 32: attn_paged_rows.cu; 128: attn_paged.cu
-constexpr int ROWS_SMALL = 16, ROWS_WIDE = 32, ROWS_TILE = 128;
-constexpr int ROWS_FEW = 24;   // packed rows of a sequence and KV head up to which the first is taken
+// rows 16: attn_paged_rows.cu; 128: attn_paged.cu
+constexpr int ROWS_FEW = 16, ROWS_TILE = 128;
 
 struct Tiling {
     int rows;   // packed query rows of a tile
@@ -206,9 +205,9 @@ struct Tiling {
 Tiling make_tiling(int G, int D, int max_q, int sms) {
     Tiling x{};
     const int64_t need = static_cast<int64_t>(G) * max_q;
-    // 32 rows, 32 / 8 heads, few-tokens kernel against the chunk kernel: 32 x 8192 keys 196 / 180 us, 8 x 8192 69 / 60,
-    // one of 500 keys 13.5 / 9.2 (but 62 / 75 for one of 131072 and a single KV head); 20 rows: 189 / 180, 64 / 60,
-    // one of 32768 keys 46 / 55; 16 rows: 177 / 179, 56 / 60
+    // 16 rows, 32 / 8 heads, few-tokens kernel against the chunk kernel: 64 x 2048 keys 99 / 97 us, 32 x 8192 177 / 171,
+    // one of 32768 41 / 36, but 4 x 4096, 16 / 4 heads, 15.7 / 19.2; 12 rows: one of 32768 37 / 36; 4 rows: 29 / 36.
+    // Tiles of 32 rows on mma.sync against it: 20 rows, 64 x 2048 105 / 99, 16 x 1000 26 / 13.5, one of 32768 47 / 36
     if (need > ROWS_FEW) {
         x.rows = ROWS_TILE;
         x.t.tokens = ROWS_TILE / G;
@@ -226,7 +225,7 @@ Tiling make_tiling(int G, int D, int max_q, int sms) {
         x.t.l2_bytes = 64 << 20;
         return x;
     }
-    x.rows = need <= ROWS_SMALL ? ROWS_SMALL : ROWS_WIDE;
+    x.rows = ROWS_FEW;
     x.t.tokens = x.rows / G;
     x.t.block = 32;
     x.t.grid = 2 * sms;
@@ -235,8 +234,7 @@ Tiling make_tiling(int G, int D, int max_q, int sms) {
     x.t.snap = 4;
     x.t.whole = 20;
     x.t.least = 512;
-    // 6 tokens over 19550 keys, 12 / 3 heads: 53 us at 0, 28 at 4, 35 at 12; one over 131072, 8 / 1: 43, 29, 28;
-    // 4 x 2 over 1527, 8 / 1: 12.2, 12.7, 13.3
+    // one token over 131072 keys, 8 / 1 heads: 43 us at 0, 29 at 4, 28 at 12; 4 x 2 over 1527, 8 / 1: 12.2, 12.7, 13.3
     x.t.join = 4;
     x.t.join_rows = 512 / D;   // four channels to a thread
     x.t.few_keys = 512;
@@ -261,8 +259,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // for every tiling of the shape, so one workspace serves steps of any max_q.
 size_t paged_work(char* base, int n, int D, int sms, xs::PagedWork* w) {
     const size_t grid = 2 * static_cast<size_t>(sms);
-    const size_t part_rows = 2 * static_cast<size_t>(sms) * ROWS_TILE;   // two parts per CTA: 2 * grid * ROWS_WIDE is as many
-    static_assert(2 * 2 * ROWS_WIDE <= 2 * ROWS_TILE, "the parts of both kernels fit");
+    const size_t part_rows = 2 * static_cast<size_t>(sms) * ROWS_TILE;   // two parts per CTA
+    static_assert(2 * 2 * ROWS_FEW <= 2 * ROWS_TILE, "the parts of both kernels fit");
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -585,7 +583,7 @@ int xs_attn_paged_fwd(const xs_attn_paged_args* args, void* stream) {
         if ((rc = encode_q(&tq, g.q, T, Hkv, a.G, D, g.q_stride, tiling.t.tokens, cache.dtype)) != XS_OK) return rc;
         e = xs::launch_attn_paged(tq, tk, tv, a, cache.dtype, st);
     } else {
-        e = xs::launch_attn_paged_rows(tk, tv, a, cache.dtype, tiling.rows, st);
+        e = xs::launch_attn_paged_rows(tk, tv, a, cache.dtype, st);
     }
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }

@@ -34,7 +34,8 @@
 // of cuBLAS's burst; the dense kernel reaches 1600 on 18432^2), 740 at the power limit; two
 // chunks of 2048 over 16384, 32 / 8 heads: 700 and 750; any page size within 3 %.  A tile
 // costs some 3 us beside its blocks (first copies 2.6, last PV and epilogue 2.9, overlapped
-// in part), a cut tile 6 more (part 1.1, fence and count 1.8, join 1.2 per part).
+// in part), a cut tile 6 more (part 1.1, fence and count 1.8, join 1.2 per part, some 0.3 with up
+// to 32 rows, whose join all warps share: 8 tokens over 32768 keys, 32 / 8 heads, 49 -> 37 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -1,4 +1,4 @@
-// Attention of a few new tokens over a paged cache: up to 32 packed query rows per KV
+// Attention of a few new tokens over a paged cache: up to 16 packed query rows per KV
 // head (single tokens and short drafts of grouped-query models).
 //
 //   O = sum_t 2^(c s_t - m) V_t / sum_t 2^(c s_t - m),  s_t = <Q, K_t>,
@@ -6,9 +6,9 @@
 //
 // t over the keys that the row sees.  One pass over K and V.
 //
-// What bounds it: the bytes of K and V.  Each is used by the 16 or 32 packed rows of
+// What bounds it: the bytes of K and V.  Each is used by the 16 packed rows of
 // its KV head only (2 to 16 flops per byte), so the matrix instructions are mma.sync on
-// m16 tiles: a tcgen05 tile of 128 rows would leave 7 of 8 rows of its softmax unused,
+// one m16 tile: a tcgen05 tile of 128 rows would leave 7 of 8 rows of its softmax unused,
 // and this work has no other use for tensor memory.  What counts is bytes in flight
 // and short tails:
 //   * 2 CTAs of 4 warps per SM.  A warp walks every fourth group of 32 keys of its CTA's
@@ -50,12 +50,12 @@ constexpr int JOIN_BATCH = 16;             // parts of a cut tile read at once
 constexpr float NO_MAX = -3.402823466e38f;           // running maximum of a row that has seen nothing
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units; P stays below 2^8
 
-template <int D, int MT>
+template <int D>
 struct RowsCfg {
     static constexpr int SLOT = GROUP * D * 2;
     static constexpr int SLOTS = 3 * 128 / D;          // per warp
     static constexpr int OCTET = D / 64 * 1024;        // 8 keys of a slot: [64-channel panel][key][channel]
-    static constexpr int ROWS = 16 * MT;
+    static constexpr int ROWS = 16;
     static constexpr int RING = WARPS * SLOTS * SLOT;  // 96 KB; reused to join the warps' results
     static constexpr int O_STRIDE = D + 8;             // floats; keeps the joining stores off each other's banks
     static constexpr int Q_OFF = RING;
@@ -145,11 +145,11 @@ __device__ __forceinline__ void store_out(const PagedAttnArgs& a, int token, int
             l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
 }
 
-template <int D, bool F16, int MT>
+template <int D, bool F16>
 __global__ void __launch_bounds__(THREADS, 2)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                            const __grid_constant__ PagedAttnArgs a) {
-    using C = RowsCfg<D, MT>;
+    using C = RowsCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -262,45 +262,38 @@ __global__ void __launch_bounds__(THREADS, 2)
         __syncthreads();
 
         // bounds of this thread's rows (two per m16 tile), and of all rows of the tile
-        int lo_row[MT][2], hi_row[MT][2];
+        int lo_row[2], hi_row[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + e * 8 + (lane >> 2);
-                int t, gh;
-                fdivmod(r, a.fd_G, t, gh);
-                const long long p = base + tok0 + t;
-                long long h = a.causal ? p + 1 : seq.kv_len, l = a.window > 0 ? p - a.window + 1 : 0;
-                if (r >= n_rows || h < 0) h = 0;
-                hi_row[mt][e] = static_cast<int>(h);
-                lo_row[mt][e] = static_cast<int>(l > 0 ? l : 0);
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int r = e * 8 + (lane >> 2);
+            int t, gh;
+            fdivmod(r, a.fd_G, t, gh);
+            const long long p = base + tok0 + t;
+            long long h = a.causal ? p + 1 : seq.kv_len, l = a.window > 0 ? p - a.window + 1 : 0;
+            if (r >= n_rows || h < 0) h = 0;
+            hi_row[e] = static_cast<int>(h);
+            lo_row[e] = static_cast<int>(l > 0 ? l : 0);
+        }
         // keys that every row sees: [all_lo, all_hi)
         const long long all_hi = a.causal ? base + tok0 + 1 : seq.kv_len;
         const long long all_lo = a.window > 0 ? base + tok0 + n_tok - a.window : 0;
 
-        uint32_t qf[MT][MT == 1 ? D / 16 : 1][4];
+        uint32_t qf[D / 16][4];
         const int q_row = (lane & 7) + ((lane >> 3) & 1) * 8;
-        auto load_q = [&](int mt, int ks, uint32_t (&f)[4]) {
-            const int r = mt * 16 + q_row, cc = ks * 2 + (lane >> 4);
+        auto load_q = [&](int ks, uint32_t (&f)[4]) {
+            const int r = q_row, cc = ks * 2 + (lane >> 4);
             ldmatrix4(q_smem + (cc >> 3) * (C::ROWS * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4), f[0], f[1], f[2],
                       f[3]);
         };
-        if constexpr (MT == 1) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) load_q(0, ks, qf[0][ks]);
-        }
-        float o[MT][D / 8][4], m_run[MT][2], l_run[MT][2];
+        for (int ks = 0; ks < D / 16; ++ks) load_q(ks, qf[ks]);
+        float o[D / 8][4], m_run[2], l_run[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.0f;
-            m_run[mt][0] = m_run[mt][1] = NO_MAX;
-            l_run[mt][0] = l_run[mt][1] = 0.0f;
-        }
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+        m_run[0] = m_run[1] = NO_MAX;
+        l_run[0] = l_run[1] = 0.0f;
 
         int waited = 0;
         for (int g = 0; g < groups && ok; ++g) {
@@ -315,13 +308,11 @@ __global__ void __launch_bounds__(THREADS, 2)
             ok = ring_wait(bars + slot * 8, round & 1, abort_flag, a.timeout_ns, pos.seq, g);
             if (!ok) break;
             ++waited;
-            float s[MT][GROUP / 8][4];
+            float s[GROUP / 8][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int i = 0; i < GROUP / 8; ++i)
 #pragma unroll
-                for (int i = 0; i < GROUP / 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) s[i][e] = 0.0f;
             {
                 const uint32_t kbase = ring + slot * C::SLOT;
                 const int krow = ((lane >> 4) << 3) + (lane & 7);
@@ -336,14 +327,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                                   b[kb][1], b[kb][2], b[kb][3]);
                     }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if constexpr (MT > 1) load_q(mt, ks, qf[mt][0]);
-                        const uint32_t(&f)[4] = qf[mt][MT == 1 ? ks : 0];
-#pragma unroll
-                        for (int kb = 0; kb < GROUP / 16; ++kb) {
-                            mma16816<F16>(s[mt][2 * kb], f, b[kb][0], b[kb][1]);
-                            mma16816<F16>(s[mt][2 * kb + 1], f, b[kb][2], b[kb][3]);
-                        }
+                    for (int kb = 0; kb < GROUP / 16; ++kb) {
+                        mma16816<F16>(s[2 * kb], qf[ks], b[kb][0], b[kb][1]);
+                        mma16816<F16>(s[2 * kb + 1], qf[ks], b[kb][2], b[kb][3]);
                     }
                 }
             }
@@ -352,64 +338,57 @@ __global__ void __launch_bounds__(THREADS, 2)
             // ---- softmax of the group
             const bool masked = key + GROUP > all_hi || key < all_lo;
             bool moved = false;
-            float alpha[MT][2];
+            float alpha[2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int e = 0; e < 2; ++e) {
+                float mx = __int_as_float(0xff800000);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = __int_as_float(0xff800000);
+                for (int i = 0; i < GROUP / 8; ++i)
 #pragma unroll
-                    for (int i = 0; i < GROUP / 8; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float x = s[mt][i][2 * e + j] * a.c;
-                            if (masked) {
-                                const int t = key + i * 8 + (lane & 3) * 2 + j;
-                                if (t >= hi_row[mt][e] || t < lo_row[mt][e]) x = __int_as_float(0xff800000);
-                            }
-                            s[mt][i][2 * e + j] = x;
-                            mx = fmaxf(mx, x);
+                    for (int j = 0; j < 2; ++j) {
+                        float x = s[i][2 * e + j] * a.c;
+                        if (masked) {
+                            const int t = key + i * 8 + (lane & 3) * 2 + j;
+                            if (t >= hi_row[e] || t < lo_row[e]) x = __int_as_float(0xff800000);
                         }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    alpha[mt][e] = 1.0f;
-                    if (mx > m_run[mt][e] + RESCALE_THRESHOLD) {
-                        alpha[mt][e] = ex2_approx(m_run[mt][e] - mx);
-                        m_run[mt][e] = mx;
-                        moved = true;
+                        s[i][2 * e + j] = x;
+                        mx = fmaxf(mx, x);
                     }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                alpha[e] = 1.0f;
+                if (mx > m_run[e] + RESCALE_THRESHOLD) {
+                    alpha[e] = ex2_approx(m_run[e] - mx);
+                    m_run[e] = mx;
+                    moved = true;
                 }
+            }
             if (__any_sync(0xffffffffu, moved)) {
+                l_run[0] *= alpha[0];
+                l_run[1] *= alpha[1];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    l_run[mt][0] *= alpha[mt][0];
-                    l_run[mt][1] *= alpha[mt][1];
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[mt][i][0] *= alpha[mt][0];
-                        o[mt][i][1] *= alpha[mt][0];
-                        o[mt][i][2] *= alpha[mt][1];
-                        o[mt][i][3] *= alpha[mt][1];
-                    }
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= alpha[0];
+                    o[i][1] *= alpha[0];
+                    o[i][2] *= alpha[1];
+                    o[i][3] *= alpha[1];
                 }
             }
             // P in 16 bits is the A operand of the second product (its relative rounding, half a step of
             // the type, is of the size of the output's own); the sum takes the fp32 values
-            uint32_t pf[MT][GROUP / 16][4];
+            uint32_t pf[GROUP / 16][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int kb = 0; kb < GROUP / 16; ++kb)
 #pragma unroll
-                for (int kb = 0; kb < GROUP / 16; ++kb)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const float* x = s[mt][2 * kb + hf];
-                        const float p0 = ex2_approx(x[0] - m_run[mt][0]), p1 = ex2_approx(x[1] - m_run[mt][0]);
-                        const float p2 = ex2_approx(x[2] - m_run[mt][1]), p3 = ex2_approx(x[3] - m_run[mt][1]);
-                        l_run[mt][0] += p0 + p1;
-                        l_run[mt][1] += p2 + p3;
-                        pf[mt][kb][2 * hf] = pack2<F16>(p0, p1);
-                        pf[mt][kb][2 * hf + 1] = pack2<F16>(p2, p3);
-                    }
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float* x = s[2 * kb + hf];
+                    const float p0 = ex2_approx(x[0] - m_run[0]), p1 = ex2_approx(x[1] - m_run[0]);
+                    const float p2 = ex2_approx(x[2] - m_run[1]), p3 = ex2_approx(x[3] - m_run[1]);
+                    l_run[0] += p0 + p1;
+                    l_run[1] += p2 + p3;
+                    pf[kb][2 * hf] = pack2<F16>(p0, p1);
+                    pf[kb][2 * hf + 1] = pack2<F16>(p2, p3);
+                }
             // ---- O += P V
             slot = (item + 2 * g + 1) % C::SLOTS;
             round = (item + 2 * g + 1) / C::SLOTS;
@@ -441,11 +420,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                         ldmatrix4_trans(vbase + (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 +
                                             (((cc & 7) ^ (r & 7)) << 4), b0, b1,
                                         b2, b3);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            mma16816<F16>(o[mt][2 * nb], pf[mt][kb], b0, b1);
-                            mma16816<F16>(o[mt][2 * nb + 1], pf[mt][kb], b2, b3);
-                        }
+                        mma16816<F16>(o[2 * nb], pf[kb], b0, b1);
+                        mma16816<F16>(o[2 * nb + 1], pf[kb], b2, b3);
                     }
                 }
             }
@@ -461,26 +437,22 @@ __global__ void __launch_bounds__(THREADS, 2)
 
         // ---- join the warps
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l_run[mt][e] += __shfl_xor_sync(0xffffffffu, l_run[mt][e], 1);
-                l_run[mt][e] += __shfl_xor_sync(0xffffffffu, l_run[mt][e], 2);
-            }
+        for (int e = 0; e < 2; ++e) {
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
+        }
         __syncthreads();   // every warp is done with its ring
         if (*abort_flag) return;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int e = 0; e < 2; ++e) {
+            const int r = e * 8 + (lane >> 2);
+            if (r >= n_rows) continue;
+            if ((lane & 3) == 0) join_ml[warp * C::ROWS + r] = make_float2(m_run[e], l_run[e]);
+            float* d = join_o + (warp * C::ROWS + r) * C::O_STRIDE + (lane & 3) * 2;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + e * 8 + (lane >> 2);
-                if (r >= n_rows) continue;
-                if ((lane & 3) == 0) join_ml[warp * C::ROWS + r] = make_float2(m_run[mt][e], l_run[mt][e]);
-                float* d = join_o + (warp * C::ROWS + r) * C::O_STRIDE + (lane & 3) * 2;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<float2*>(d + i * 8) = make_float2(o[mt][i][2 * e], o[mt][i][2 * e + 1]);
-            }
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2*>(d + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+        }
         __syncthreads();
         // this piece's CTA slot: 2c + 1 for a piece that starts its tile, 2c for one that continues it
         const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (pos.k == 0 ? 1 : 0);
@@ -581,10 +553,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
 }
 
-template <int D, bool F16, int MT>
+template <int D, bool F16>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, cudaStream_t stream) {
-    auto kern = attn_paged_rows_kernel<D, F16, MT>;
-    const int smem = RowsCfg<D, MT>::ALLOC;
+    auto kern = attn_paged_rows_kernel<D, F16>;
+    const int smem = RowsCfg<D>::ALLOC;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_overlapped(kern, dim3(static_cast<unsigned>(a.tile.grid)), THREADS, smem, stream, tk, tv, a);
@@ -593,14 +565,9 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Page
 }  // namespace
 
 cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int dtype,
-                                   int rows, cudaStream_t stream) {
-    const bool wide = rows > 16;
-    if (a.D == 128) {
-        if (dtype == 0) return wide ? launch_rows<128, false, 2>(tk, tv, a, stream) : launch_rows<128, false, 1>(tk, tv, a, stream);
-        return wide ? launch_rows<128, true, 2>(tk, tv, a, stream) : launch_rows<128, true, 1>(tk, tv, a, stream);
-    }
-    if (dtype == 0) return wide ? launch_rows<64, false, 2>(tk, tv, a, stream) : launch_rows<64, false, 1>(tk, tv, a, stream);
-    return wide ? launch_rows<64, true, 2>(tk, tv, a, stream) : launch_rows<64, true, 1>(tk, tv, a, stream);
+                                   cudaStream_t stream) {
+    if (a.D == 128) return dtype == 0 ? launch_rows<128, false>(tk, tv, a, stream) : launch_rows<128, true>(tk, tv, a, stream);
+    return dtype == 0 ? launch_rows<64, false>(tk, tv, a, stream) : launch_rows<64, true>(tk, tv, a, stream);
 }
 
 cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed) {

@@ -75,7 +75,7 @@ cudaError_t launch_paged_step(const StepArgs& a, int num_sms, cudaStream_t strea
 // Query rows of one KV head are packed token-major, the G = H / Hkv query heads of a
 // token side by side: a tile is `tokens` consecutive new tokens of one sequence and
 // one KV head (up to tokens * G rows), and its keys are walked in blocks of `block`.
-// Two kernels share plan and arguments: mma.sync on up to 32 rows (single tokens and
+// Two kernels share plan and arguments: mma.sync on up to 16 rows (single tokens and
 // short drafts) and tcgen05 on up to 128 rows (chunks).
 struct PagedTiling {
     int tokens;     // new tokens per tile
@@ -176,9 +176,9 @@ struct PagedAttnArgs {
 // lands as [token / 8][panel][token % 8][64 channels]: 1024-byte swizzle atoms, so that any
 // number of pages side by side form one operand tile, with one copy per page.
 //
-// rows: 16 or 32 (the tile's packed rows, tile.tokens * G, fit)
+// Tiles of up to 16 packed rows.
 cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int dtype,
-                                   int rows, cudaStream_t stream);
+                                   cudaStream_t stream);
 
 // Tiles of up to 128 packed rows; tq covers [T, Hkv, G, D] in boxes of one tile's rows.
 cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
