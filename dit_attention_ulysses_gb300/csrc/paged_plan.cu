@@ -36,6 +36,7 @@ constexpr int PLAN_THREADS = 1024;
 constexpr int MAX_RANGES = 511;
 constexpr int SORTED = 4 * PLAN_THREADS;      // tiles that a plan sorts, four per thread
 constexpr int SORT_ROWS = SORTED / 32;        // one per warp and turn
+constexpr int SMEM_MOST = 200 * 1024;         // dynamic shared memory: 8192 sequences on 152 SMs take 172,448 bytes
 
 // Sums over the threads before this one, and over all.
 struct Sums {
@@ -482,9 +483,11 @@ cudaError_t launch_paged_plan(const PagedPlanArgs& a, cudaStream_t stream) {
     if (a.tile.grid > MAX_RANGES || a.tile.waves > MAX_PAGED_WAVES) return cudaErrorInvalidConfiguration;
     const size_t smem = static_cast<size_t>(a.n + 1) * 16 + static_cast<size_t>(a.tile.grid + 1) * sizeof(PagedPos) +
                         static_cast<size_t>(a.tile.grid) * a.tile.waves * sizeof(float);
+    if (smem > SMEM_MOST) return cudaErrorInvalidConfiguration;
     if (smem > 32 * 1024) {   // (the kernel has 14 KB of its own beside these)
-        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        // The limit is the function's, not the launch's: one constant for all, so that no thread's call takes it
+        // below what another's launch needs
+        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST);
         if (e != cudaSuccess) return e;
     }
     return launch_overlapped(paged_plan_kernel, dim3(1), PLAN_THREADS, smem, stream, a);

@@ -236,9 +236,12 @@ __global__ void __launch_bounds__(THREADS) paged_step_kernel(const __grid_consta
 template <int THREADS, int K>
 static cudaError_t launch(const StepArgs& a, int num_sms, cudaStream_t stream) {
     const size_t smem = (static_cast<size_t>(a.n) * 4 + 3) * sizeof(int);
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel<THREADS, K>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    constexpr int most = (THREADS * K * 4 + 3) * static_cast<int>(sizeof(int));
+    if (most > 40 * 1024 && smem > 40 * 1024) {
+        // The limit is the function's, not the launch's: one constant for all, so that no thread's call takes it
+        // below what another's launch needs
+        const cudaError_t e =
+            cudaFuncSetAttribute(paged_step_kernel<THREADS, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     long long work = a.rows > a.n ? a.rows : a.n;
