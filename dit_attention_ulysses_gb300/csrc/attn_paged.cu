@@ -20,7 +20,8 @@
 //              issues one page's copy
 //   warp  9    issuer of the S = Q K^T MMAs (one lane) and TMEM owner
 //   warp 10    issuer of the O += P V MMAs (one lane; all lanes clear the V rows past a
-//              sequence's end, whose stale contents 0 * NaN would carry into O)
+//              sequence's end and before its first row's window, whose contents 0 * NaN
+//              would carry into O)
 //   warp 11    producer of Q and K: walks the CTA's part of the plan and describes every
 //              piece of work in shared memory for the other roles
 // TMEM: S buffers 0-2 (P over their first halves) and the O accumulator, as in attn_fwd.cu.
@@ -78,7 +79,8 @@ struct Piece {
     int c0, c1;     // CTAs of an unfinished tile
     int index;      // row of the block table
     int lo_key;     // first key that some row sees
-    int unused[4];
+    int unseen;     // keys below it: no row of the sequence sees them
+    int unused[3];
 };
 static_assert(sizeof(Piece) == 64, "descriptor");
 
@@ -255,6 +257,7 @@ __device__ void producer_k_role(const CUtensorMap* tq, const CUtensorMap* tk, co
             d.pos0 = seq.kv_len - seq.q_len + tok0;
             d.head = pos.head;
             d.index = seq.index;
+            d.unseen = paged_unseen(seq, a.window);
             const bool whole = pos.k == 0 && !cut_end;
             d.part = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos.k == 0 ? 1 : 0);
             d.c0 = pos.k == 0 ? static_cast<int>(blockIdx.x) : range.c0;
@@ -422,22 +425,23 @@ __device__ void mma_pv_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0
         const Piece& d = piece_of(smem, C::PIECE_OFF, u);
         const int n = d.nb;
         if (n == 0) break;
-        // blocks [tail, n) reach past the sequence: their V rows from `left` on are cleared
-        const int left = d.kv_len - d.key0;
+        // blocks [tail, n) reach past the sequence: their V rows from `left` on are cleared; so are the first block's
+        // below `unseen`
+        const int left = d.kv_len - d.key0, low = d.unseen - d.key0;
         const int tail = left > 0 ? left / BLOCK_N : 0;
         // every block below `stop` is lane 0's alone; then the warp clears one and goes on
         for (int j0 = 0; j0 < n && ok;) {
-            const bool clear = j0 >= tail;
+            const bool clear = j0 >= tail || (j0 == 0 && low > 0);
             const int stop = clear ? j0 + 1 : (tail < n ? tail : n);
             if (clear) {
                 const uint32_t item = item0 + ring_pos_v(j0, n);
                 const uint32_t stage = item % C::KV_STAGES;
                 ok = warp_wait(bar(C::B_KV_FULL + stage), (item / C::KV_STAGES) & 1, abort_flag, a.timeout_ns, u, j0);
                 if (!ok) break;
-                const int first = left - j0 * BLOCK_N > 0 ? left - j0 * BLOCK_N : 0;
+                const int first = min(max(left - j0 * BLOCK_N, 0), BLOCK_N), below = j0 == 0 ? max(low, 0) : 0;
                 uint8_t* v = smem + C::KV_OFF + stage * C::TILE_BYTES;
-                for (int i = lane; i < (BLOCK_N - first) * (D / 8); i += 32) {
-                    const int r = first + i / (D / 8), c8 = i % (D / 8);
+                for (int i = lane; i < (below + BLOCK_N - first) * (D / 8); i += 32) {
+                    const int r = i / (D / 8) + (i < below * (D / 8) ? 0 : first - below), c8 = i % (D / 8);
                     *reinterpret_cast<uint4*>(v + (r >> 3) * C::GROUP + (c8 >> 3) * 1024 + (r & 7) * 128 + (c8 & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }

@@ -34,6 +34,13 @@ __host__ __device__ __forceinline__ void paged_tile_keys(const PagedSeq& s, int 
     lo = static_cast<int>(l);
 }
 
+// Keys below it are before the window of the sequence's first new token: no row sees them.  (The first block of any
+// tile may begin below it.)
+__host__ __device__ __forceinline__ int paged_unseen(const PagedSeq& s, int window) {
+    const long long l = static_cast<long long>(s.kv_len) - s.q_len - window + 1;
+    return window > 0 && l > 0 ? static_cast<int>(l) : 0;
+}
+
 // Key blocks of tile t: blocks [first, first + count).
 __host__ __device__ __forceinline__ void paged_tile_blocks(const PagedSeq& s, int t, const PagedTiling& g, int causal,
                                                            int window, int& first, int& count) {
