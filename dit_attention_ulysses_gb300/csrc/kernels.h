@@ -15,6 +15,7 @@ constexpr int XS_DEVICE_TIMEOUT_CODE = 1; // a bounded wait expired; the launch 
 constexpr int XS_DEVICE_BOUNDS_CODE = 3;  // a per-piece index check failed; the access was skipped
 // Where the first device error of a launch happened (see report_error).
 struct DeviceErrorInfo {
+    unsigned long long when;   // %globaltimer, ns: which of several kernels' records is the first
     int code;       // XS_DEVICE_*_CODE
     int cta;        // blockIdx.x
     int warp;       // threadIdx.x / 32
