@@ -421,9 +421,7 @@ class Rope:
                  high: float = 32.0, magnitude: float = 1.0):
         self._struct = _RopeStruct()
         self.ptr = ctypes.addressof(self._struct)
-        self.D, self.rot = D, D if rot is None else rot
-        self._args = (D, self.rot, layout, base, scaling, factor, context, low, high, magnitude)
-        xs_rope_init(self, *self._args)
+        xs_rope_init(self, D, D if rot is None else rot, layout, base, scaling, factor, context, low, high, magnitude)
 
     def __reduce__(self):   # copies have a table of their own
         return Rope, self._args
@@ -431,9 +429,11 @@ class Rope:
 
 def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling: int, factor: float,
                  context: float, low: float, high: float, magnitude: float) -> None:
-    """Fill ``rope`` on the host (``Rope(...)`` calls it)."""
+    """Fill ``rope`` on the host (``Rope(...)`` calls it); a refused call leaves it as it was."""
     _check(lib.xs_rope_init(rope.ptr, D, rot, layout, base, scaling, factor, context, low, high, magnitude),
            "xs_rope_init")
+    rope.D, rope.rot = D, rot
+    rope._args = (D, rot, layout, base, scaling, factor, context, low, high, magnitude)
 
 
 # The checks below run on every call of a decoding loop, where they cost more than the
