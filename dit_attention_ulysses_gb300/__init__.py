@@ -173,6 +173,13 @@ def _check(code: int, where: str) -> None:
         raise XsError(code, where)
 
 
+def _c_int(x: int, code: int, where: str) -> int:
+    """``x`` if a C int holds it (ctypes would pass its lower 32 bits on), else the refusal ``code``."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise XsError(code, where)
+    return x
+
+
 def _ptr_array(ptrs):
     arr = (_vp * max(1, len(ptrs)))()
     for i, p in enumerate(ptrs):
@@ -430,8 +437,10 @@ class Rope:
 def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling: int, factor: float,
                  context: float, low: float, high: float, magnitude: float) -> None:
     """Fill ``rope`` on the host (``Rope(...)`` calls it); a refused call leaves it as it was."""
-    _check(lib.xs_rope_init(rope.ptr, D, rot, layout, base, scaling, factor, context, low, high, magnitude),
-           "xs_rope_init")
+    where = "xs_rope_init"
+    _check(lib.xs_rope_init(rope.ptr, _c_int(D, XS_ERR_HEAD_DIM, where), _c_int(rot, XS_ERR_ROPE, where),
+                            _c_int(layout, XS_ERR_LAYOUT, where), base, _c_int(scaling, XS_ERR_ROPE, where), factor, context,
+                            low, high, magnitude), where)
     rope.D, rope.rot = D, rot
     rope._args = (D, rot, layout, base, scaling, factor, context, low, high, magnitude)
 
@@ -609,6 +618,7 @@ def xs_paged_step(cache_lens, new_lens, block_table, free_pages, free_count, pag
     _on_device(block_table, "block_table", dev)
     n, width = block_table.shape
     rows, n_pages = positions.numel(), free_pages.numel()
+    page_size = _c_int(page_size, XS_ERR_PAGE, "xs_paged_step")
     code = lib.xs_paged_step(_vec(cache_lens, "cache_lens", i32, n, dev), _vec(new_lens, "new_lens", i32, n, dev),
                              block_table.data_ptr(), _vec(free_pages, "free_pages", i32, n_pages, dev),
                              _vec(free_count, "free_count", i32, 1, dev), n, width, n_pages, page_size, rows,
@@ -658,6 +668,8 @@ def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, cau
     if code is None:
         dev = _device()
         _on_device(w._buf, "workspace", dev)
+        for x in (max_q, window):
+            _c_int(x, XS_ERR_SHAPE, "xs_attn_paged_plan")
         code = lib.xs_attn_paged_plan(_vec(cu_q, "cu_q", _I32, w.n + 1, dev), _vec(kv_lens, "kv_lens", _I32, w.n, dev),
                                       w.n, w.H, w.Hkv, w.D, max_q, causal, window, w.ptr, w.nbytes,
                                       _stream_of(stream, dev))
