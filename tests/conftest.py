@@ -18,13 +18,14 @@ def _sees_a_gpu():
 
 
 def pytest_collection_modifyitems(config, items):
-    """Those files run in processes that see no GPU only: not beside GPU tests on a machine with one
-    (``-m "not gpu"`` hides it)."""
+    """Those files run in processes that see no GPU only: beside GPU tests on a machine with one they
+    are skipped, and test_host_files.py runs them in such a process (``-m "not gpu"`` hides the GPU and
+    runs them directly)."""
     if _sees_a_gpu():
-        out = [i for i in items if os.path.basename(str(i.fspath)) in NO_GPU_FILES and not i.get_closest_marker("gpu")]
-        if out:
-            config.hook.pytest_deselected(items=out)
-            items[:] = [i for i in items if i not in out]
+        skip = pytest.mark.skip(reason="made-up addresses: test_host_files.py runs this file in a process that sees no GPU")
+        for i in items:
+            if os.path.basename(str(i.fspath)) in NO_GPU_FILES and not i.get_closest_marker("gpu"):
+                i.add_marker(skip)
 
 
 def pytest_configure(config):
