@@ -80,7 +80,8 @@ struct Piece {
     int index;      // row of the block table
     int lo_key;     // first key that some row sees
     int unseen;     // keys below it: no row of the sequence sees them
-    int unused[3];
+    int unseen_rows;   // so many of them, right below it, come in with the first block (the others read as zeros)
+    int unused[2];
 };
 static_assert(sizeof(Piece) == 64, "descriptor");
 
@@ -258,6 +259,7 @@ __device__ void producer_k_role(const CUtensorMap* tq, const CUtensorMap* tk, co
             d.head = pos.head;
             d.index = seq.index;
             d.unseen = paged_unseen(seq, a.window);
+            d.unseen_rows = pos.k == 0 ? max(d.unseen - (d.lo_key & ~(box - 1)), 0) : 0;
             const bool whole = pos.k == 0 && !cut_end;
             d.part = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (pos.k == 0 ? 1 : 0);
             d.c0 = pos.k == 0 ? static_cast<int>(blockIdx.x) : range.c0;
@@ -426,8 +428,8 @@ __device__ void mma_pv_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0
         const int n = d.nb;
         if (n == 0) break;
         // blocks [tail, n) reach past the sequence: their V rows from `left` on are cleared; so are the first block's
-        // below `unseen`
-        const int left = d.kv_len - d.key0, low = d.unseen - d.key0;
+        // `low` rows below `unseen`
+        const int left = d.kv_len - d.key0, low = d.unseen_rows;
         const int tail = left > 0 ? left / BLOCK_N : 0;
         // every block below `stop` is lane 0's alone; then the warp clears one and goes on
         for (int j0 = 0; j0 < n && ok;) {
@@ -438,10 +440,11 @@ __device__ void mma_pv_role(const PagedAttnArgs& a, uint8_t* smem, uint32_t bar0
                 const uint32_t stage = item % C::KV_STAGES;
                 ok = warp_wait(bar(C::B_KV_FULL + stage), (item / C::KV_STAGES) & 1, abort_flag, a.timeout_ns, u, j0);
                 if (!ok) break;
-                const int first = min(max(left - j0 * BLOCK_N, 0), BLOCK_N), below = j0 == 0 ? max(low, 0) : 0;
+                const int first = min(max(left - j0 * BLOCK_N, 0), BLOCK_N), below = j0 == 0 ? low : 0;
+                const int from = d.unseen - d.key0 - below;
                 uint8_t* v = smem + C::KV_OFF + stage * C::TILE_BYTES;
                 for (int i = lane; i < (below + BLOCK_N - first) * (D / 8); i += 32) {
-                    const int r = i / (D / 8) + (i < below * (D / 8) ? 0 : first - below), c8 = i % (D / 8);
+                    const int r = i / (D / 8) + (i < below * (D / 8) ? from : first - below), c8 = i % (D / 8);
                     *reinterpret_cast<uint4*>(v + (r >> 3) * C::GROUP + (c8 >> 3) * 1024 + (r & 7) * 128 + (c8 & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }

@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int n_tok = min(a.tile.tokens, seq.q_len - tok0);
         const int n_rows = n_tok * a.G;
         const long long base = static_cast<long long>(seq.kv_len) - seq.q_len;
-        const int unseen = paged_unseen(seq, a.window);
+        // keys [loaded, unseen) come in with the first copy although no row of the sequence sees them
+        const int unseen = paged_unseen(seq, a.window), loaded = lo_tile & ~(box - 1);
         const int* table = a.table + static_cast<long long>(seq.index) * a.table_stride;
 
         // group g of this warp starts at key0 + (warp + WARPS g) * GROUP
@@ -396,13 +397,13 @@ __global__ void __launch_bounds__(THREADS, 2)
             ok = ring_wait(bars + slot * 8, round & 1, abort_flag, a.timeout_ns, pos.seq, g);
             if (!ok) break;
             ++waited;
-            if (key + GROUP > seq.kv_len || key < unseen) {
-                // what no row of the sequence sees holds whatever was there (rows of a page past its end, keys before
-                // its first row's window): 0 * NaN must not reach the sum
+            if (key + GROUP > seq.kv_len || (key < unseen && loaded < unseen)) {
+                // what no row of the sequence sees holds whatever was there (rows of a page past its end, keys of a page
+                // before its first row's window): 0 * NaN must not reach the sum
                 const int bad = seq.kv_len > key ? min(seq.kv_len - key, GROUP) : 0;
-                const int low = min(max(unseen - key, 0), GROUP);
+                const int from = max(loaded - key, 0), low = max(min(unseen - key, GROUP) - from, 0);   // rows
                 for (int i = lane; i < (low + GROUP - bad) * (D / 8); i += 32) {
-                    const int r = i / (D / 8) + (i < low * (D / 8) ? 0 : bad - low), cc = i % (D / 8);
+                    const int r = i / (D / 8) + (i < low * (D / 8) ? from : bad - low), cc = i % (D / 8);
                     *reinterpret_cast<uint4*>(smem + (ring - smem_addr(smem)) + slot * C::SLOT +
                                               (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 + (cc & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
