@@ -205,9 +205,15 @@ struct Tiling {
 Tiling make_tiling(int G, int D, int max_q, int sms) {
     Tiling x{};
     const int64_t need = static_cast<int64_t>(G) * max_q;
-    // 16 rows, 32 / 8 heads, few-tokens kernel against the chunk kernel: 64 x 2048 keys 99 / 97 us, 32 x 8192 177 / 171,
-    // one of 32768 41 / 36, but 4 x 4096, 16 / 4 heads, 15.7 / 19.2; 12 rows: one of 32768 37 / 36; 4 rows: 29 / 36.
-    // Tiles of 32 rows on mma.sync against it: 20 rows, 64 x 2048 105 / 99, 16 x 1000 26 / 13.5, one of 32768 47 / 36
+    // Few-tokens kernel against chunk kernel, us, by keys (which the host does not know):
+    //   rows, heads    1 x 300   1 x 4096   1 x 32768  4 x 4096   16 x 1000  64 x 2048  32 x 8192  64 ragged
+    //   16, 32 / 8     8.4/8.6   15.2/18.2  39.4/36.7  17.3/19.3  20.0/13.8  97.5/98.0  176/172    54.8/58.3
+    //   16, 16 / 4     8.4/8.7   13.7/17.9  26.9/23.7  15.8/18.9  15.8/13.1  55.9/54.4  96.9/92.9  32.9/36.5
+    //   16, 16 / 1     8.4/8.6   13.1/17.9  24.0/23.0  14.4/18.2  13.6/12.3  18.9/20.9  35.1/35.3  18.1/19.2
+    //   12, 32 / 8     8.1/8.8   13.4/18.4  36.7/37.2  16.0/19.5  18.5/13.7  95.3/97.7  175/172    51.8/58.6
+    // At 16 rows the chunk kernel wins with several short tiles to a CTA (16 x 1000) and on one long sequence, the other
+    // elsewhere; at 12 to 15 rows that one is faster by 5 .. 15 % in the mean over these shapes.  Above 16 rows it would
+    // need a second m16 tile: 20 rows, 64 x 2048 105 / 99, 16 x 1000 26 / 13.5, one of 32768 47 / 36
     if (need > ROWS_FEW) {
         x.rows = ROWS_TILE;
         x.t.tokens = ROWS_TILE / G;

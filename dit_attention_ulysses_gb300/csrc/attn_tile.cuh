@@ -76,7 +76,9 @@ static __device__ __forceinline__ float max64(const uint32_t (&sr)[2][32]) {
 // p = 2^(s*c - m) for a thread's 64 scores: one packed f32x2 FMA per pair of
 // scores and one MUFU ex2 each, packed to bf16 pairs; the fp32 values are summed
 // with packed f32x2 adds in two independent chains (half the FP32-pipe
-// instructions of scalar FMAs and adds).
+// instructions of scalar FMAs and adds).  The second product takes its operands in
+// the type of V: rounding p to it is off by half a step relative to p, which is of
+// the size of the output's own rounding.
 // TAIL: columns at or past `valid` (keys past the sequence) get p = 0.
 // F16: p in fp16 instead of bf16.
 template <bool TAIL, bool F16 = false>

@@ -21,7 +21,8 @@ struct DeviceErrorInfo {
     int warp;       // threadIdx.x / 32
     int lane;
     int site;       // waits: shared-memory address of the mbarrier (split-tile flags: 0x40000 + slot);
-                    // index checks: 1 packed-sequence table entry, 2 destination shard
+                    // index checks: 1 packed-sequence table entry, 2 destination shard,
+                    // 3 a plan that does not match its call
     int detail[3];  // waits: phase parity, piece index, key block; index checks: the values checked
 };
 

@@ -11,10 +11,10 @@
 //
 // What bounds it: the launch and a chain of dependent steps (load the lengths,
 // scan, look up, store); the bytes are a few MB at most.  So it is one launch with
-// no exchange between CTAs: every CTA scans all requests itself (at most 8192: up to
-// eight per thread in registers, all three sums in one scan), then the CTAs share the outputs out between them, one thread per
-// token, per page taken and per page given back, each finding its request by
-// bisection.  A page that this step hands out is never read from the table or the
+// no exchange between CTAs: every CTA scans all requests itself (at most 8192: one to
+// eight per thread, in registers up to 4096 requests, partly spilled above; all three sums
+// in one scan), then the CTAs share the outputs out between them, one thread per token, per
+// page taken and per page given back, each finding its request by bisection.  A page that this step hands out is never read from the table or the
 // list cell that another CTA writes: it is computed again from the prefix sums and
 // cells that stay as they are.  256 requests with one token each: 3.2 us; 4096 requests
 // with 125,000 tokens: 8 us.

@@ -404,8 +404,9 @@ int xs_attn_varlen_fwd(const void* q, const void* k, const void* v, const int* s
  *
  * Keys and values of earlier tokens are kept in pages of `page_size` tokens (a power
  * of two, 16 .. 1024).  A cache is [n_pages, page_size, Hkv, D], D contiguous, with
- * caller-given strides between pages, tokens and heads (elements, multiples of 8, at
- * least D), so token-major and head-major pages are the same to the library, and K and
+ * caller-given strides between pages, tokens and heads (elements, multiples of 8, D .. 2^35;
+ * the last head of a token at most 2^31 - 1 - D elements behind the first: XS_ERR_SHAPE
+ * otherwise), so token-major and head-major pages are the same to the library, and K and
  * V may share a buffer.  Row i of a block table [n, width] lists the pages of request
  * i in order; entries past its tokens are not read.  A step brings a_i new tokens to
  * request i, which holds c_i already:
@@ -418,8 +419,9 @@ int xs_attn_varlen_fwd(const void* q, const void* k, const void* v, const int* s
  * a step can be captured in a CUDA graph and replayed with other lengths.
  * Calls are asynchronous on `stream`; every buffer is the caller's and must belong to
  * the current device; two calls that may run at the same time must not share a
- * workspace.  Inputs hold finite values, except in places that the definitions below
- * do not read (entries, slots and rows past the sequences).
+ * workspace.  Inputs hold finite values, except in places that no row's definition below
+ * reads (entries, slots and rows past the sequences, keys before the window of a
+ * sequence's first new token).
  * ---------------------------------------------------------------------------
  */
 
@@ -643,7 +645,7 @@ int xs_burst_gap(void* dst, size_t dst_bytes, int producers, size_t burst_bytes,
  * suspect); else XS_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel expired
  * (the kernel abandoned its work and returned; its outputs are unspecified);
  * XS_ERR_DEVICE_BOUNDS if an index check inside a kernel failed (the access was
- * skipped: an internal error); or XS_ERR_CUDA if synchronisation itself failed.
+ * skipped: an internal error, or a plan that does not match its call); or XS_ERR_CUDA if synchronisation itself failed.
  */
 int xs_attn_get_device_error(void* stream);
 
@@ -656,7 +658,8 @@ int xs_attn_get_device_error(void* stream);
  *   info[1]  CTA index, info[2] warp, info[3] lane of the thread that recorded it
  *   info[4]  site: for a wait, the shared-memory address of its mbarrier (the
  *            split-tile flags of CTA slot s: 0x40000 + s); for an index check,
- *            1 = packed-sequence table entry, 2 = destination shard
+ *            1 = packed-sequence table entry, 2 = destination shard,
+ *            3 = a plan of xs_attn_paged_plan that does not match its call
  *   info[5..7]  details: for a wait, the phase parity, the piece index and the
  *            key block it waited in (-1: none); for an index check, the values
  *            that failed it.
