@@ -991,14 +991,17 @@ int xs_attn_get_device_error_info(void* stream, int* info, int n_info) {
     if (e != cudaSuccess) return cuda_fail(e);
     int v = 0, drain = 0;
     xs::DeviceErrorInfo r{};
+    unsigned long long t = 0;
     // each kernel family keeps its own words: the earliest record is reported, all are cleared
     for (auto read : {xs::read_and_clear_device_error, xs::read_and_clear_paged_error, xs::read_and_clear_paged_rows_error}) {
         int v1 = 0, d1 = 0;
+        unsigned long long t1 = 0;
         xs::DeviceErrorInfo r1{};
-        if ((e = read(&v1, &r1, &d1)) != cudaSuccess) return cuda_fail(e);
-        if (v1 != 0 && (v == 0 || r1.when < r.when)) {
+        if ((e = read(&v1, &r1, &d1, &t1)) != cudaSuccess) return cuda_fail(e);
+        if (v1 != 0 && (v == 0 || t1 < t)) {
             v = v1;
             r = r1;
+            t = t1;
         }
         drain |= d1;
     }

@@ -1072,8 +1072,8 @@ cudaError_t set_tile_spans(unsigned long long* buf, int ctas, int per_cta) {
 }
 #endif
 
-cudaError_t read_and_clear_device_error(int* value, DeviceErrorInfo* info, int* drain_failed) {
-    return read_and_clear_error_words(value, info, drain_failed);
+cudaError_t read_and_clear_device_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
+    return read_and_clear_error_words(value, info, drain_failed, when);
 }
 
 }  // namespace xs

@@ -918,8 +918,8 @@ cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, cons
     return dtype == 0 ? launch<64, false>(tq, tk, tv, a, stream) : launch<64, true>(tq, tk, tv, a, stream);
 }
 
-cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed) {
-    return read_and_clear_error_words(value, info, drain_failed);
+cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
+    return read_and_clear_error_words(value, info, drain_failed, when);
 }
 
 }  // namespace xs

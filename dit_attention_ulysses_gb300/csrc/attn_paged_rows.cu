@@ -574,8 +574,8 @@ cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv,
     return dtype == 0 ? launch_rows<64, false>(tk, tv, a, stream) : launch_rows<64, true>(tk, tv, a, stream);
 }
 
-cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed) {
-    return read_and_clear_error_words(value, info, drain_failed);
+cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
+    return read_and_clear_error_words(value, info, drain_failed, when);
 }
 
 }  // namespace xs

@@ -15,7 +15,6 @@ constexpr int XS_DEVICE_TIMEOUT_CODE = 1; // a bounded wait expired; the launch 
 constexpr int XS_DEVICE_BOUNDS_CODE = 3;  // a per-piece index check failed; the access was skipped
 // Where the first device error of a launch happened (see report_error).
 struct DeviceErrorInfo {
-    unsigned long long when;   // %globaltimer, ns: which of several kernels' records is the first
     int code;       // XS_DEVICE_*_CODE
     int cta;        // blockIdx.x
     int warp;       // threadIdx.x / 32
@@ -167,10 +166,10 @@ template <int D>
 cudaError_t launch_attn_sharded(const ShardMaps& maps, int P, const AttnArgs& args, int grid, bool cooperative,
                                 cudaStream_t stream);
 
-// Reads and clears the device error word, the record of the first error and the
-// flag of abort drains that gave up (copies or MMAs possibly still in flight when
-// a CTA exited).
-cudaError_t read_and_clear_device_error(int* value, DeviceErrorInfo* info, int* drain_failed);
+// Reads and clears the device error word, the record of the first error (and its
+// time, when there is one) and the flag of abort drains that gave up (copies or
+// MMAs possibly still in flight when a CTA exited).
+cudaError_t read_and_clear_device_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 
 #ifdef XS_TILE_SPANS
 // Instrumented build only: where the per-tile timestamps go (device buffer of

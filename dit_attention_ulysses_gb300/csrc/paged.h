@@ -184,7 +184,7 @@ cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv,
 cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PagedAttnArgs& a, int dtype, cudaStream_t stream);
 
-cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed);
-cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed);
+cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
+cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 
 }  // namespace xs
