@@ -46,6 +46,10 @@ __all__ = [
     "xs_attn_paged_workspace_bytes",
     "xs_attn_paged_plan",
     "xs_attn_paged_fwd",
+    "xs_rope_append_paged8",
+    "xs_paged_read8",
+    "xs_attn_paged8_plan",
+    "xs_attn_paged8_fwd",
     "xs_attn_get_device_error",
     "xs_attn_get_device_error_info",
     "xs_attn_error_string",
@@ -134,6 +138,10 @@ EXPORTS = {
     "xs_attn_paged_workspace_bytes": (_int, [_int, _int, _int, _int, ctypes.POINTER(_size)]),
     "xs_attn_paged_plan": (_int, [_vp, _vp] + [_int] * 7 + [_vp, _size, _vp]),
     "xs_attn_paged_fwd": (_int, [ctypes.c_char_p, _vp]),
+    "xs_rope_append_paged8": (_int, [ctypes.c_char_p, _vp]),
+    "xs_paged_read8": (_int, [ctypes.c_char_p, _vp]),
+    "xs_attn_paged8_plan": (_int, [_vp, _vp] + [_int] * 7 + [_vp, _size, _vp]),
+    "xs_attn_paged8_fwd": (_int, [ctypes.c_char_p, _vp]),
     "xs_burst_gap": (_int, [_vp, _size, _int, _size, _int, ctypes.c_longlong, ctypes.c_longlong, _vp, _vp]),
     "xs_attn_get_device_error": (_int, [_vp]),
     "xs_attn_get_device_error_info": (_int, [_vp, ctypes.POINTER(_int), _int]),
@@ -450,7 +458,8 @@ def xs_rope_init(rope: Rope, D: int, rot: int, layout: int, base: float, scaling
 # refusal is worked out only once there is one.  Where the native binding (csrc/binding.cpp)
 # has been built for this torch, it reads the tensors and makes the call itself; what it does
 # not accept (it returns None) goes through the checks here.
-_I32 = _I64 = _F32 = None
+_I32 = _I64 = _F32 = _E4M3 = None
+_E8M0 = ()
 _DTYPES = {}
 _current_device = _raw_stream = None
 _native = None
@@ -463,13 +472,14 @@ def _bind_native(torch):
         return None
     if _binding.torch_version != torch.__version__.partition("+")[0]:
         return None
-    names = ("xs_rope_fwd", "xs_rope_append_paged", "xs_paged_step", "xs_attn_paged_plan", "xs_attn_paged_fwd")
+    names = ("xs_rope_fwd", "xs_rope_append_paged", "xs_paged_step", "xs_attn_paged_plan", "xs_attn_paged_fwd",
+             "xs_rope_append_paged8", "xs_paged_read8", "xs_attn_paged8_plan", "xs_attn_paged8_fwd")
     _binding.bind(*(ctypes.cast(getattr(lib, name), _vp).value for name in names))
     return _binding
 
 
 def _bind_torch():
-    global _I32, _I64, _F32, _current_device, _raw_stream, _native
+    global _I32, _I64, _F32, _E4M3, _E8M0, _current_device, _raw_stream, _native
     import torch
     _native = _bind_native(torch)
     _DTYPES.update({torch.bfloat16: XS_DTYPE_BF16, torch.float16: XS_DTYPE_FP16})
@@ -478,6 +488,7 @@ def _bind_torch():
         _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     else:
         _current_device, _raw_stream = (lambda: -2), (lambda dev: 0)   # no tensor is on device -2
+    _E4M3, _E8M0 = torch.float8_e4m3fn, (torch.float8_e8m0fnu, torch.uint8)
     _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
@@ -530,9 +541,12 @@ def _vec(t, name, dtype, n, dev):
 
 
 # The argument structs of include/xsattn.h, packed in one go (no field of theirs needs padding):
-# xs_paged_cache is "2Q6q6i".
+# xs_paged_cache is "2Q6q6i", xs_paged_cache8 "4Q12q6i"; xs_paged_read8_args ends in four bytes of it.
 _APPEND_ARGS = struct.Struct("=7Q2Q6q6i4q2i")
 _ATTN_ARGS = {P: struct.Struct(f"=5Q{P}Q{8 * (XS_MAX_P - P)}x2Q6q6i2q9if") for P in range(1, XS_MAX_P + 1)}
+_APPEND8_ARGS = struct.Struct("=7Q4Q12q6i4q2i")
+_READ8_ARGS = struct.Struct("=5Q4Q12q6i3q3i4x")
+_ATTN8_ARGS = {P: struct.Struct(f"=5Q{P}Q{8 * (XS_MAX_P - P)}x4Q12q6i2q9if") for P in range(1, XS_MAX_P + 1)}
 
 
 def _cache(t, name, dtype, dev):
@@ -651,6 +665,7 @@ class PagedWorkspace:
         self.ptr = (self._buf.data_ptr() + 255) & ~255
         self._dims = (n, H, Hkv, D, self.ptr, self.nbytes)
         self.planned = None   # (max_q, causal, window) of the plan
+        self.cache8 = False   # the plan is one of xs_attn_paged8_plan
 
     def __reduce__(self):   # a copy is a new workspace without a plan
         return PagedWorkspace, (self.n, self.H, self.Hkv, self.D, self._buf.device)
@@ -661,20 +676,25 @@ def xs_attn_paged_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, cau
     """Divide the attention of a step among the SMs: ``cu_q`` int32 [n + 1], ``kv_lens`` int32 [n]
     on the device; ``max_q`` an upper estimate of a sequence's new tokens; ``causal`` and
     ``window`` (0: none) as the attention is to use them."""
-    w, causal = workspace, 1 if causal else 0
+    _plan_call("xs_attn_paged_plan", _native and _native.plan, cu_q, kv_lens, max_q, workspace, causal, window, stream)
+    workspace.cache8 = False
+
+
+def _plan_call(where, native, cu_q, kv_lens, max_q, w, causal, window, stream):
+    causal = 1 if causal else 0
     code = None
-    if _native is not None:
-        code = _native.plan(cu_q, kv_lens, max_q, w._buf, w._dims, causal, window, _handle(stream))
+    if native is not None:
+        code = native(cu_q, kv_lens, max_q, w._buf, w._dims, causal, window, _handle(stream))
     if code is None:
         dev = _device()
         _on_device(w._buf, "workspace", dev)
         for x in (max_q, window):
-            _c_int(x, XS_ERR_SHAPE, "xs_attn_paged_plan")
-        code = lib.xs_attn_paged_plan(_vec(cu_q, "cu_q", _I32, w.n + 1, dev), _vec(kv_lens, "kv_lens", _I32, w.n, dev),
-                                      w.n, w.H, w.Hkv, w.D, max_q, causal, window, w.ptr, w.nbytes,
-                                      _stream_of(stream, dev))
+            _c_int(x, XS_ERR_SHAPE, where)
+        code = getattr(lib, where)(_vec(cu_q, "cu_q", _I32, w.n + 1, dev), _vec(kv_lens, "kv_lens", _I32, w.n, dev),
+                                   w.n, w.H, w.Hkv, w.D, max_q, causal, window, w.ptr, w.nbytes,
+                                   _stream_of(stream, dev))
     if code:
-        _check(code, "xs_attn_paged_plan")
+        _check(code, where)
     w.planned = (max_q, causal, window)
 
 
@@ -684,24 +704,36 @@ def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale
     each, any strides with D contiguous) as ``workspace`` plans it.  ``block_table`` int32 [n, width];
     ``layout`` XS_LAYOUT_A2A (P shards [T/P, H, D]), XS_LAYOUT_CONTIGUOUS (one [T, H, D] tensor) or
     XS_LAYOUT_HEADS (P head shards [T, H/P, D]); ``lse``: fp32 [T, H] or None."""
-    if _native is not None:
+    if _native is not None and not workspace.cache8:
         code = _native.attn(q, k_cache, v_cache, block_table, layout, outs, scale, workspace._buf, workspace._dims,
                             workspace.planned, lse, _handle(stream))
         if code is not None:
             return _check(code, "xs_attn_paged_fwd") if code else None
     w, dev, dt = workspace, _device(), q.dtype
-    if w.planned is None:
-        raise ValueError("xs_attn_paged_fwd: the workspace has no plan (call xs_attn_paged_plan first)")
+    _planned(w, False, "xs_attn_paged_fwd")
+    kc, vc = _cache(k_cache, "k_cache", dt, dev), _cache(v_cache, "v_cache", dt, dev)
+    if v_cache.shape != k_cache.shape:
+        _same("xs_attn_paged_fwd", tuple(k_cache.shape), tuple(v_cache.shape))
+    _attn_call("xs_attn_paged_fwd", _ATTN_ARGS, q, k_cache.shape, (k_cache.data_ptr(), v_cache.data_ptr(), *kc, *vc),
+               (_dtype_of(q, "q"), 0), block_table, layout, outs, scale, w, lse, stream, dev)
+
+
+def _planned(w, cache8, where):
+    if w.planned is None or w.cache8 != cache8:
+        plan = "xs_attn_paged8_plan" if cache8 else "xs_attn_paged_plan"
+        raise ValueError(f"{where}: the workspace has no plan (call {plan} first)")
+
+
+def _attn_call(where, packs, q, shape, cache, tail, block_table, layout, outs, scale, w, lse, stream, dev):
+    """Checks that the attention over either cache shares, and the call: `cache` are the struct's fields
+    before the cache's extents, `tail` those behind them."""
     max_q, causal, window = w.planned
-    D, n = w.D, w.n
-    dtype = _dtype_of(q, "q")
+    D, n, dt = w.D, w.n, q.dtype
     T, H, qs = _rows(q, "q", dt, D, dev)
     _on_device(w._buf, "workspace", dev)
-    kc, vc = _cache(k_cache, "k_cache", dt, dev), _cache(v_cache, "v_cache", dt, dev)
-    shape = k_cache.shape
     n_pages, page_size, Hkv, Dc = shape
-    if H != w.H or Hkv != w.Hkv or Dc != D or v_cache.shape != shape:
-        _same("xs_attn_paged_fwd", (H, Hkv, Dc, tuple(shape)), (w.H, w.Hkv, D, tuple(v_cache.shape)))
+    if H != w.H or Hkv != w.Hkv or Dc != D:
+        _same(where, (H, Hkv, Dc), (w.H, w.Hkv, D))
     if block_table.dim() != 2 or block_table.dtype is not _I32 or block_table.shape[0] != n:
         raise TypeError(f"block_table must be an int32 tensor [{n}, width]")
     _on_device(block_table, "block_table", dev)
@@ -724,15 +756,127 @@ def xs_attn_paged_fwd(q, k_cache, v_cache, block_table, layout: int, outs, scale
             raise TypeError("lse must be a contiguous float32 tensor [T, H]")
         _on_device(lse, "lse", dev)
         z = lse.data_ptr()
-    pack = _ATTN_ARGS.get(P)
+    pack = packs.get(P)
     if pack is None:
-        raise XsError(XS_ERR_SHAPE if P < 1 else XS_ERR_TOO_MANY_RANKS, "xs_attn_paged_fwd")
+        raise XsError(XS_ERR_SHAPE if P < 1 else XS_ERR_TOO_MANY_RANKS, where)
     args = pack.pack(q.data_ptr(), block_table.data_ptr(), z, w.ptr, w.nbytes, *[o.data_ptr() for o in outs],
-                     k_cache.data_ptr(), v_cache.data_ptr(), *kc, *vc, n_pages, page_size, Hkv, D, dtype, 0, qs, ts,
-                     layout, P, T, H, n, width, max_q, causal, window, scale)
-    code = lib.xs_attn_paged_fwd(args, _stream_of(stream, dev))
+                     *cache, n_pages, page_size, Hkv, D, *tail, qs, ts, layout, P, T, H, n, width,
+                     max_q, causal, window, scale)
+    code = getattr(lib, where)(args, _stream_of(stream, dev))
     if code:
-        _check(code, "xs_attn_paged_fwd")
+        _check(code, where)
+
+
+def _cache8(where, k_cache, v_cache, k_scales, v_scales, dev):
+    """The fields of xs_paged_cache8 up to `block`, and the cache's shape."""
+    kc, vc = _cache(k_cache, "k_cache", _E4M3, dev), _cache(v_cache, "v_cache", _E4M3, dev)
+    shape = k_cache.shape
+    n_pages, page_size, Hkv, D = shape
+    if v_cache.shape != shape:
+        _same(where, tuple(shape), tuple(v_cache.shape))
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t.dim() != 3 or t.dtype not in _E8M0:
+            raise TypeError(f"{name} must be a float8_e8m0fnu (or uint8) tensor [n_pages, page_size / block, Hkv]")
+        _on_device(t, name, dev)
+        if t.shape != k_scales.shape or t.shape[0] != n_pages or t.shape[2] != Hkv or t.shape[1] < 1 or page_size % t.shape[1]:
+            raise TypeError(f"{name} must have the shape [n_pages, page_size / block, Hkv]")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), *kc, *vc, *k_scales.stride(),
+            *v_scales.stride()), page_size // k_scales.shape[1], shape
+
+
+def xs_rope_append_paged8(q, k, v, positions, slots, q_out, k_cache, v_cache, k_scales, v_scales, rope: Rope | None,
+                          stream=None) -> None:
+    """Rotate the new tokens' ``q`` [T, H, D] into ``q_out`` and store ``k`` (rotated) and ``v`` [T, Hkv, D]
+    quantised into the slots of an 8-bit cache: ``k_cache``, ``v_cache`` float8_e4m3fn [n_pages, page_size,
+    Hkv, D], ``k_scales``, ``v_scales`` float8_e8m0fnu [n_pages, page_size / block, Hkv] (include/xsattn.h has
+    the rules).  ``positions`` int32 [T], ``slots`` int64 [T] (outside the cache: not stored).  ``rope=None``:
+    nothing is rotated, ``q``, ``q_out`` and ``positions`` are None."""
+    where = "xs_rope_append_paged8"
+    if _native is not None and rope is not None:
+        code = _native.append8(q, k, v, positions, slots, q_out, k_cache, v_cache, k_scales, v_scales, rope.ptr, rope.D,
+                               _handle(stream))
+        if code is not None:
+            return _check(code, where) if code else None
+    dev, dt = _device(), k.dtype
+    dtype = _dtype_of(k, "k")
+    cache, block, shape = _cache8(where, k_cache, v_cache, k_scales, v_scales, dev)
+    D = shape[3]
+    T, Hkv, ks = _rows(k, "k", dt, D, dev)
+    Tv, Hv, vs = _rows(v, "v", dt, D, dev)
+    if rope is None:
+        if q is not None or q_out is not None or positions is not None:
+            raise TypeError(f"{where}: without a rotation q, q_out and positions must be None")
+        To, H, qs, os_, q_p, o_p, pos_p, rope_p = T, 0, 0, 0, 0, 0, 0, 0
+    else:
+        To, H, qs = _rows(q, "q", dt, D, dev)
+        To2, Ho, os_ = _rows(q_out, "q_out", dt, D, dev)
+        if (To, H) != (To2, Ho) or rope.D != D:
+            _same(where, (To, H, rope.D), (To2, Ho, D))
+        q_p, o_p, pos_p, rope_p = q.data_ptr(), q_out.data_ptr(), _vec(positions, "positions", _I32, T, dev), rope.ptr
+    if T != To or T != Tv or Hkv != Hv or Hkv != shape[2]:
+        _same(where, [(T, Hkv), (T, Hkv), T], [(Tv, Hv), (T, shape[2]), To])
+    args = _APPEND8_ARGS.pack(q_p, k.data_ptr(), v.data_ptr(), pos_p, _vec(slots, "slots", _I64, T, dev), o_p, rope_p, *cache,
+                              *shape, block, dtype, qs, ks, vs, os_, T, H)
+    code = lib.xs_rope_append_paged8(args, _stream_of(stream, dev))
+    if code:
+        _check(code, where)
+
+
+def xs_paged_read8(k_cache, v_cache, k_scales, v_scales, block_table, cu_rows, first, k_out, v_out, stream=None) -> None:
+    """Elements of an 8-bit cache in 16 bits: rows ``cu_rows[i]`` .. ``cu_rows[i + 1]`` of ``k_out`` and
+    ``v_out`` [T, Hkv, D] are the tokens of sequence i from position ``first[i]`` on (``first=None``: 0).
+    ``block_table`` int32 [n, width], ``cu_rows`` int32 [n + 1], ``first`` int32 [n]."""
+    where = "xs_paged_read8"
+    if _native is not None:
+        code = _native.read8(k_cache, v_cache, k_scales, v_scales, block_table, cu_rows, first, k_out, v_out,
+                             _handle(stream))
+        if code is not None:
+            return _check(code, where) if code else None
+    dev, dt = _device(), k_out.dtype
+    dtype = _dtype_of(k_out, "k_out")
+    cache, block, shape = _cache8(where, k_cache, v_cache, k_scales, v_scales, dev)
+    T, Hkv, ks = _rows(k_out, "k_out", dt, shape[3], dev)
+    Tv, Hv, vs = _rows(v_out, "v_out", dt, shape[3], dev)
+    if T != Tv or Hkv != Hv or Hkv != shape[2]:
+        _same(where, [(T, Hkv)] * 2, [(Tv, Hv), (T, shape[2])])
+    if block_table.dim() != 2 or block_table.dtype is not _I32:
+        raise TypeError("block_table must be an int32 tensor [n, width]")
+    _on_device(block_table, "block_table", dev)
+    n, width = block_table.shape
+    ts, ts1 = block_table.stride()
+    if ts1 != 1 and width > 1:
+        raise TypeError("block_table: the entries of a row must be contiguous")
+    args = _READ8_ARGS.pack(block_table.data_ptr(), _vec(cu_rows, "cu_rows", _I32, n + 1, dev),
+                            0 if first is None else _vec(first, "first", _I32, n, dev), k_out.data_ptr(), v_out.data_ptr(),
+                            *cache, *shape, block, dtype, ks, vs, ts, T, n, width)
+    code = lib.xs_paged_read8(args, _stream_of(stream, dev))
+    if code:
+        _check(code, where)
+
+
+def xs_attn_paged8_plan(cu_q, kv_lens, max_q: int, workspace: PagedWorkspace, causal: bool = True, window: int = 0,
+                        stream=None) -> None:
+    """:func:`xs_attn_paged_plan` for the attention over an 8-bit cache."""
+    w = workspace
+    _plan_call("xs_attn_paged8_plan", _native and _native.plan8, cu_q, kv_lens, max_q, w, causal, window, stream)
+    w.cache8 = True
+
+
+def xs_attn_paged8_fwd(q, k_cache, v_cache, k_scales, v_scales, block_table, layout: int, outs, scale: float,
+                       workspace: PagedWorkspace, lse=None, stream=None) -> None:
+    """:func:`xs_attn_paged_fwd` over an 8-bit cache (as in :func:`xs_rope_append_paged8`), as
+    :func:`xs_attn_paged8_plan` plans it."""
+    where = "xs_attn_paged8_fwd"
+    if _native is not None and workspace.cache8:
+        code = _native.attn8(q, k_cache, v_cache, k_scales, v_scales, block_table, layout, outs, scale, workspace._buf,
+                             workspace._dims, workspace.planned, lse, _handle(stream))
+        if code is not None:
+            return _check(code, where) if code else None
+    dev = _device()
+    _planned(workspace, True, where)
+    cache, block, shape = _cache8(where, k_cache, v_cache, k_scales, v_scales, dev)
+    _attn_call(where, _ATTN8_ARGS, q, shape, cache, (block, _dtype_of(q, "q")), block_table, layout, outs, scale, workspace,
+               lse, stream, dev)
 
 
 def attn_a2a(q, k, v, P: int, scale: float | None = None, stream=None, workspace=None):

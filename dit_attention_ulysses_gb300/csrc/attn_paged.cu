@@ -199,7 +199,7 @@ __device__ void producer_k_role(const CUtensorMap* tq, const CUtensorMap* tk, co
     const int n_seqs = h.n_seqs, per_slot = h.slot;
     int waves = h.waves - (static_cast<int>(blockIdx.x) >= h.slot_ctas ? 1 : 0);
     if (h.n != a.n || h.H != a.H || h.Hkv != a.Hkv || h.D != D || h.tokens != tokens || h.block != BLOCK_N ||
-        h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window) {
+        h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window || h.cache8 != 0) {
         if (lane == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, h.n, h.tokens, h.grid);
         range.end = range.start;
         waves = 0;

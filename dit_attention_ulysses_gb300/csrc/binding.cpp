@@ -28,6 +28,10 @@ decltype(&xs_rope_append_paged) append_fwd;
 decltype(&xs_paged_step) step_fwd;
 decltype(&xs_attn_paged_plan) plan_fwd;
 decltype(&xs_attn_paged_fwd) attn_fwd;
+decltype(&xs_rope_append_paged8) append8_fwd;
+decltype(&xs_paged_read8) read8_fwd;
+decltype(&xs_attn_paged8_plan) plan8_fwd;
+decltype(&xs_attn_paged8_fwd) attn8_fwd;
 
 struct NotAccepted {};
 
@@ -118,6 +122,37 @@ xs_paged_cache cache_of(PyObject* ko, PyObject* vo, at::ScalarType type, int dty
     c.page_size = extent(k, 1);
     c.Hkv = extent(k, 2);
     c.D = extent(k, 3);
+    c.dtype = dtype;
+    return c;
+}
+
+// A cache of e4m3 numbers, and its scales (e8m0, or their bytes).
+xs_paged_cache8 cache8_of(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso, int dtype, int dev) {
+    const at::Tensor &k = tensor(ko), &v = tensor(vo), &ks = tensor(kso), &vs = tensor(vso);
+    need(k.dim() == 4 && k.scalar_type() == at::kFloat8_e4m3fn && k.get_device() == dev && k.stride(3) == 1);
+    need(v.scalar_type() == at::kFloat8_e4m3fn && v.get_device() == dev && v.sizes() == k.sizes() && v.stride(3) == 1);
+    xs_paged_cache8 c;
+    std::memset(&c, 0, sizeof c);
+    c.n_pages = extent(k, 0);
+    c.page_size = extent(k, 1);
+    c.Hkv = extent(k, 2);
+    c.D = extent(k, 3);
+    for (const at::Tensor* t : {&ks, &vs}) {
+        need(t->scalar_type() == at::kFloat8_e8m0fnu || t->scalar_type() == at::kByte);
+        need(t->dim() == 3 && t->size(0) == c.n_pages && t->size(2) == c.Hkv && t->size(1) == ks.size(1) && t->get_device() == dev);
+    }
+    need(ks.size(1) >= 1 && c.page_size % ks.size(1) == 0);
+    c.k = k.data_ptr();
+    c.v = v.data_ptr();
+    c.k_scales = ks.data_ptr();
+    c.v_scales = vs.data_ptr();
+    for (int i = 0; i < 3; ++i) {
+        c.k_strides[i] = k.stride(i);
+        c.v_strides[i] = v.stride(i);
+        c.k_scale_strides[i] = ks.stride(i);
+        c.v_scale_strides[i] = vs.stride(i);
+    }
+    c.block = static_cast<int>(c.page_size / ks.size(1));
     c.dtype = dtype;
     return c;
 }
@@ -219,47 +254,48 @@ Work work_of(PyObject* buffer, PyObject* dims, int dev) {
 }
 
 // cu_q, kv_lens, max_q, buffer, dims, causal, window, stream
-PyObject* plan(PyObject* const* a) {
+PyObject* plan_with(decltype(&xs_attn_paged_plan) f, PyObject* const* a) {
     const int dev = device_of(tensor(a[0]));
     const Work w = work_of(a[3], a[4], dev);
     const int *cu = ints(a[0], int64_t(w.n) + 1, dev), *kv = ints(a[1], w.n, dev);
     const int max_q = int32(a[2]), causal = int32(a[5]), window = int32(a[6]);
     void* stream = stream_of(a[7], dev);
-    return call([&] { return plan_fwd(cu, kv, w.n, w.H, w.Hkv, w.D, max_q, causal, window, w.p, w.bytes, stream); });
+    return call([&] { return f(cu, kv, w.n, w.H, w.Hkv, w.D, max_q, causal, window, w.p, w.bytes, stream); });
 }
 
-// q, k_cache, v_cache, block_table, layout, outs, scale, buffer, dims, planned, lse, stream
-PyObject* attn(PyObject* const* a) {
-    const at::Tensor &q = tensor(a[0]), &table = tensor(a[3]);
+PyObject* plan(PyObject* const* a) { return plan_with(plan_fwd, a); }
+PyObject* plan8(PyObject* const* a) { return plan_with(plan8_fwd, a); }
+
+// The arguments of an attention beside q and the cache, from `a` = block_table, layout, outs, scale, buffer, dims,
+// planned, lse.
+template <typename Args>
+void fill_attn(Args& g, const at::Tensor& q, PyObject* const* a, int dev) {
+    const at::Tensor& table = tensor(a[0]);
     const at::ScalarType type = q.scalar_type();
-    const int dtype = dtype_of(q), dev = device_of(q);
-    const Work w = work_of(a[7], a[8], dev);
+    const Work w = work_of(a[4], a[5], dev);
     const Rows qr = rows(q, type, w.D, dev);
-    xs_attn_paged_args g;
-    std::memset(&g, 0, sizeof g);
-    g.cache = cache_of(a[1], a[2], type, dtype, dev);
     need(qr.H == w.H && g.cache.Hkv == w.Hkv && g.cache.D == w.D);
     need(table.dim() == 2 && table.scalar_type() == at::kInt && table.size(0) == w.n && table.get_device() == dev);
     g.table_width = extent(table, 1);
     need(table.stride(1) == 1 || g.table_width <= 1);
-    g.layout = int32(a[4]);
-    need(PyList_CheckExact(a[5]) || PyTuple_CheckExact(a[5]));
-    const Py_ssize_t P = PySequence_Fast_GET_SIZE(a[5]);
+    g.layout = int32(a[1]);
+    need(PyList_CheckExact(a[2]) || PyTuple_CheckExact(a[2]));
+    const Py_ssize_t P = PySequence_Fast_GET_SIZE(a[2]);
     need(P >= 1 && P <= XS_MAX_P);
     const bool one = g.layout == XS_LAYOUT_CONTIGUOUS, shards = g.layout == XS_LAYOUT_A2A;
     const int64_t out_T = shards ? qr.T / P : qr.T, out_H = one || shards ? qr.H : qr.H / P;
     for (Py_ssize_t i = 0; i < P; ++i) {
-        const at::Tensor& o = tensor(PySequence_Fast_GET_ITEM(a[5], i));
+        const at::Tensor& o = tensor(PySequence_Fast_GET_ITEM(a[2], i));
         need(o.dim() == 3 && o.size(0) == out_T && o.size(1) == out_H && o.size(2) == w.D && o.scalar_type() == type &&
              o.is_contiguous() && o.get_device() == dev);
         g.outs[i] = o.data_ptr();
     }
-    need(PyFloat_CheckExact(a[6]));
-    const double scale = PyFloat_AS_DOUBLE(a[6]);
+    need(PyFloat_CheckExact(a[3]));
+    const double scale = PyFloat_AS_DOUBLE(a[3]);
     need(std::fabs(scale) <= FLT_MAX);
-    need(PyTuple_CheckExact(a[9]) && PyTuple_GET_SIZE(a[9]) == 3);
-    if (a[10] != Py_None) {
-        const at::Tensor& z = tensor(a[10]);
+    need(PyTuple_CheckExact(a[6]) && PyTuple_GET_SIZE(a[6]) == 3);
+    if (a[7] != Py_None) {
+        const at::Tensor& z = tensor(a[7]);
         need(z.scalar_type() == at::kFloat && z.dim() == 2 && z.size(0) == qr.T && z.size(1) == qr.H && z.is_contiguous() &&
              z.get_device() == dev);
         g.lse = static_cast<float*>(z.data_ptr());
@@ -274,22 +310,98 @@ PyObject* attn(PyObject* const* a) {
     g.T = qr.T;
     g.H = qr.H;
     g.n = w.n;
-    g.max_q = int32(PyTuple_GET_ITEM(a[9], 0));
-    g.causal = int32(PyTuple_GET_ITEM(a[9], 1));
-    g.window = int32(PyTuple_GET_ITEM(a[9], 2));
+    g.max_q = int32(PyTuple_GET_ITEM(a[6], 0));
+    g.causal = int32(PyTuple_GET_ITEM(a[6], 1));
+    g.window = int32(PyTuple_GET_ITEM(a[6], 2));
     g.scale = static_cast<float>(scale);
+}
+
+// q, k_cache, v_cache, block_table, layout, outs, scale, buffer, dims, planned, lse, stream
+PyObject* attn(PyObject* const* a) {
+    const at::Tensor& q = tensor(a[0]);
+    const int dtype = dtype_of(q), dev = device_of(q);
+    xs_attn_paged_args g;
+    std::memset(&g, 0, sizeof g);
+    g.cache = cache_of(a[1], a[2], q.scalar_type(), dtype, dev);
+    fill_attn(g, q, a + 3, dev);
     void* stream = stream_of(a[11], dev);
     return call([&] { return attn_fwd(&g, stream); });
 }
 
-// The addresses of the five entry points, in the order below.
+// q, k_cache, v_cache, k_scales, v_scales, block_table, layout, outs, scale, buffer, dims, planned, lse, stream
+PyObject* attn8(PyObject* const* a) {
+    const at::Tensor& q = tensor(a[0]);
+    const int dtype = dtype_of(q), dev = device_of(q);
+    xs_attn_paged8_args g;
+    std::memset(&g, 0, sizeof g);
+    g.cache = cache8_of(a[1], a[2], a[3], a[4], dtype, dev);
+    fill_attn(g, q, a + 5, dev);
+    void* stream = stream_of(a[13], dev);
+    return call([&] { return attn8_fwd(&g, stream); });
+}
+
+// q, k, v, positions, slots, q_out, k_cache, v_cache, k_scales, v_scales, rope, D, stream
+PyObject* append8(PyObject* const* a) {
+    const at::Tensor& q = tensor(a[0]);
+    const at::ScalarType type = q.scalar_type();
+    const int dtype = dtype_of(q), dev = device_of(q), D = int32(a[11]);
+    const Rows qr = rows(q, type, D, dev), k = rows(tensor(a[1]), type, D, dev), v = rows(tensor(a[2]), type, D, dev),
+               o = rows(tensor(a[5]), type, D, dev);
+    xs_rope_append8_args g;
+    std::memset(&g, 0, sizeof g);
+    g.cache = cache8_of(a[6], a[7], a[8], a[9], dtype, dev);
+    need(qr.T == k.T && qr.T == v.T && qr.T == o.T && qr.H == o.H && k.H == v.H && g.cache.Hkv == k.H && g.cache.D == D);
+    g.q = qr.p;
+    g.k = k.p;
+    g.v = v.p;
+    g.positions = ints(a[3], qr.T, dev);
+    g.slots = vec<long long>(a[4], at::kLong, qr.T, dev);
+    g.q_out = o.p;
+    g.rope = static_cast<const xs_rope*>(address(a[10]));
+    g.q_stride = qr.stride;
+    g.k_stride = k.stride;
+    g.v_stride = v.stride;
+    g.q_out_stride = o.stride;
+    g.T = qr.T;
+    g.H = qr.H;
+    void* stream = stream_of(a[12], dev);
+    return call([&] { return append8_fwd(&g, stream); });
+}
+
+// k_cache, v_cache, k_scales, v_scales, block_table, cu_rows, first, k_out, v_out, stream
+PyObject* read8(PyObject* const* a) {
+    const at::Tensor &ko = tensor(a[7]), &table = tensor(a[4]);
+    const int dtype = dtype_of(ko), dev = device_of(ko);
+    xs_paged_read8_args g;
+    std::memset(&g, 0, sizeof g);
+    g.cache = cache8_of(a[0], a[1], a[2], a[3], dtype, dev);
+    const Rows k = rows(ko, ko.scalar_type(), g.cache.D, dev), v = rows(tensor(a[8]), ko.scalar_type(), g.cache.D, dev);
+    need(k.T == v.T && k.H == v.H && k.H == g.cache.Hkv);
+    need(table.dim() == 2 && table.scalar_type() == at::kInt && table.get_device() == dev);
+    g.n = extent(table, 0);
+    g.table_width = extent(table, 1);
+    need(table.stride(1) == 1 || g.table_width <= 1);
+    g.block_table = static_cast<const int*>(table.data_ptr());
+    g.cu_rows = ints(a[5], int64_t(g.n) + 1, dev);
+    g.first = a[6] == Py_None ? nullptr : ints(a[6], g.n, dev);
+    g.k_out = k.p;
+    g.v_out = v.p;
+    g.k_stride = k.stride;
+    g.v_stride = v.stride;
+    g.table_stride = table.stride(0);
+    g.T = k.T;
+    void* stream = stream_of(a[9], dev);
+    return call([&] { return read8_fwd(&g, stream); });
+}
+
+// The addresses of the nine entry points, in the order below.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    unsigned long long p[5];
-    for (Py_ssize_t i = 0; i < 5; ++i) {
-        p[i] = n == 5 ? PyLong_AsUnsignedLongLong(args[i]) : 0;
+    unsigned long long p[9];
+    for (Py_ssize_t i = 0; i < 9; ++i) {
+        p[i] = n == 9 ? PyLong_AsUnsignedLongLong(args[i]) : 0;
         if (PyErr_Occurred()) return nullptr;
         if (p[i] == 0) {
-            PyErr_SetString(PyExc_ValueError, "five addresses");
+            PyErr_SetString(PyExc_ValueError, "nine addresses");
             return nullptr;
         }
     }
@@ -298,6 +410,10 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     step_fwd = reinterpret_cast<decltype(step_fwd)>(p[2]);
     plan_fwd = reinterpret_cast<decltype(plan_fwd)>(p[3]);
     attn_fwd = reinterpret_cast<decltype(attn_fwd)>(p[4]);
+    append8_fwd = reinterpret_cast<decltype(append8_fwd)>(p[5]);
+    read8_fwd = reinterpret_cast<decltype(read8_fwd)>(p[6]);
+    plan8_fwd = reinterpret_cast<decltype(plan8_fwd)>(p[7]);
+    attn8_fwd = reinterpret_cast<decltype(attn8_fwd)>(p[8]);
     Py_RETURN_NONE;
 }
 
@@ -313,6 +429,10 @@ PyMethodDef methods[] = {
     {"step", fast(entry<step, 13>), METH_FASTCALL, "xs_paged_step"},
     {"plan", fast(entry<plan, 8>), METH_FASTCALL, "xs_attn_paged_plan"},
     {"attn", fast(entry<attn, 12>), METH_FASTCALL, "xs_attn_paged_fwd"},
+    {"append8", fast(entry<append8, 13>), METH_FASTCALL, "xs_rope_append_paged8"},
+    {"read8", fast(entry<read8, 10>), METH_FASTCALL, "xs_paged_read8"},
+    {"plan8", fast(entry<plan8, 8>), METH_FASTCALL, "xs_attn_paged8_plan"},
+    {"attn8", fast(entry<attn8, 14>), METH_FASTCALL, "xs_attn_paged8_fwd"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Serving calls on tensors.", -1, methods, nullptr, nullptr, nullptr,

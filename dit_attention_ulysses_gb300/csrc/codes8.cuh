@@ -1,0 +1,52 @@
+// e4m3 numbers and their e8m0 scales in registers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace xs {
+
+constexpr int LEAST_SCALE = 63;   // the smallest scale byte that is written: 2^-64
+
+// 2^(byte - 127), byte 1 .. 254 (0: 0)
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Scale byte of values up to `largest` (the bits of a non-negative float): the least s >= 63 with
+// largest <= 448 * 2^(s - 127) = 1.75 * 2^(s - 119).  The sum carries into the exponent if the
+// significand is above 1.75.
+__device__ __forceinline__ int scale_byte(uint32_t largest) {
+    const int s = static_cast<int>((largest + 0x1fffffu) >> 23) - 8;
+    return s > LEAST_SCALE ? s : LEAST_SCALE;
+}
+
+// Two e4m3 numbers (a byte each) as two fp16 ones: exact.
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t codes_to_f16x2_high(uint32_t four) {
+    uint32_t r;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(r) : "r"(four));
+    return r;
+}
+
+// Four values to the nearest e4m3 numbers (ties to even), the first in the lowest byte.
+__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n.reg .b16 lo, hi;\ncvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+        "mov.b32 %0, {lo, hi};\n}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+__device__ __forceinline__ float2 f16x2_values(uint32_t w) {
+    float2 f;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.f32.f16 %0, lo;\ncvt.f32.f16 %1, hi;\n}" : "=f"(f.x), "=f"(f.y) : "r"(w));
+    return f;
+}
+
+}  // namespace xs

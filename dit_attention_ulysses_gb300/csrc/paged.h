@@ -51,6 +51,52 @@ struct RopeArgs {
 
 cudaError_t launch_rope(const RopeArgs& a, int dtype, int layout, bool append, int num_sms, cudaStream_t stream);
 
+// ---- the 8-bit cache: quantising append, read back (paged8.cu)
+// Codes and scales of K or V: bytes between pages, tokens (scales: blocks) and heads.
+struct Codes8 {
+    uint8_t* code;
+    uint8_t* scale;
+    long long cs[3];
+    long long ss[3];
+};
+
+struct Append8Args {
+    const void* q;            // [T, H, D], rows q_stride elements apart; H == 0: none
+    const void* k;            // [T, Hkv, D]
+    const void* v;
+    void* q_out;
+    const int* positions;     // [T]; rot == 0: not read
+    const long long* slots;   // [T]
+    Codes8 kc, vc;
+    long long q_stride, k_stride, v_stride, qo_stride;
+    long long n_slots;
+    int T, H, Hkv, D, rot;
+    int page_shift, block_shift;
+    // set by the launch function
+    int window;               // rows whose runs a block writes
+    int kv_per, kv_groups;    // heads of K and V (2 Hkv in all) per block
+    int q_per;                // heads of q per block
+    float magnitude;
+    unsigned long long turns[64];
+};
+
+cudaError_t launch_append8(const Append8Args& a, int dtype, int layout, int num_sms, cudaStream_t stream);
+
+struct Read8Args {
+    const int* table;         // [n], rows table_stride entries apart
+    const int* cu;            // [n + 1]
+    const int* first;         // [n] or null
+    void* k_out;              // [T, Hkv, D], rows k_stride elements apart
+    void* v_out;
+    Codes8 kc, vc;
+    long long k_stride, v_stride, table_stride;
+    int T, n, width, n_pages, Hkv, D;
+    int page_shift, block_shift;
+    FastDiv fd_row;           // 16-channel pieces of a row of K (Hkv * D / 16)
+};
+
+cudaError_t launch_read8(const Read8Args& a, int dtype, int num_sms, cudaStream_t stream);
+
 // ---- block tables and slot maps (paged_step.cu)
 constexpr int MAX_PAGED_SEQS = 8192;
 struct StepArgs {
@@ -91,6 +137,7 @@ struct PagedTiling {
     int l2_bytes;   // (waves) keys and values beyond this do not stay in L2 for long
     // below few_keys keys per CTA on average (waves == 0) these replace start_cost and least
     int few_keys, few_start_cost, few_least;
+    int cache8;     // for the 8-bit cache
 };
 constexpr int MAX_PAGED_WAVES = 64;
 
@@ -131,7 +178,8 @@ struct alignas(16) PagedHeader {
     int waves;            // slots of every CTA before its range
     int slot;             // tiles per slot
     int slot_ctas;        // CTAs that have a slot in the last wave
-    int unused[2];
+    int cache8;           // for the 8-bit cache
+    int unused;
 };
 constexpr int PAGED_MAGIC_SITE = 3;   // error record: the plan does not match the call
 
@@ -171,6 +219,14 @@ struct PagedAttnArgs {
     FastDiv fd_G;
 };
 
+// Over an 8-bit cache: scales in bytes, strides between pages, blocks and heads.
+struct PagedAttn8Args : PagedAttnArgs {
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    long long k_scale_strides[3], v_scale_strides[3];
+    int block_shift;
+};
+
 // tk, tv: a cache as the 5-D tensor (element, token % 8, 64-channel panel, token / 8, page), the
 // head in the first coordinate.  A box is one page's tokens of one head (at most a block's), and
 // lands as [token / 8][panel][token % 8][64 channels]: 1024-byte swizzle atoms, so that any
@@ -183,6 +239,11 @@ cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv,
 // Tiles of up to 128 packed rows; tq covers [T, Hkv, G, D] in boxes of one tile's rows.
 cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PagedAttnArgs& a, int dtype, cudaStream_t stream);
+
+// tk, tv: an 8-bit cache as the 3-D tensor (element, token, page), the head in the first coordinate; a box, one
+// page's tokens of one head, lands as [token][channel] with a row's 16-byte pieces swizzled over its D bytes.
+cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
+                                    cudaStream_t stream);
 
 cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);

@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
         h.waves = waves;
         h.slot = static_cast<int>(per_slot);
         h.slot_ctas = slot_ctas;
+        h.cache8 = a.tile.cache8;
         *a.work.header = h;
     }
 }

@@ -30,6 +30,7 @@
 
 #include "paged.h"
 #include "ptx.cuh"
+#include "rope_tile.cuh"
 
 namespace xs {
 namespace {
@@ -37,58 +38,6 @@ namespace {
 constexpr int ROPE_THREADS = 128;
 constexpr int ROPE_UNROLL = 4;
 constexpr int ROPE_RESIDENT = 5;   // blocks that an SM holds (88 .. 96 registers)
-
-template <bool F16>
-__device__ __forceinline__ void widen(uint32_t w, float& lo, float& hi) {
-    if constexpr (F16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        lo = f.x;
-        hi = f.y;
-    } else {
-        lo = __uint_as_float(w << 16);
-        hi = __uint_as_float(w & 0xffff0000u);
-    }
-}
-
-// Round to nearest even: the one rounding of the operator.
-template <bool F16>
-__device__ __forceinline__ uint32_t narrow(float lo, float hi) {
-    if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-
-struct Chunk2 {
-    uint4 a, b;
-};
-
-template <bool F16, bool INTERLEAVED>
-__device__ __forceinline__ void turn(Chunk2& x, const float (&c)[8], const float (&s)[8], bool rot_a, bool rot_b) {
-    uint32_t* wa = reinterpret_cast<uint32_t*>(&x.a);
-    uint32_t* wb = reinterpret_cast<uint32_t*>(&x.b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float a0, a1, b0, b1;
-        widen<F16>(wa[j], a0, a1);
-        widen<F16>(wb[j], b0, b1);
-        if constexpr (INTERLEAVED) {   // pairs inside each chunk
-            const uint32_t ra = narrow<F16>(a0 * c[j] - a1 * s[j], a0 * s[j] + a1 * c[j]);
-            const uint32_t rb = narrow<F16>(b0 * c[4 + j] - b1 * s[4 + j], b0 * s[4 + j] + b1 * c[4 + j]);
-            if (rot_a) wa[j] = ra;
-            if (rot_b) wb[j] = rb;
-        } else {                       // pairs across the two chunks
-            const float c0 = c[2 * j], c1 = c[2 * j + 1], s0 = s[2 * j], s1 = s[2 * j + 1];
-            if (rot_a) {
-                wa[j] = narrow<F16>(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-                wb[j] = narrow<F16>(a0 * s0 + b0 * c0, a1 * s1 + b1 * c1);
-            }
-        }
-    }
-}
 
 // Block: 128 / units tokens (blockIdx.x) x one group of heads (blockIdx.y).
 // Heads are numbered q 0 .. H-1, then (APPEND) k H .. H+Hkv-1, v H+Hkv .. H+2Hkv-1.
@@ -100,33 +49,12 @@ __global__ void __launch_bounds__(ROPE_THREADS, 1) rope_kernel(const __grid_cons
     const int tl = threadIdx.x / units, u = threadIdx.x - tl * units;
     const long long t = static_cast<long long>(blockIdx.x) * (ROPE_THREADS / units) + tl;
     if (t >= g.T) return;
-    // channel offsets of the thread's two chunks, and whether they rotate
     int oa, ob;
     bool rot_a, rot_b;
-    if constexpr (INTERLEAVED) {
-        oa = u * 8;
-        ob = (g.D >> 1) + u * 8;
-        rot_a = oa < g.rot;
-        rot_b = ob < g.rot;
-    } else {
-        const int ru = g.rot >> 4;   // rotating units; the others copy the rest of the head
-        const int base = u < ru ? 0 : g.rot, span = u < ru ? g.rot >> 1 : (g.D - g.rot) >> 1;
-        oa = base + (u < ru ? u : u - ru) * 8;
-        ob = oa + span;
-        rot_a = rot_b = u < ru;
-    }
+    rope_chunks<INTERLEAVED>(u, g.D, g.rot, oa, ob, rot_a, rot_b);
     float c[8], s[8];
     if (rot_a || rot_b) {
-        const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(g.positions[t]));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int pair = INTERLEAVED ? ((j < 4 ? oa : ob) >> 1) + (j & 3) : oa + j;
-            const unsigned long long turn64 = pos * g.turns[pair < 64 ? pair : 63];
-            const float half_turns = static_cast<float>(static_cast<int>(turn64 >> 32)) * 4.656612873077393e-10f;
-            sincospif(half_turns, &s[j], &c[j]);
-            c[j] *= g.magnitude;
-            s[j] *= g.grad ? -g.magnitude : g.magnitude;
-        }
+        rope_angles<INTERLEAVED>(g.positions[t], g.turns, oa, ob, g.magnitude, g.grad ? -g.magnitude : g.magnitude, c, s);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c[j] = s[j] = 0.0f;   // not used

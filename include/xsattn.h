@@ -605,6 +605,122 @@ typedef struct xs_attn_paged_args {
 int xs_attn_paged_fwd(const xs_attn_paged_args* args, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The cache in 8 bits.
+ *
+ * xs_paged_cache8 holds K and V as e4m3 numbers in pages as above, and for every block of
+ * `block` tokens of a page and every head a scale, a power of two in e8m0 (byte s stands for
+ * 2^(s - 127)); an element stands for its number times its block's scale.  A power of two,
+ * because e4m3 numbers are floating point: another factor would not make their relative
+ * rounding smaller, while a block whose range grows with a later token is rescaled by moving
+ * exponents, without a second rounding.  The library writes scales from 2^-64 on.
+ *
+ * A step uses it in place of the 16-bit cache: xs_paged_step, xs_attn_paged8_plan, then per
+ * layer xs_rope_append_paged8 and xs_attn_paged8_fwd; xs_paged_read8 gives elements back in
+ * 16 bits.  Pages that xs_paged_step hands on need no clearing: a block's first token sets its
+ * scale anew.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct xs_paged_cache8 {
+    void* k;
+    void* v;                  /* device, e4m3, [n_pages, page_size, Hkv, D], D contiguous    */
+    void* k_scales;
+    void* v_scales;           /* device, e8m0, [n_pages, page_size / block, Hkv]             */
+    long long k_strides[3];
+    long long v_strides[3];   /* bytes between pages, tokens, heads: multiples of 16, limits as
+                                 in xs_paged_cache                                           */
+    long long k_scale_strides[3];
+    long long v_scale_strides[3];   /* bytes between pages, blocks, heads: 1 .. 2^35         */
+    int n_pages, page_size, Hkv, D;
+    int block;                /* tokens of a scale: a power of two, 16 .. min(page_size, 128)
+                                 (XS_ERR_PAGE otherwise)                                     */
+    int dtype;                /* XS_DTYPE_* of the tensors used with it                      */
+} xs_paged_cache8;
+
+/*
+ * xs_rope_append_paged8 -- xs_rope_append_paged into an 8-bit cache: rotates q into q_out (the
+ * same bits) and k, and stores k and v quantised, K from the rotation's fp32 values.
+ * Adjacent rows whose slots follow one another within a block are written together, as a run
+ * (xs_paged_step lays a request's tokens out like this).  A run that begins at offset o of its
+ * block keeps the block's first o tokens; what the block holds behind the run has no meaning
+ * afterwards.  Two runs into one block race.  Per head, with a the largest magnitude of the run
+ * and e the least exponent >= -64 with a <= 448 * 2^e:
+ *     o == 0:  the scale becomes 2^e;
+ *     o > 0:   it becomes the larger of 2^e and the block's scale; where that is 2^e, the first
+ *              o tokens' numbers are divided by the ratio (rounded to nearest even: exact but
+ *              for numbers that end below 2^-6);
+ *     numbers = x / scale, rounded to nearest even.
+ * A slot outside [0, n_pages * page_size) (padding) stores no K and V.
+ *   rope == NULL: nothing is rotated, q, q_out and positions must be NULL, H 0 (a cache filled
+ *   from keys that are rotated already).
+ * The scales share no byte with anything else that the call reads or writes.
+ */
+typedef struct xs_rope_append8_args {
+    const void* q;            /* as in xs_rope_append_args                                   */
+    const void* k;
+    const void* v;
+    const int* positions;
+    const long long* slots;
+    void* q_out;
+    const xs_rope* rope;
+    xs_paged_cache8 cache;
+    long long q_stride, k_stride, v_stride, q_out_stride;
+    int T, H;
+} xs_rope_append8_args;
+
+int xs_rope_append_paged8(const xs_rope_append8_args* args, void* stream);
+
+/*
+ * xs_paged_read8 -- elements of an 8-bit cache in 16 bits: row r of [cu_rows[i], cu_rows[i+1])
+ * is the token of sequence i at position first[i] + r - cu_rows[i]:
+ *     k_out[r, h, :] = numbers * scale
+ * rounded once to nearest even (bf16: exact), magnitudes past the type's largest finite
+ * number become that.  Rows from cu_rows[n] on are left as they are; positions outside
+ * [0, table_width * page_size) and page numbers outside [0, n_pages) give zeros.
+ */
+typedef struct xs_paged_read8_args {
+    const int* block_table;   /* device, [n] rows of table_width entries, table_stride apart */
+    const int* cu_rows;       /* device, [n + 1], ascending from 0                           */
+    const int* first;         /* device, [n], or NULL: all 0                                 */
+    void* k_out;
+    void* v_out;              /* device, [T, Hkv, D] of cache.dtype                          */
+    xs_paged_cache8 cache;
+    long long k_stride, v_stride, table_stride;   /* between rows, as in xs_rope_fwd         */
+    int T, n, table_width;    /* n <= 8192                                                   */
+} xs_paged_read8_args;
+
+int xs_paged_read8(const xs_paged_read8_args* args, void* stream);
+
+/*
+ * xs_attn_paged8_plan, xs_attn_paged8_fwd -- xs_attn_paged_plan and xs_attn_paged_fwd over an
+ * 8-bit cache: the same rows, keys, layouts, lse and workspace, on plans of their own (a plan of
+ * the other cache computes nothing, see there).  Elements are those that the cache stands for
+ * (scale bytes 63 .. 254); q keeps 18 or more bits relative to its row's largest channel, the
+ * probabilities enter the second product in fp16, sums, maxima and accumulators are fp32.
+ * Places that no row sees may hold anything, also in the scales.  H / Hkv <= 16.
+ */
+int xs_attn_paged8_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,
+                        int window, void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct xs_attn_paged8_args {
+    const void* q;            /* as in xs_attn_paged_args                                    */
+    const int* block_table;
+    float* lse;
+    void* workspace;          /* of xs_attn_paged_workspace_bytes                            */
+    size_t workspace_bytes;
+    void* outs[XS_MAX_P];
+    xs_paged_cache8 cache;
+    long long q_stride, table_stride;
+    int layout, P;
+    int T, H;
+    int n, table_width;
+    int max_q, causal, window;
+    float scale;
+} xs_attn_paged8_args;
+
+int xs_attn_paged8_fwd(const xs_attn_paged8_args* args, void* stream);
+
+/*
  * xs_burst_gap -- Burst-Gap microbenchmark of the store path the fused epilogue
  * uses (SM -> L2 -> HBM on one GPU).  X-Stage (arXiv 2607.23264), gist.science
  * technical summary, "Methodology: The X-Stage Abstraction and Burst-Gap

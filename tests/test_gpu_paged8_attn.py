@@ -1,0 +1,60 @@
+"""xs_attn_paged8_fwd on the GPU against plain attention in 64 bits over the elements that the cache stands
+for (_paged8.py has the bounds)."""
+import numpy as np
+import pytest
+
+import _paged as pg
+import _paged8 as p8
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def xs():
+    from conftest import build_library
+    build_library()
+    import dit_attention_ulysses_gb300 as xs
+    assert torch.cuda.is_available()
+    return xs
+
+
+def _run(xs, c, causal=True, window=0, scale=None, max_q=None, ws=None, lse=True, layout=None, P=1, fill=float("nan")):
+    scale = c.D ** -0.5 if scale is None else scale
+    max_q = max(max(c.q_lens), 1) if max_q is None else max_q
+    ws = ws or xs.PagedWorkspace(c.n, c.H, c.Hkv, c.D)
+    layout = xs.XS_LAYOUT_CONTIGUOUS if layout is None else layout
+    shape = {xs.XS_LAYOUT_A2A: (c.T // P, c.H, c.D), xs.XS_LAYOUT_HEADS: (c.T, c.H // P, c.D)}.get(layout, (c.T, c.H, c.D))
+    outs = [torch.full(shape, fill, dtype=c.dtype, device="cuda") for _ in range(P)]
+    z = torch.full((c.T, c.H), fill, dtype=torch.float32, device="cuda") if lse else None
+    xs.xs_attn_paged8_plan(c.cu, c.kv, max_q, ws, causal=causal, window=window)
+    xs.xs_attn_paged8_fwd(c.q, *c.cache, c.table, layout, outs, scale, ws, lse=z)
+    assert xs.xs_attn_get_device_error_info()[0] == xs.XS_OK
+    return (outs if P > 1 else outs[0]), z
+
+
+# q_lens, kv_lens, H, Hkv, D, page, block
+DECODE = [
+    ([1], [1], 1, 1, 64, 16, 16),
+    ([1], [33], 2, 1, 128, 16, 16),
+    ([1], [5000], 8, 2, 128, 32, 32),
+    ([1, 1, 1], [31, 32, 33], 4, 4, 64, 32, 16),
+    ([1, 0, 1, 0, 1], [700, 50, 1, 0, 257], 12, 4, 128, 64, 64),
+    ([1] * 40, [1 + 97 * i for i in range(40)], 8, 1, 128, 16, 16),
+    ([2, 1, 4, 3], [900, 3, 4, 130], 8, 2, 64, 128, 128),
+    ([1, 1], [3000, 2100], 28, 4, 128, 256, 32),   # 7 heads to a KV head
+    ([1, 3], [70, 900], 5, 1, 128, 1024, 128),
+    ([3, 3], [4000, 2], 10, 2, 64, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: "n%d_kv%d_H%d_%d_D%d_p%d_b%d" % (len(c[0]), max(c[1]), *c[2:]))
+def test_few_tokens(xs, case, dtype):
+    c = p8.Paged8Case(*case, dtype=dtype, seed=len(case[0]), extra_rows=2)
+    out, lse = _run(xs, c)
+    c.check(out, lse, True, 0, c.D ** -0.5)
+    rows = sum(c.q_lens)
+    assert out[rows:].isnan().all() and lse[rows:].isnan().all()     # rows behind the last sequence
+    out2, _ = _run(xs, c, lse=False)
+    assert torch.equal(out2[:rows], out[:rows])
