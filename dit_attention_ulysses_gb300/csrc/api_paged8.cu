@@ -85,8 +85,25 @@ int encode_cache8(CUtensorMap* m, const void* base, const CacheStrides& s, const
 
 Tiling make_tiling8(int G, int D, int max_q, int sms) {
     Tiling x{};
+    x.t.cache8 = 1;
+    if (static_cast<int64_t>(G) * max_q > ROWS_FEW) {
+        x.rows = ROWS_TILE;
+        x.t.tokens = ROWS_TILE / G;
+        x.t.block = 128;
+        x.t.grid = sms;
+        x.t.start_cost = 512;
+        x.t.snap = 4;
+        x.t.whole = 12;
+        x.t.least = 1024;
+        x.t.join = 38;
+        x.t.join_rows = 32;
+        x.t.waves = xs::MAX_PAGED_WAVES;
+        x.t.one_each = 1280;
+        x.t.l2_bytes = 64 << 20;
+        return x;
+    }
     x.rows = ROWS_FEW;
-    x.t.tokens = G <= x.rows ? x.rows / G : 1;   // (more rows: refused)
+    x.t.tokens = x.rows / G;
     x.t.block = 32;
     x.t.grid = 2 * sms;
     x.t.start_cost = 256;
@@ -99,7 +116,6 @@ Tiling make_tiling8(int G, int D, int max_q, int sms) {
     x.t.few_start_cost = 128;
     x.t.few_least = 128;
     x.t.waves = 0;
-    x.t.cache8 = 1;
     return x;
 }
 
@@ -238,7 +254,6 @@ int xs_paged_read8(const xs_paged_read8_args* args, void* stream) {
 
 int xs_attn_paged8_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,
                         int window, void* workspace, size_t workspace_bytes, void* stream) {
-    if (Hkv > 0 && H / Hkv > ROWS_FEW) return XS_ERR_SHAPE;
     return plan_attn(make_tiling8, cu_q, kv_lens, n, H, Hkv, D, max_q, causal, window, workspace, workspace_bytes, stream);
 }
 
@@ -248,7 +263,6 @@ int xs_attn_paged8_fwd(const xs_attn_paged8_args* args, void* stream) {
     Checked8 x;
     int rc = check_cache8(cache, &x);
     if (rc != XS_OK) return rc;
-    if (args->H / cache.Hkv > ROWS_FEW) return XS_ERR_SHAPE;
     xs::PagedAttn8Args a;
     std::memset(&a, 0, sizeof a);
     const Range scales[2] = {x.k_scales, x.v_scales};
@@ -261,11 +275,13 @@ int xs_attn_paged8_fwd(const xs_attn_paged8_args* args, void* stream) {
         a.v_scale_strides[i] = x.vss.s[i];
     }
     a.block_shift = log2_of(cache.block);
-    const int box = cache.page_size < 32 ? cache.page_size : 32;
+    const int box_max = tiling.rows == ROWS_TILE ? 128 : 32;
+    const int box = cache.page_size < box_max ? cache.page_size : box_max;
     CUtensorMap tk, tv;
     if ((rc = encode_cache8(&tk, cache.k, x.ks, cache, box)) != XS_OK) return rc;
     if ((rc = encode_cache8(&tv, cache.v, x.vs, cache, box)) != XS_OK) return rc;
-    const cudaError_t e = xs::launch_attn_paged8_rows(tk, tv, a, cache.dtype, static_cast<cudaStream_t>(stream));
+    const auto launch = tiling.rows == ROWS_TILE ? xs::launch_attn_paged8 : xs::launch_attn_paged8_rows;
+    const cudaError_t e = launch(tk, tv, a, cache.dtype, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
 

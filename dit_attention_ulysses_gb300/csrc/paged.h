@@ -244,8 +244,11 @@ cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, cons
 // page's tokens of one head, lands as [token][channel] with a row's 16-byte pieces swizzled over its D bytes.
 cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
                                     cudaStream_t stream);
+cudaError_t launch_attn_paged8(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
+                               cudaStream_t stream);
 
 cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
+cudaError_t read_and_clear_paged8_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 
 }  // namespace xs

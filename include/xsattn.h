@@ -697,7 +697,7 @@ int xs_paged_read8(const xs_paged_read8_args* args, void* stream);
  * the other cache computes nothing, see there).  Elements are those that the cache stands for
  * (scale bytes 63 .. 254); q keeps 18 or more bits relative to its row's largest channel, the
  * probabilities enter the second product in fp16, sums, maxima and accumulators are fp32.
- * Places that no row sees may hold anything, also in the scales.  H / Hkv <= 16.
+ * Places that no row sees may hold anything, also in the scales.
  */
 int xs_attn_paged8_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,
                         int window, void* workspace, size_t workspace_bytes, void* stream);

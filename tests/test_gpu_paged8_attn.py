@@ -58,3 +58,55 @@ def test_few_tokens(xs, case, dtype):
     assert out[rows:].isnan().all() and lse[rows:].isnan().all()     # rows behind the last sequence
     out2, _ = _run(xs, c, lse=False)
     assert torch.equal(out2[:rows], out[:rows])
+
+
+FEW_HEADS = [   # one tile of a few rows of the chunk kernel, and of heads that do not divide its 128
+    ([1], [700], 32, 1, 128, 32, 16),
+    ([1, 2], [500, 3000], 40, 1, 128, 16, 16),
+    ([1, 1, 0, 3], [900, 128, 5, 40000], 128, 1, 64, 64, 64),
+    ([5, 6, 1], [20, 5000, 300], 32, 8, 128, 32, 32),
+    ([33], [1300], 48, 2, 128, 128, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("case", FEW_HEADS, ids=lambda c: "n%d_kv%d_H%d_%d_D%d_p%d_b%d" % (len(c[0]), max(c[1]), *c[2:]))
+def test_many_heads_to_a_key(xs, case, dtype):
+    c = p8.Paged8Case(*case, dtype=dtype, seed=len(case[0]), extra_rows=2)
+    out, lse = _run(xs, c)
+    c.check(out, lse, True, 0, c.D ** -0.5)
+    rows = sum(c.q_lens)
+    assert out[rows:].isnan().all() and lse[rows:].isnan().all()
+
+
+CHUNKS = [  # q_lens, kv_lens, H, Hkv, D, page, block, causal, window
+    ([130], [130], 2, 2, 128, 16, 16, True, 0),
+    ([128], [256], 2, 1, 64, 64, 32, False, 0),
+    ([257, 1, 64], [1000, 700, 64], 8, 2, 128, 16, 16, True, 0),
+    ([100, 3, 0, 31], [100, 900, 77, 2000], 6, 2, 64, 32, 32, True, 100),
+    ([300], [1111], 3, 1, 128, 128, 128, True, 1),
+    ([200, 129], [200, 1500], 5, 5, 128, 256, 64, True, 200),
+    ([65, 200], [500, 201], 4, 4, 128, 32, 16, False, 0),
+    ([90], [2500], 24, 8, 64, 1024, 128, False, 0),
+    ([10, 6], [4, 0], 4, 2, 128, 16, 16, True, 0),      # more new tokens than keys: rows that see nothing
+    ([10, 6], [4, 0], 4, 2, 64, 16, 16, False, 0),
+    ([40, 200], [30, 150], 2, 1, 128, 16, 16, True, 7),
+    ([17] * 33, [17 + 13 * i for i in range(33)], 4, 1, 128, 16, 16, True, 0),
+    ([515], [2061], 8, 1, 128, 64, 32, True, 0),
+    ([77, 400], [1500, 400], 7, 1, 128, 32, 32, True, 0),     # 18 tokens of 7 heads: 126 of 128 rows
+    ([301], [700], 24, 1, 64, 16, 16, True, 333),
+    ([2000], [2000], 2, 1, 64, 16, 16, True, 0),
+    ([129] * 9, [129 * (i + 1) for i in range(9)], 12, 3, 128, 64, 64, False, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "q%d_kv%d_H%d_%d_D%d_p%d_b%d_%s_w%d" % (
+    max(c[0]), max(c[1]), *c[2:7], "causal" if c[7] else "full", c[8]))
+def test_chunks(xs, case, dtype):
+    *shape, causal, window = case
+    c = p8.Paged8Case(*shape, dtype=dtype, seed=sum(case[0]), extra_rows=1, window=window, freed=window > 0)
+    out, lse = _run(xs, c, causal, window)
+    c.check(out, lse, causal, window, c.D ** -0.5)
+    rows = sum(c.q_lens)
+    assert out[rows:].isnan().all() and lse[rows:].isnan().all()
