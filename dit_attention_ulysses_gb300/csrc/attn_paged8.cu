@@ -71,8 +71,8 @@ struct Cfg8 {
     static constexpr int CODE_BYTES = BLOCK_N * D;         // a block of K or V in the cache's form: [key][D]
     static constexpr int V_BYTES = BLOCK_N * D * 2;        // as the fp16 operand: [8 keys][panel][key][64 channels]
     static constexpr int GROUP = D / 64 * 1024;
-    static constexpr int K_STAGES = D == 128 ? (F16 ? 3 : 4) : 5;
-    static constexpr int C_STAGES = D == 128 ? 2 : 4;      // copies of V
+    static constexpr int K_STAGES = D == 128 ? (F16 ? 2 : 3) : 5;
+    static constexpr int C_STAGES = D == 128 ? 3 : 4;      // copies of V
     static constexpr int V_STAGES = D == 128 ? 2 : 3;      // operands
     static constexpr int Q_OFF = 0;
     static constexpr int V_OFF = Q_OFF + Q_BYTES;
@@ -149,29 +149,112 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The waits of device_wait.cuh, in line as far as their first test.  All roles' loops together have to fit the
+// instruction cache of an SM: with every wait in line (700 bytes each) and the producers' loops apart, 41 % of the
+// warps' time went to instruction fetches (causal chunk: 1474 us).
+__device__ __noinline__ bool thread_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
+                                            int blk) {
+    return thread_wait(bar, parity, abort_flag, timeout_ns, unit, blk);
+}
+
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
+                                          int blk = -1) {
+    return mbar_test_wait(bar, parity) || thread_wait_on(bar, parity, abort_flag, timeout_ns, unit, blk);
+}
+
+__device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
+                                          int blk) {
+    return warp_wait(bar, parity, abort_flag, timeout_ns, unit, blk);
+}
+
+__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
+                                         int blk = -1) {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) || warp_wait_on(bar, parity, abort_flag, timeout_ns, unit, blk);
+}
+
 // --------------------------------------------------------------- producers
-// One block of K or V, by the whole warp: waits for its stage, then one copy per page.
-__device__ __forceinline__ bool load_codes(const CUtensorMap* map, const PagedAttnArgs& a, uint32_t base, uint32_t full0,
-                                           uint32_t free0, uint32_t item, int stages, int D, int pages, int blk, int key0, int x,
-                                           int boxes, int box, volatile int* abort_flag, int u, volatile uint32_t* loaded) {
+// Loads the blocks of a piece: K's, or V's and the scales of both.  By a whole warp: a block's stage is waited for by
+// one lane, then each of up to eight lanes issues one page's copy.
+//
+// Lane 8 j + i has the scales of keys 16 i .. 16 i + 15 of block 4 m + j; they are fetched a group of four blocks
+// ahead of use, from the pages of that group, fetched one more ahead.  Those of block g (counted over the CTA's
+// lifetime) lie in slot g % 8 until those of block g + 8 are written: after the stage of V(g + 8)'s copy was given back,
+// V(g + 8 - C_STAGES) converted, hence (its operand's stage) PV(g + 8 - C_STAGES - V_STAGES) done, which is g or later:
+// after the softmax of block g.
+template <int D, bool F16>
+__device__ __forceinline__ bool load_blocks(const CUtensorMap* map, const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0,
+                                         const Piece& piece, int u, uint32_t item, bool is_v, volatile int* abort_flag) {
+    using C = Cfg8<D, F16>;
+    static_assert(C::C_STAGES + C::V_STAGES <= SCALE_SLOTS, "see above");
     const int lane = static_cast<int>(lane_id());
-    const uint32_t stage = item % stages, round = item / stages;
-    const uint32_t full = full0 + stage * 8u;
-    bool ok = true;
-    if (lane == 0) {
-        if (round > 0) ok = thread_wait(free0 + stage * 8u, (round - 1) & 1, abort_flag, a.timeout_ns, u, blk);
-        if (ok) {
-            mbar_arrive_expect_tx(full, BLOCK_N * D);
-            loaded[stage] = round + 1;
+    auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
+    const Piece d = piece;
+    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);   // keys of one copy
+    const int boxes = BLOCK_N / box;                              // 1 .. 8
+    const uint32_t stages = is_v ? C::C_STAGES : C::K_STAGES;
+    const uint32_t base = smem_addr(smem + (is_v ? C::C_OFF : C::K_OFF));
+    const uint32_t full0 = bar(is_v ? C::B_C_FULL : C::B_K_FULL), free0 = bar(is_v ? C::B_C_FREE : C::B_K_FREE);
+    const int x = d.head * (is_v ? a.v_head : a.k_head);
+    volatile uint32_t* const loaded = reinterpret_cast<volatile uint32_t*>(smem + C::LOADED_OFF) + (is_v ? C::K_STAGES : 0);
+    Scales* const scales = reinterpret_cast<Scales*>(smem + C::SCALES_OFF);
+    const int* table = a.table + static_cast<long long>(d.index) * a.table_stride;
+    auto scales_of = [&](int m, int pages) {   // bytes of K's, V's << 8
+        const int page = __shfl_sync(0xffffffffu, pages, (lane & 24) + (lane & 7) * 16 / box);
+        int w = 127 | 127 << 8;
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
+            const int off = (d.key0 + (4 * m + (lane >> 3)) * BLOCK_N + (lane & 7) * 16) & ((1 << a.page_shift) - 1);
+            const int b = off >> a.block_shift;
+            w = a.k_scale[page * a.k_scale_strides[0] + b * a.k_scale_strides[1] + d.head * a.k_scale_strides[2]] |
+                a.v_scale[page * a.v_scale_strides[0] + b * a.v_scale_strides[1] + d.head * a.v_scale_strides[2]] << 8;
+        }
+        return w;
+    };
+    int cur = -1, next = -1, after = -1, bytes = 0, bytes_next = 0;   // of groups m, m + 1, m + 2
+    uint32_t stage = item % stages, round = item / stages;
+#pragma unroll 1
+    for (int j = -8; j < d.nb; ++j) {   // (two groups before the first block fill the pipeline)
+        if ((j & 3) == 0) {
+            cur = next;
+            next = after;
+            after = load_pages(a, table, (j >> 2) + 2, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
+            bytes = bytes_next;
+            if (is_v && j >= -4) bytes_next = scales_of((j >> 2) + 1, next);
+            if (j < 0) {
+                j += 3;
+                continue;
+            }
+        }
+        bool ok = true;
+        if (lane == 0) {
+            if (round > 0) ok = lane_wait(free0 + stage * 8u, (round - 1) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok) {
+                mbar_arrive_expect_tx(full0 + stage * 8u, BLOCK_N * D);
+                loaded[stage] = round + 1;
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        const int page = __shfl_sync(0xffffffffu, cur, (j & 3) * 8 + (lane & 7));
+        __syncwarp();
+        if (!ok) return false;
+        if (lane < boxes)
+            tma_load_3d(base + stage * (BLOCK_N * D) + lane * box * D, map, full0 + stage * 8u, x,
+                        (d.key0 + j * BLOCK_N) & ((1 << a.page_shift) - 1), page);
+        if (is_v) {
+            const uint32_t slot = item % SCALE_SLOTS;
+            if ((lane >> 3) == (j & 3)) {
+                // (of keys that no row sees: anything; a factor that stays positive keeps their scores at -infinity)
+                const int k = min(max(bytes & 255, 1), 254), v = min(max(bytes >> 8, LEAST_SCALE), 254);
+                scales[slot * 8 + (lane & 7)] =
+                    Scales{scale_value(k), static_cast<float>(v - 127), scale_value(254 - v), 0.0f};
+            }
+            warp_arrive(bar(C::B_SCALES + slot));
+        }
+        ++item;
+        if (++stage == stages) {
+            stage = 0;
+            ++round;
         }
     }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    const int page = __shfl_sync(0xffffffffu, pages, (blk & 3) * 8 + (lane & 7));
-    __syncwarp();
-    if (!ok) return false;
-    if (lane < boxes)
-        tma_load_3d(base + stage * BLOCK_N * D + lane * box * D, map, full, x,
-                    (key0 + blk * BLOCK_N) & ((1 << a.page_shift) - 1), page);
     return true;
 }
 
@@ -183,15 +266,14 @@ __device__ void producer_k_role(const CUtensorMap* tk, const PagedAttn8Args& a, 
     using C = Cfg8<D, F16>;
     const int lane = static_cast<int>(lane_id());
     auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
-    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);   // keys of one copy
-    const int boxes = BLOCK_N / box;                              // 1 .. 8
-    volatile uint32_t* const loaded = reinterpret_cast<volatile uint32_t*>(smem + C::LOADED_OFF);
+    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
     PieceWalk walk(a, 1);
     uint32_t item = 0;
     bool ok = true;
+#pragma unroll 1
     for (int u = 0;; ++u) {
         if (u >= 2) {
-            if (lane == 0) ok = thread_wait(bar(C::B_Q_FREE + (u & 1)), ((u >> 1) - 1) & 1, abort_flag, a.timeout_ns, u);
+            if (lane == 0) ok = lane_wait(bar(C::B_Q_FREE + (u & 1)), ((u >> 1) - 1) & 1, abort_flag, a.timeout_ns, u);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             __syncwarp();
         }
@@ -202,87 +284,28 @@ __device__ void producer_k_role(const CUtensorMap* tk, const PagedAttn8Args& a, 
             *reinterpret_cast<Piece*>(smem + C::PIECE_OFF + (u % PIECES) * 64) = d;
             mbar_arrive(bar(C::B_PIECE + u % PIECES));   // release: the descriptor is visible to whoever waits
         }
+        __syncwarp();
         if (!more) break;
         if (walk.cut_end) pdl_launch();   // the CTA's last piece
-        const int* table = a.table + static_cast<long long>(d.index) * a.table_stride;
-        int cur = -1, next = load_pages(a, table, 0, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
-        for (int j = 0; j < d.nb && ok; ++j) {
-            if ((j & 3) == 0) {
-                cur = next;
-                next = load_pages(a, table, (j >> 2) + 1, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
-            }
-            ok = load_codes(tk, a, smem_addr(smem + C::K_OFF), bar(C::B_K_FULL), bar(C::B_K_FREE), item++, C::K_STAGES, D, cur, j,
-                            d.key0, d.head * a.k_head, boxes, box, abort_flag, u, loaded);
-        }
-        if (!ok) break;
+        if (!load_blocks<D, F16>(tk, a, smem, bar0, piece_of(smem, C::PIECE_OFF, u), u, item, false, abort_flag)) break;
+        item += d.nb;
         walk.advance(a);
     }
     __syncwarp();
 }
 
-// V, and the scales of both.  Lane 8 j + i has the scales of keys 16 i .. 16 i + 15 of block 4 m + j; they are
-// fetched a group of four blocks ahead of use, from the pages of that group, fetched one more ahead.
-//
-// The scales of block g (counted over the CTA's lifetime) lie in slot g % 8 until those of block g + 8 are written.  That
-// happens after V(g + 6) of the stages has been converted and its stage given back at the earliest (C_STAGES <= 4:
-// V(g + 4)), hence after V(g + 4)'s operand stage was free (V_STAGES <= 3: after PV(g + 1)), hence after the softmax
-// of block g + 1.
 template <int D, bool F16>
 __device__ void producer_v_role(const CUtensorMap* tv, const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0,
                                 volatile int* abort_flag) {
     using C = Cfg8<D, F16>;
-    static_assert(C::C_STAGES + C::V_STAGES < SCALE_SLOTS, "see above");
-    const int lane = static_cast<int>(lane_id());
-    auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
-    const int box = 1 << (a.page_shift < 7 ? a.page_shift : 7);
-    const int boxes = BLOCK_N / box;
-    volatile uint32_t* const loaded = reinterpret_cast<volatile uint32_t*>(smem + C::LOADED_OFF) + C::K_STAGES;
-    Scales* const scales = reinterpret_cast<Scales*>(smem + C::SCALES_OFF);
     uint32_t item = 0;
-    bool ok = true;
-    for (int u = 0; ok; ++u) {
-        ok = warp_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
-        if (!ok) break;
-        const Piece d = piece_of(smem, C::PIECE_OFF, u);
-        if (d.nb == 0) break;
-        const int* table = a.table + static_cast<long long>(d.index) * a.table_stride;
-        auto pages_of = [&](int m) {
-            return load_pages(a, table, m, d.key0, d.nb, d.kv_len, d.lo_key, boxes, box);
-        };
-        auto scales_of = [&](int m, int pages) {   // bytes of K's, V's << 8
-            const int page = __shfl_sync(0xffffffffu, pages, (lane & 24) + (lane & 7) * 16 / box);
-            int w = 127 | 127 << 8;
-            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
-                const int off = (d.key0 + (4 * m + (lane >> 3)) * BLOCK_N + (lane & 7) * 16) & ((1 << a.page_shift) - 1);
-                const int b = off >> a.block_shift;
-                w = a.k_scale[page * a.k_scale_strides[0] + b * a.k_scale_strides[1] + d.head * a.k_scale_strides[2]] |
-                    a.v_scale[page * a.v_scale_strides[0] + b * a.v_scale_strides[1] + d.head * a.v_scale_strides[2]] << 8;
-            }
-            return w;
-        };
-        int cur = -1, next = pages_of(0), after = pages_of(1);
-        int bytes = 0, bytes_next = scales_of(0, next);
-        for (int j = 0; j < d.nb && ok; ++j) {
-            if ((j & 3) == 0) {
-                cur = next;
-                next = after;
-                after = pages_of((j >> 2) + 2);
-                bytes = bytes_next;
-                bytes_next = scales_of((j >> 2) + 1, next);
-            }
-            ok = load_codes(tv, a, smem_addr(smem + C::C_OFF), bar(C::B_C_FULL), bar(C::B_C_FREE), item, C::C_STAGES, D, cur, j,
-                            d.key0, d.head * a.v_head, boxes, box, abort_flag, u, loaded);
-            if (!ok) break;
-            const uint32_t slot = item % SCALE_SLOTS;
-            if ((lane >> 3) == (j & 3)) {
-                // (of keys that no row sees: anything; a factor that stays positive keeps their scores at -infinity)
-                const int k = min(max(bytes & 255, 1), 254), v = min(max(bytes >> 8, LEAST_SCALE), 254);
-                scales[slot * 8 + (lane & 7)] =
-                    Scales{scale_value(k), static_cast<float>(v - 127), scale_value(254 - v), 0.0f};
-            }
-            warp_arrive(bar(C::B_SCALES + slot));
-            ++item;
-        }
+#pragma unroll 1
+    for (int u = 0;; ++u) {
+        if (!all_wait(bar0 + (C::B_PIECE + u % PIECES) * 8u, (u / PIECES) & 1, abort_flag, a.timeout_ns, u)) break;
+        const Piece& d = piece_of(smem, C::PIECE_OFF, u);
+        const int n = d.nb;
+        if (n == 0 || !load_blocks<D, F16>(tv, a, smem, bar0, d, u, item, true, abort_flag)) break;
+        item += n;
     }
     __syncwarp();
 }
@@ -292,25 +315,34 @@ __device__ void producer_v_role(const CUtensorMap* tv, const PagedAttn8Args& a, 
 template <int D, bool F16>
 __device__ __forceinline__ void convert_q(const PagedAttn8Args& a, const Piece& d, uint8_t* smem, int tid, float* factor) {
     using C = Cfg8<D, F16>;
-    constexpr int PER_ROW = D / 16, ROWS = CONVERTERS * 32 / PER_ROW, BATCH = 4;
+    constexpr int PER_ROW = D / 16, ROWS = CONVERTERS * 32 / PER_ROW, BATCH = 2;
     const int piece = tid % PER_ROW;
-#pragma unroll 1
-    for (int r0 = tid / PER_ROW; r0 < BLOCK_M; r0 += BATCH * ROWS) {
-        uint4 w[BATCH][2];
+    uint4 w[BATCH][2], next[BATCH][2];
+    auto fetch = [&](int r0) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const int r = r0 + i * ROWS;
             int t, gh;
             fdivmod(r, a.fd_G, t, gh);
             const int token = d.row0 + t;
-            w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+            next[i][0] = next[i][1] = make_uint4(0, 0, 0, 0);
             if (r < d.n_rows && token >= 0 && token < a.T) {
                 const uint4* p = reinterpret_cast<const uint4*>(
                     static_cast<const uint16_t*>(a.q) + token * a.q_stride + (static_cast<long long>(d.head) * a.G + gh) * D + piece * 16);
-                w[i][0] = p[0];
-                w[i][1] = p[1];
+                next[i][0] = p[0];
+                next[i][1] = p[1];
             }
         }
+    };
+    fetch(tid / PER_ROW);
+#pragma unroll 1
+    for (int r0 = tid / PER_ROW; r0 < BLOCK_M; r0 += BATCH * ROWS) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            w[i][0] = next[i][0];
+            w[i][1] = next[i][1];
+        }
+        fetch(r0 + BATCH * ROWS);   // (past the rows: nothing)
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const int r = r0 + i * ROWS;
@@ -351,42 +383,56 @@ __device__ __forceinline__ void convert_q(const PagedAttn8Args& a, const Piece& 
     }
 }
 
-// A block of V from its copy to the fp16 operand; keys outside [from, to) as zeros.  Eight lanes read a key's 16-byte
-// pieces (D = 64: two keys') side by side; each writes two, the upper half of a key's the second one first, so that
-// the eight are apart.
+// A thread's part of V's conversion: a 16-byte piece of every KEYS-th key, read at code + n KEYS D, written as two at
+// lo and hi + n KEYS D 2 (KEYS a multiple of 8, so that the swizzles of all its keys are the same).  Eight lanes read
+// and write different banks: two keys, with D = 128 the first half of one and the second half of the other.
 template <int D>
-__device__ __forceinline__ void convert_v(const uint8_t* code, uint8_t* v, int tid, int from, int to) {
-    constexpr int PER_ROW = D / 16, KEYS = CONVERTERS * 32 / PER_ROW, GROUP = D / 64 * 1024;
-    const int piece = tid % PER_ROW;
-#pragma unroll 4
-    for (int key = tid / PER_ROW; key < BLOCK_N; key += KEYS) {
+struct ConvertV {
+    static constexpr int GROUP = D / 64 * 1024, KEYS = CONVERTERS * 32 * 16 / D;
+    uint32_t code, lo, hi;   // offsets
+    int key;
+
+    __device__ __forceinline__ explicit ConvertV(int tid) {
+        const int pair = D == 128 ? tid >> 4 : tid >> 3, odd = (tid >> 2) & 1;
+        const int piece = (tid & 3) + (D == 128 ? 4 * (odd ^ ((tid >> 3) & 1)) : 0);
+        key = 2 * pair + odd;
         const int r = key & 7;
-        uint4 w = *reinterpret_cast<const uint4*>(code + key * D + ((piece ^ (D == 128 ? r : (r >> 1))) << 4));
-        if (key < from || key >= to) w = make_uint4(0, 0, 0, 0);
-        const uint4 lo = make_uint4(codes_to_f16x2(w.x), codes_to_f16x2_high(w.x), codes_to_f16x2(w.y), codes_to_f16x2_high(w.y));
-        const uint4 hi = make_uint4(codes_to_f16x2(w.z), codes_to_f16x2_high(w.z), codes_to_f16x2(w.w), codes_to_f16x2_high(w.w));
-        uint8_t* const row = v + (key >> 3) * GROUP + (piece >> 2) * 1024 + r * 128;
-        const int c0 = ((2 * piece) & 7) ^ r, c1 = ((2 * piece + 1) & 7) ^ r;
-        const bool second = piece >= 4;
-        *reinterpret_cast<uint4*>(row + ((second ? c1 : c0) << 4)) = second ? hi : lo;
-        *reinterpret_cast<uint4*>(row + ((second ? c0 : c1) << 4)) = second ? lo : hi;
+        code = key * D + ((piece ^ (D == 128 ? r : r >> 1)) << 4);
+        const uint32_t row = (key >> 3) * GROUP + (piece >> 2) * 1024 + r * 128;
+        lo = row + ((((2 * piece) & 7) ^ r) << 4);
+        hi = row + ((((2 * piece + 1) & 7) ^ r) << 4);
     }
-}
+
+    // Keys outside [from, to) become zeros.
+    __device__ __forceinline__ void block(const uint8_t* from_code, uint8_t* v, int from, int to) const {
+        const bool edge = from > 0 || to < BLOCK_N;
+#pragma unroll 4
+        for (int n = 0; n < BLOCK_N / KEYS; ++n) {
+            uint4 w = *reinterpret_cast<const uint4*>(from_code + code + n * (KEYS * D));
+            if (edge && (key + n * KEYS < from || key + n * KEYS >= to)) w = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(v + lo + n * (KEYS * D * 2)) =
+                make_uint4(codes_to_f16x2(w.x), codes_to_f16x2_high(w.x), codes_to_f16x2(w.y), codes_to_f16x2_high(w.y));
+            *reinterpret_cast<uint4*>(v + hi + n * (KEYS * D * 2)) =
+                make_uint4(codes_to_f16x2(w.z), codes_to_f16x2_high(w.z), codes_to_f16x2(w.w), codes_to_f16x2_high(w.w));
+        }
+    }
+};
 
 template <int D, bool F16>
 __device__ void convert_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0, volatile int* abort_flag) {
     using C = Cfg8<D, F16>;
     const int tid = threadIdx.x - WARP_CONVERT * 32;
+    const ConvertV<D> convert_v(tid);
     auto bar = [&](int i) { return bar0 + static_cast<uint32_t>(i) * 8u; };
     uint32_t item = 0;
     bool ok = true;
     for (int u = 0; ok; ++u) {
-        ok = warp_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
+        ok = all_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
         const Piece d = piece_of(smem, C::PIECE_OFF, u);
         if (d.nb == 0) break;
         // the previous piece's S MMAs have read Q
-        if (u > 0) ok = warp_wait(bar(C::B_Q_FREE + ((u - 1) & 1)), ((u - 1) >> 1) & 1, abort_flag, a.timeout_ns, u);
+        if (u > 0) ok = all_wait(bar(C::B_Q_FREE + ((u - 1) & 1)), ((u - 1) >> 1) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
         convert_q<D, F16>(a, d, smem, tid, reinterpret_cast<float*>(smem + C::FACTOR_OFF) + (u & 1) * BLOCK_M);
         fence_proxy_async_smem();   // before the MMAs read it
@@ -397,11 +443,11 @@ __device__ void convert_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t ba
         }
         for (int j = 0; j < d.nb; ++j, ++item) {
             const uint32_t cs = item % C::C_STAGES, vs = item % C::V_STAGES, cr = item / C::C_STAGES, vr = item / C::V_STAGES;
-            if (vr > 0) ok = warp_wait(bar(C::B_V_FREE + vs), (vr - 1) & 1, abort_flag, a.timeout_ns, u, j);
-            if (ok) ok = warp_wait(bar(C::B_C_FULL + cs), cr & 1, abort_flag, a.timeout_ns, u, j);
+            if (vr > 0) ok = all_wait(bar(C::B_V_FREE + vs), (vr - 1) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok) ok = all_wait(bar(C::B_C_FULL + cs), cr & 1, abort_flag, a.timeout_ns, u, j);
             if (!ok) break;
-            convert_v<D>(smem + C::C_OFF + cs * C::CODE_BYTES, smem + C::V_OFF + vs * C::V_BYTES, tid,
-                         d.unseen - d.key0 - j * BLOCK_N, d.kv_len - d.key0 - j * BLOCK_N);
+            convert_v.block(smem + C::C_OFF + cs * C::CODE_BYTES, smem + C::V_OFF + vs * C::V_BYTES,
+                            d.unseen - d.key0 - j * BLOCK_N, d.kv_len - d.key0 - j * BLOCK_N);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane_id() == 0) {
@@ -426,17 +472,17 @@ __device__ void mma_s_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0
     uint32_t sb = 0, sph = 0;   // S buffer of block g (g % 3) and its phase parity ((g / 3) & 1)
     bool ok = true;
     for (int u = 0; ok; ++u) {
-        ok = thread_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
+        ok = lane_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
         const int n = piece_of(smem, C::PIECE_OFF, u).nb;
         if (n == 0) break;
-        ok = thread_wait(bar(C::B_Q_FULL), u & 1, abort_flag, a.timeout_ns, u);
+        ok = lane_wait(bar(C::B_Q_FULL), u & 1, abort_flag, a.timeout_ns, u);
         // the previous piece's last PV first: its epilogue waits for it
-        if (ok && u > 0) ok = thread_wait(bar(C::B_O_FINAL), (u - 1) & 1, abort_flag, a.timeout_ns, u);
+        if (ok && u > 0) ok = lane_wait(bar(C::B_O_FINAL), (u - 1) & 1, abort_flag, a.timeout_ns, u);
         for (int j = 0; j < n && ok; ++j, ++g) {
-            if (g >= S_BUFS) ok = thread_wait(bar(C::B_P_FREE + sb), sph ^ 1u, abort_flag, a.timeout_ns, u, j);
+            if (g >= S_BUFS) ok = lane_wait(bar(C::B_P_FREE + sb), sph ^ 1u, abort_flag, a.timeout_ns, u, j);
             const uint32_t stage = g % C::K_STAGES;
-            if (ok) ok = thread_wait(bar(C::B_K_FULL + stage), (g / C::K_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok) ok = lane_wait(bar(C::B_K_FULL + stage), (g / C::K_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kdesc = desc_add(kdesc0, stage * (C::CODE_BYTES >> 4));
@@ -473,16 +519,16 @@ __device__ void mma_pv_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar
     uint32_t pb = 0, pph = 0;   // buffer of block g (g % 3) and its phase parity ((g / 3) & 1)
     bool ok = true;
     for (int u = 0; ok; ++u) {
-        ok = thread_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
+        ok = lane_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
         const int n = piece_of(smem, C::PIECE_OFF, u).nb;
         if (n == 0) break;
         for (int j = 0; j < n && ok; ++j, ++g) {
-            ok = thread_wait(bar(C::B_P_FULL + pb), pph, abort_flag, a.timeout_ns, u, j);
+            ok = lane_wait(bar(C::B_P_FULL + pb), pph, abort_flag, a.timeout_ns, u, j);
             // the epilogue has read the previous piece's O (PV(0) overwrites it)
-            if (ok && j == 0 && u > 0) ok = thread_wait(bar(C::B_O_FREE), (u - 1) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok && j == 0 && u > 0) ok = lane_wait(bar(C::B_O_FREE), (u - 1) & 1, abort_flag, a.timeout_ns, u, j);
             const uint32_t stage = g % C::V_STAGES;
-            if (ok) ok = thread_wait(bar(C::B_V_FULL + stage), (g / C::V_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok) ok = lane_wait(bar(C::B_V_FULL + stage), (g / C::V_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
             if (!ok) break;
             tc_fence_after();
             const uint64_t vdesc = desc_add(vdesc0, stage * (C::V_BYTES >> 4));
