@@ -994,7 +994,7 @@ int xs_attn_get_device_error_info(void* stream, int* info, int n_info) {
     unsigned long long t = 0;
     // each kernel family keeps its own words: the earliest record is reported, all are cleared
     for (auto read : {xs::read_and_clear_device_error, xs::read_and_clear_paged_error, xs::read_and_clear_paged_rows_error,
-                      xs::read_and_clear_paged8_error}) {
+                      xs::read_and_clear_paged8_error, xs::read_and_clear_paged8_rows_error}) {
         int v1 = 0, d1 = 0;
         unsigned long long t1 = 0;
         xs::DeviceErrorInfo r1{};

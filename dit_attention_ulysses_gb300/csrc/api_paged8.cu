@@ -102,7 +102,7 @@ Tiling make_tiling8(int G, int D, int max_q, int sms) {
         x.t.l2_bytes = 64 << 20;
         return x;
     }
-    x.rows = ROWS_FEW;
+    x.rows = static_cast<int64_t>(G) * max_q <= ROWS_FEW / 2 ? ROWS_FEW / 2 : ROWS_FEW;
     x.t.tokens = x.rows / G;
     x.t.block = 32;
     x.t.grid = 2 * sms;

@@ -33,15 +33,13 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
 
-#include "codes8.cuh"
 #include "device_wait.cuh"
 #include "kernels.h"
 #include "paged.h"
+#include "paged_rows.cuh"
 #include "paged_walk.cuh"
 #include "ptx.cuh"
-#include "rope_tile.cuh"
 
 namespace xs {
 namespace {
@@ -49,16 +47,12 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int GROUP = 32;                  // keys of a ring slot
-constexpr int JOIN_BATCH = 16;             // parts of a cut tile read at once
-constexpr float NO_MAX = -3.402823466e38f;           // running maximum of a row that has seen nothing
-constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units; P stays below 2^8
 
-template <int D, bool E8>
+template <int D>
 struct RowsCfg {
-    static constexpr int BYTES = E8 ? 1 : 2;           // of an element of the cache
-    static constexpr int SLOT = GROUP * D * BYTES;
-    static constexpr int SLOTS = 6 / BYTES * 128 / D;  // per warp
-    static constexpr int OCTET = 8 * D * BYTES;        // 8 keys of a slot: [64-channel panel][key][channel], 8 bits: [key][channel]
+    static constexpr int SLOT = GROUP * D * 2;
+    static constexpr int SLOTS = 3 * 128 / D;          // per warp
+    static constexpr int OCTET = D / 64 * 1024;        // 8 keys of a slot: [64-channel panel][key][channel]
     static constexpr int ROWS = 16;
     static constexpr int RING = WARPS * SLOTS * SLOT;  // 96 KB; reused to join the warps' results
     static constexpr int O_STRIDE = D + 8;             // floats; keeps the joining stores off each other's banks
@@ -66,121 +60,17 @@ struct RowsCfg {
     static constexpr int ML_OFF = Q_OFF + ROWS * D * 2;
     static constexpr int BAR_OFF = ML_OFF + WARPS * ROWS * 8;
     static constexpr int MISC_OFF = BAR_OFF + WARPS * SLOTS * 8;
-    static constexpr int FACTOR_OFF = MISC_OFF + 16;   // 8 bits: c 2^E of every row
-    static constexpr int SMEM = FACTOR_OFF + ROWS * 4;
+    static constexpr int SMEM = MISC_OFF + 16;
     static constexpr int ALLOC = SMEM + 1024;          // alignment of the swizzled slots
     static_assert(WARPS * ROWS * O_STRIDE * 4 <= RING, "the joined results fit the ring");
     static_assert(ALLOC <= 113 * 1024, "two CTAs per SM");
 };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-                 : "r"(addr)
-                 : "memory");
-}
-
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (F16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    return F16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
-}
-
-// Offset of the 16 channels `chunk` of key `row` of an octet of 8-bit rows, under TMA's swizzle of D-byte rows.
-template <int D>
-__device__ __forceinline__ uint32_t code_at(int row, int chunk) {
-    return row * D + ((chunk ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
-}
-
-// The 16 bytes of a row of Q (D / 8 lanes side by side hold it) from bf16 or fp16 to fp16, scaled to the row's
-// largest channel; returns the scale's inverse.
 template <int D, bool F16>
-__device__ __forceinline__ float q_to_f16(uint4& v) {
-    uint32_t* const w = reinterpret_cast<uint32_t*>(&v);
-    float x[8], m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        widen<F16>(w[i], x[2 * i], x[2 * i + 1]);
-        m = fmaxf(m, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    }
-#pragma unroll
-    for (int d = D / 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const int e = min(max(static_cast<int>(__float_as_uint(m) >> 23), 15), 254);   // its exponent byte
-    const float f = scale_value(268 - e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(x[2 * i] * f, x[2 * i + 1] * f);
-    return scale_value(e - 14);
-}
-
-// warp_wait, except that a limit of 0 gives up at the first test that finds the copy not
-// landed: the wait's own first probe may be suspended until it has.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns,
-                                          int unit, int blk) {
-    if (timeout_ns == 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
-        *abort_flag = 1;
-        report_error(XS_DEVICE_TIMEOUT_CODE, static_cast<int>(bar), static_cast<int>(parity), unit, blk);
-        return false;
-    }
-    return warp_wait(bar, parity, abort_flag, timeout_ns, unit, blk);
-}
-
-// Destination of output row (token, head) in the call's layout.
-__device__ __forceinline__ uint16_t* out_row(const PagedAttnArgs& a, int token, int head) {
-    int ps, s, ph, h;
-    fdivmod(token, a.epi.fd_Sl, ps, s);
-    fdivmod(head, a.epi.fd_Hl, ph, h);
-    const int p = ps + ph;
-    if (p >= MAX_PTRS || a.epi.ptr[p] == nullptr) {
-        report_error(XS_DEVICE_BOUNDS_CODE, 2, p, token, head);
-        return nullptr;
-    }
-    return reinterpret_cast<uint16_t*>(a.epi.ptr[p]) + (static_cast<size_t>(s) * a.epi.Hl + h) * a.D;
-}
-
-// Four channels and, once per row, the log-sum-exp of a finished row.
-template <bool F16>
-__device__ __forceinline__ void store_out(const PagedAttnArgs& a, int token, int head, int c4, float4 o, float m,
-                                          float l) {
-    uint16_t* p = out_row(a, token, head);
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;   // a row that saw no key: 0
-    if (p != nullptr) {
-        uint2 w;
-        w.x = pack2<F16>(o.x * inv, o.y * inv);
-        w.y = pack2<F16>(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(p + c4 * 4) = w;
-    }
-    if (c4 == 0 && a.lse != nullptr)
-        a.lse[static_cast<size_t>(token) * a.H + head] =
-            l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
-}
-
-template <int D, bool F16, bool E8>
 __global__ void __launch_bounds__(THREADS, 2)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                           const __grid_constant__ std::conditional_t<E8, PagedAttn8Args, PagedAttnArgs> a) {
-    using C = RowsCfg<D, E8>;
+                           const __grid_constant__ PagedAttnArgs a) {
+    using C = RowsCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -205,7 +95,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     {
         const PagedHeader& h = *a.work.header;
         if (h.n != a.n || h.H != a.H || h.Hkv != a.Hkv || h.D != D || h.tokens != a.tile.tokens ||
-            h.block != a.tile.block || h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window || h.cache8 != (E8 ? 1 : 0)) {
+            h.block != a.tile.block || h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window || h.cache8 != 0) {
             if (tid == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, h.n, h.tokens, h.grid);
             return;
         }
@@ -256,20 +146,6 @@ __global__ void __launch_bounds__(THREADS, 2)
         };
         int pages = load_pages(0), pages_next = load_pages(16);
         int page_base = 0;   // group of `pages`' first lane pair
-        // scale bytes of the 16 keys `lane & 1` of group `first + lane / 2`: K's, V's << 8
-        auto load_scales = [&](int first, int page) -> int {
-            int w = 127 | 127 << 8;
-            if constexpr (E8) {
-                if (halves == 1) page = __shfl_sync(0xffffffffu, page, lane & ~1);
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
-                    const int off = (key_of(first + (lane >> 1)) + (lane & 1) * 16) & (page_size - 1);
-                    const int b = off >> a.block_shift;
-                    w = a.k_scale[page * a.k_scale_strides[0] + b * a.k_scale_strides[1] + pos.head * a.k_scale_strides[2]] |
-                        a.v_scale[page * a.v_scale_strides[0] + b * a.v_scale_strides[1] + pos.head * a.v_scale_strides[2]] << 8;
-                }
-            }
-            return w;
-        };
         auto issue = [&](int i) {   // item i of the piece: K (even) or V (odd) of group i / 2
             const int g = i >> 1;
             const int from = ((g - page_base) & 15) * 2;
@@ -283,19 +159,13 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const uint32_t dst = ring + slot * C::SLOT;
                 const CUtensorMap* m = (i & 1) ? &tv : &tk;
                 const int x = pos.head * ((i & 1) ? a.v_head : a.k_head);
-                if constexpr (E8) {
-                    tma_load_3d(dst, m, bar, x, row, p0);
-                    if (halves == 2) tma_load_3d(dst + C::SLOT / 2, m, bar, x, row, p1);
-                } else {
-                    tma_load_5d(dst, m, bar, x, 0, 0, row >> 3, p0);
-                    if (halves == 2) tma_load_5d(dst + C::SLOT / 2, m, bar, x, 0, 0, row >> 3, p1);
-                }
+                tma_load_5d(dst, m, bar, x, 0, 0, row >> 3, p0);
+                if (halves == 2) tma_load_5d(dst + C::SLOT / 2, m, bar, x, 0, 0, row >> 3, p1);
             }
         };
         const int items = 2 * groups;
         int issued = 0;
         for (; issued < C::SLOTS && issued < items; ++issued) issue(issued);
-        int scales = load_scales(0, pages), scales_next = scales;   // of the groups of `pages`, `pages_next`
 
         // Q rows into shared memory, swizzled as TMA does; rows past the tile are zero
         for (int i = tid; i < C::ROWS * (D / 8); i += THREADS) {
@@ -308,12 +178,6 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (token < a.T)
                     v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + token * a.q_stride +
                                                         (static_cast<long long>(pos.head) * a.G + gh) * D + c8 * 8);
-            }
-            if constexpr (E8) {
-                // in fp16, times the power of two that takes the row's largest channel to [2^14, 2^15): exact but for
-                // channels 2^-22 of it and below, off by 2^-39 of it
-                const float f = q_to_f16<D, F16>(v);
-                if (c8 == 0) reinterpret_cast<float*>(smem + C::FACTOR_OFF)[r] = a.c * f;
             }
             const int panel = c8 >> 3, cc = c8 & 7;
             *reinterpret_cast<uint4*>(smem + C::Q_OFF + panel * (C::ROWS * 128) + r * 128 + ((cc ^ (r & 7)) << 4)) = v;
@@ -339,30 +203,13 @@ __global__ void __launch_bounds__(THREADS, 2)
 
         uint32_t qf[D / 16][4];
         const int q_row = (lane & 7) + ((lane >> 3) & 1) * 8;
-        // 8 bits: a thread's four channels of 16 are the ones that ldmatrix hands it of a key, 4 (lane & 3) .. + 3
         auto load_q = [&](int ks, uint32_t (&f)[4]) {
-            if constexpr (E8) {
-                const int cc = ks * 2 + ((lane >> 1) & 1);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = e * 8 + (lane >> 2);
-                    const uint2 w = *reinterpret_cast<const uint2*>(smem + C::Q_OFF + (cc >> 3) * (C::ROWS * 128) + r * 128 +
-                                                                    (((cc & 7) ^ (r & 7)) << 4) + (lane & 1) * 8);
-                    f[e] = w.x;
-                    f[2 + e] = w.y;
-                }
-                return;
-            }
             const int r = q_row, cc = ks * 2 + (lane >> 4);
             ldmatrix4(q_smem + (cc >> 3) * (C::ROWS * 128) + r * 128 + (((cc & 7) ^ (r & 7)) << 4), f[0], f[1], f[2],
                       f[3]);
         };
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) load_q(ks, qf[ks]);
-        float factor[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            factor[e] = E8 ? reinterpret_cast<const float*>(smem + C::FACTOR_OFF)[e * 8 + (lane >> 2)] : a.c;
         float o[D / 8][4], m_run[2], l_run[2];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -377,9 +224,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 pages = pages_next;
                 page_base = g;
                 pages_next = load_pages(g + 16);
-                scales = scales_next;
             }
-            if (E8 && g == page_base + 1) scales_next = load_scales(page_base + 16, pages_next);   // (the pages have arrived)
             const int key = key_of(g);
             // ---- S = Q K^T
             uint32_t slot = (item + 2 * g) % C::SLOTS, round = (item + 2 * g) / C::SLOTS;
@@ -395,15 +240,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const uint32_t kbase = ring + slot * C::SLOT;
                 const int krow = ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
-                for (int ks = 0; ks < (E8 ? D / 16 : 0); ++ks) {   // four octets of keys, 16 channels
-                    uint32_t w[4];
-                    ldmatrix4(kbase + (lane >> 3) * C::OCTET + code_at<D>(lane & 7, ks), w[0], w[1], w[2], w[3]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma16816<true>(s[i], qf[ks], codes_to_f16x2(w[i]), codes_to_f16x2_high(w[i]));
-                }
-#pragma unroll
-                for (int ks = 0; ks < (E8 ? 0 : D / 16); ++ks) {
+                for (int ks = 0; ks < D / 16; ++ks) {
                     const int cc = ks * 2 + ((lane >> 3) & 1);
                     uint32_t b[GROUP / 16][4];
 #pragma unroll
@@ -425,19 +262,6 @@ __global__ void __launch_bounds__(THREADS, 2)
             const bool masked = key + GROUP > all_hi || key < all_lo;
             bool moved = false;
             float alpha[2];
-            // 8 bits, per 16 keys: x = s c 2^E_k + E_v, so that 2^(x - m) multiplies the numbers of V as they are; the sum
-            // takes the probabilities themselves, 2^-E_v of that (m: the running maximum of x)
-            float k_scale[2] = {1.0f, 1.0f}, v_exp[2] = {0.0f, 0.0f}, v_inv[2] = {1.0f, 1.0f};
-            if constexpr (E8) {
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    const int w = __shfl_sync(0xffffffffu, scales, (g - page_base) * 2 + hb);
-                    const int v = min(max(w >> 8, LEAST_SCALE), 254);   // (of a block that no row sees: anything)
-                    k_scale[hb] = scale_value(w & 255);
-                    v_exp[hb] = static_cast<float>(v - 127);
-                    v_inv[hb] = scale_value(254 - v);
-                }
-            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float mx = __int_as_float(0xff800000);
@@ -445,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (int i = 0; i < GROUP / 8; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float x = E8 ? fmaf(s[i][2 * e + j], factor[e] * k_scale[i >> 1], v_exp[i >> 1]) : s[i][2 * e + j] * a.c;
+                        float x = s[i][2 * e + j] * a.c;
                         if (masked) {
                             const int t = key + i * 8 + (lane & 3) * 2 + j;
                             if (t >= hi_row[e] || t < lo_row[e]) x = __int_as_float(0xff800000);
@@ -477,28 +301,17 @@ __global__ void __launch_bounds__(THREADS, 2)
             // the type, is of the size of the output's own); the sum takes the fp32 values
             uint32_t pf[GROUP / 16][4];
 #pragma unroll
-            for (int kb = 0; kb < GROUP / 16; ++kb) {
-                float sum[2] = {0.0f, 0.0f};
+            for (int kb = 0; kb < GROUP / 16; ++kb)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const float* x = s[2 * kb + hf];
                     const float p0 = ex2_approx(x[0] - m_run[0]), p1 = ex2_approx(x[1] - m_run[0]);
                     const float p2 = ex2_approx(x[2] - m_run[1]), p3 = ex2_approx(x[3] - m_run[1]);
-                    if constexpr (E8) {
-                        sum[0] += p0 + p1;
-                        sum[1] += p2 + p3;
-                    } else {
-                        l_run[0] += p0 + p1;
-                        l_run[1] += p2 + p3;
-                    }
-                    pf[kb][2 * hf] = pack2<F16 || E8>(p0, p1);
-                    pf[kb][2 * hf + 1] = pack2<F16 || E8>(p2, p3);
+                    l_run[0] += p0 + p1;
+                    l_run[1] += p2 + p3;
+                    pf[kb][2 * hf] = pack2<F16>(p0, p1);
+                    pf[kb][2 * hf + 1] = pack2<F16>(p2, p3);
                 }
-                if constexpr (E8) {
-                    l_run[0] = fmaf(sum[0], v_inv[kb], l_run[0]);
-                    l_run[1] = fmaf(sum[1], v_inv[kb], l_run[1]);
-                }
-            }
             // ---- O += P V
             slot = (item + 2 * g + 1) % C::SLOTS;
             round = (item + 2 * g + 1) / C::SLOTS;
@@ -510,11 +323,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                 // before its first row's window): 0 * NaN must not reach the sum
                 const int bad = seq.kv_len > key ? min(seq.kv_len - key, GROUP) : 0;
                 const int from = max(loaded - key, 0), low = max(min(unseen - key, GROUP) - from, 0);   // rows
-                constexpr int PIECES = D * C::BYTES / 16;   // of a row
-                for (int i = lane; i < (low + GROUP - bad) * PIECES; i += 32) {
-                    const int r = i / PIECES + (i < low * PIECES ? from : bad - low), cc = i % PIECES;
-                    const int at = E8 ? r * D + cc * 16 : (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 + (cc & 7) * 16;
-                    *reinterpret_cast<uint4*>(smem + (ring - smem_addr(smem)) + slot * C::SLOT + at) = make_uint4(0, 0, 0, 0);
+                for (int i = lane; i < (low + GROUP - bad) * (D / 8); i += 32) {
+                    const int r = i / (D / 8) + (i < low * (D / 8) ? from : bad - low), cc = i % (D / 8);
+                    *reinterpret_cast<uint4*>(smem + (ring - smem_addr(smem)) + slot * C::SLOT +
+                                              (r >> 3) * C::OCTET + (cc >> 3) * 1024 + (r & 7) * 128 + (cc & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();   // before the next TMA copy into the slot
                 __syncwarp();
@@ -522,26 +335,8 @@ __global__ void __launch_bounds__(THREADS, 2)
             {
                 const uint32_t vbase = ring + slot * C::SLOT;
                 const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7);
-                // 8 bits: a transposed 16-bit element is two channels of a key; the numbers of one channel and two keys side
-                // by side make a fragment, the even channels of 16 in one n8 tile and the odd ones in the next
 #pragma unroll
-                for (int kb = 0; kb < (E8 ? GROUP / 16 : 0); ++kb)
-#pragma unroll
-                    for (int nb = 0; nb < D / 16; nb += 2) {
-                        uint32_t w[4];   // keys 0-7 and 8-15 of channels 16 nb .., then of the next 16
-                        ldmatrix4_trans(vbase + (kb * 2 + ((lane >> 3) & 1)) * C::OCTET + code_at<D>(lane & 7, nb + (lane >> 4)),
-                                        w[0], w[1], w[2], w[3]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], 0, 0x3120);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            mma16816<true>(o[2 * (nb + i)], pf[kb], codes_to_f16x2(w[2 * i]), codes_to_f16x2(w[2 * i + 1]));
-                            mma16816<true>(o[2 * (nb + i) + 1], pf[kb], codes_to_f16x2_high(w[2 * i]),
-                                           codes_to_f16x2_high(w[2 * i + 1]));
-                        }
-                    }
-#pragma unroll
-                for (int kb = 0; kb < (E8 ? 0 : GROUP / 16); ++kb) {
+                for (int kb = 0; kb < GROUP / 16; ++kb) {
                     const int r = kb * 16 + vrow;
 #pragma unroll
                     for (int nb = 0; nb < D / 16; ++nb) {
@@ -578,18 +373,10 @@ __global__ void __launch_bounds__(THREADS, 2)
             const int r = e * 8 + (lane >> 2);
             if (r >= n_rows) continue;
             if ((lane & 3) == 0) join_ml[warp * C::ROWS + r] = make_float2(m_run[e], l_run[e]);
-            if constexpr (E8) {
-                float* d = join_o + (warp * C::ROWS + r) * C::O_STRIDE + (lane & 3) * 4;
+            float* d = join_o + (warp * C::ROWS + r) * C::O_STRIDE + (lane & 3) * 2;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    *reinterpret_cast<float4*>(d + i * 16) =
-                        make_float4(o[2 * i][2 * e], o[2 * i + 1][2 * e], o[2 * i][2 * e + 1], o[2 * i + 1][2 * e + 1]);
-            } else {
-                float* d = join_o + (warp * C::ROWS + r) * C::O_STRIDE + (lane & 3) * 2;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<float2*>(d + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-            }
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2*>(d + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
         }
         __syncthreads();
         // this piece's CTA slot: 2c + 1 for a piece that starts its tile, 2c for one that continues it
@@ -640,47 +427,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             __syncthreads();
             if (*last_flag) {
                 __threadfence();   // the other CTAs' parts, published before their counts
-                for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
-                    const int r = i / (D / 4), c4 = i % (D / 4);
-                    float m = NO_MAX, l = 0.0f;
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    // in CTA order, a batch at a time in flight (past the last: the last once more, at weight 0)
-                    for (int cb = c0; cb <= c1; cb += JOIN_BATCH) {
-                        float2 ml[JOIN_BATCH];
-                        float4 v[JOIN_BATCH];
-#pragma unroll
-                        for (int j = 0; j < JOIN_BATCH; ++j) {
-                            const int c = min(cb + j, c1);
-                            const size_t at = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * C::ROWS + r;
-                            ml[j] = __ldcg(a.work.part_ml + at);
-                            v[j] = __ldcg(reinterpret_cast<const float4*>(a.work.part_o + at * D + c4 * 4));
-                            if (cb + j > c1) ml[j] = make_float2(NO_MAX, 0.0f);
-                        }
-                        float m_new = m;
-#pragma unroll
-                        for (int j = 0; j < JOIN_BATCH; ++j) m_new = fmaxf(m_new, ml[j].x);
-                        const float f0 = ex2_approx(m - m_new);
-                        m = m_new;
-                        l *= f0;
-                        acc.x *= f0;
-                        acc.y *= f0;
-                        acc.z *= f0;
-                        acc.w *= f0;
-#pragma unroll
-                        for (int j = 0; j < JOIN_BATCH; ++j) {
-                            const float f = cb + j > c1 ? 0.0f : ex2_approx(ml[j].x - m);
-                            l += ml[j].y * f;
-                            acc.x += v[j].x * f;
-                            acc.y += v[j].y * f;
-                            acc.z += v[j].z * f;
-                            acc.w += v[j].w * f;
-                        }
-                    }
-                    int t, gh;
-                    fdivmod(r, a.fd_G, t, gh);
-                    const int token = seq.q_start + tok0 + t;
-                    if (token < a.T) store_out<F16>(a, token, pos.head * a.G + gh, c4, acc, m, l);
-                }
+                join_parts<D, C::ROWS, THREADS, F16>(a, seq.q_start + tok0, pos.head, n_rows, c0, c1);
             }
         }
         fence_proxy_async_smem();   // the joined results before the next copies into the ring
@@ -691,32 +438,21 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
 }
 
-template <int D, bool F16, bool E8, typename Args>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a, cudaStream_t stream) {
-    auto kern = attn_paged_rows_kernel<D, F16, E8>;
-    const int smem = RowsCfg<D, E8>::ALLOC;
+template <int D, bool F16>
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, cudaStream_t stream) {
+    auto kern = attn_paged_rows_kernel<D, F16>;
+    const int smem = RowsCfg<D>::ALLOC;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_overlapped(kern, dim3(static_cast<unsigned>(a.tile.grid)), THREADS, smem, stream, tk, tv, a);
-}
-
-template <bool E8, typename Args>
-cudaError_t launch_any(const CUtensorMap& tk, const CUtensorMap& tv, const Args& a, int dtype, cudaStream_t stream) {
-    if (a.D == 128)
-        return dtype == 0 ? launch_rows<128, false, E8>(tk, tv, a, stream) : launch_rows<128, true, E8>(tk, tv, a, stream);
-    return dtype == 0 ? launch_rows<64, false, E8>(tk, tv, a, stream) : launch_rows<64, true, E8>(tk, tv, a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, int dtype,
                                    cudaStream_t stream) {
-    return launch_any<false>(tk, tv, a, dtype, stream);
-}
-
-cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
-                                    cudaStream_t stream) {
-    return launch_any<true>(tk, tv, a, dtype, stream);
+    if (a.D == 128) return dtype == 0 ? launch_rows<128, false>(tk, tv, a, stream) : launch_rows<128, true>(tk, tv, a, stream);
+    return dtype == 0 ? launch_rows<64, false>(tk, tv, a, stream) : launch_rows<64, true>(tk, tv, a, stream);
 }
 
 cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
