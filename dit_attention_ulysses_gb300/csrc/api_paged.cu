@@ -66,8 +66,9 @@ int encode_q(CUtensorMap* m, const void* base, int T, int Hkv, int G, int D, lon
 }
 
 // ---- tiling of the paged attention, a function of the shape alone
-Tiling make_tiling(int G, int D, int max_q, int sms) {
+Tiling make_tiling(int, int, int G, int D, int max_q, int sms) {
     Tiling x{};
+    x.t.heads = 1;
     const int64_t need = static_cast<int64_t>(G) * max_q;
     // Few-tokens kernel against chunk kernel, us, by keys (which the host does not know):
     //   rows, heads    1 x 300   1 x 4096   1 x 32768  4 x 4096   16 x 1000  64 x 2048  32 x 8192  64 ragged

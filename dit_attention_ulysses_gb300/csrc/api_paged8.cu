@@ -63,18 +63,17 @@ xs::Codes8 codes_of(void* code, void* scale, const CacheStrides& cs, const Cache
     return x;
 }
 
-// [n_pages, page, Hkv, D] as the 3-D tensor (element, token, page); the heads lie along the first dimension,
-// whatever their stride.  Box: `box_rows` tokens of one head.
-int encode_cache8(CUtensorMap* m, const void* base, const CacheStrides& s, const xs_paged_cache8& c, int box_rows) {
+// [n_pages, page, Hkv, D] as the 4-D tensor (element, token, head, page).  Box: `box_rows` tokens of `heads` heads.
+int encode_cache8(CUtensorMap* m, const void* base, const CacheStrides& s, const xs_paged_cache8& c, int box_rows, int heads) {
     PFN_cuTensorMapEncodeTiled_v12000 enc;
     int rc = get_encoder(&enc);
     if (rc != XS_OK) return rc;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>((c.Hkv - 1) * s.s[2] + c.D), static_cast<cuuint64_t>(c.page_size),
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.Hkv),
                                 static_cast<cuuint64_t>(c.n_pages)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.s[1]), static_cast<cuuint64_t>(s.s[0])};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.D), static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s.s[1]), static_cast<cuuint64_t>(s.s[2]), static_cast<cuuint64_t>(s.s[0])};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.D), static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(heads), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE,
                            c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                            c.D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
@@ -83,9 +82,10 @@ int encode_cache8(CUtensorMap* m, const void* base, const CacheStrides& s, const
     return XS_OK;
 }
 
-Tiling make_tiling8(int G, int D, int max_q, int sms) {
+Tiling make_tiling8(int n, int Hkv, int G, int D, int max_q, int sms) {
     Tiling x{};
     x.t.cache8 = 1;
+    x.t.heads = 1;
     if (static_cast<int64_t>(G) * max_q > ROWS_FEW) {
         x.rows = ROWS_TILE;
         x.t.tokens = ROWS_TILE / G;
@@ -104,9 +104,10 @@ Tiling make_tiling8(int G, int D, int max_q, int sms) {
     }
     x.rows = static_cast<int64_t>(G) * max_q <= ROWS_FEW / 2 ? ROWS_FEW / 2 : ROWS_FEW;
     x.t.tokens = x.rows / G;
+    if (x.rows == ROWS_FEW / 2 && Hkv % 2 == 0 && static_cast<int64_t>(n) * Hkv >= 2 * sms) x.t.heads = 2;
     x.t.block = 32;
     x.t.grid = 2 * sms;
-    x.t.start_cost = 256;
+    x.t.start_cost = 512;
     x.t.snap = 4;
     x.t.whole = 20;
     x.t.least = 512;
@@ -278,8 +279,8 @@ int xs_attn_paged8_fwd(const xs_attn_paged8_args* args, void* stream) {
     const int box_max = tiling.rows == ROWS_TILE ? 128 : 32;
     const int box = cache.page_size < box_max ? cache.page_size : box_max;
     CUtensorMap tk, tv;
-    if ((rc = encode_cache8(&tk, cache.k, x.ks, cache, box)) != XS_OK) return rc;
-    if ((rc = encode_cache8(&tv, cache.v, x.vs, cache, box)) != XS_OK) return rc;
+    if ((rc = encode_cache8(&tk, cache.k, x.ks, cache, box, tiling.t.heads)) != XS_OK) return rc;
+    if ((rc = encode_cache8(&tv, cache.v, x.vs, cache, box, tiling.t.heads)) != XS_OK) return rc;
     const auto launch = tiling.rows == ROWS_TILE ? xs::launch_attn_paged8 : xs::launch_attn_paged8_rows;
     const cudaError_t e = launch(tk, tv, a, cache.dtype, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : cuda_fail(e);

@@ -194,7 +194,6 @@ __device__ __forceinline__ bool load_blocks(const CUtensorMap* map, const PagedA
     const uint32_t stages = is_v ? C::C_STAGES : C::K_STAGES;
     const uint32_t base = smem_addr(smem + (is_v ? C::C_OFF : C::K_OFF));
     const uint32_t full0 = bar(is_v ? C::B_C_FULL : C::B_K_FULL), free0 = bar(is_v ? C::B_C_FREE : C::B_K_FREE);
-    const int x = d.head * (is_v ? a.v_head : a.k_head);
     volatile uint32_t* const loaded = reinterpret_cast<volatile uint32_t*>(smem + C::LOADED_OFF) + (is_v ? C::K_STAGES : 0);
     Scales* const scales = reinterpret_cast<Scales*>(smem + C::SCALES_OFF);
     const int* table = a.table + static_cast<long long>(d.index) * a.table_stride;
@@ -237,8 +236,8 @@ __device__ __forceinline__ bool load_blocks(const CUtensorMap* map, const PagedA
         __syncwarp();
         if (!ok) return false;
         if (lane < boxes)
-            tma_load_3d(base + stage * (BLOCK_N * D) + lane * box * D, map, full0 + stage * 8u, x,
-                        (d.key0 + j * BLOCK_N) & ((1 << a.page_shift) - 1), page);
+            tma_load_4d(base + stage * (BLOCK_N * D) + lane * box * D, map, full0 + stage * 8u, 0,
+                        (d.key0 + j * BLOCK_N) & ((1 << a.page_shift) - 1), d.head, page);
         if (is_v) {
             const uint32_t slot = item % SCALE_SLOTS;
             if ((lane >> 3) == (j & 3)) {

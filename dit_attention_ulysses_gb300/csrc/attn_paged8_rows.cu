@@ -40,19 +40,20 @@ constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int GROUP = 32;                  // keys of a ring slot
 
-template <int D, bool F16, int NT>
+// HP: KV heads of a tile, of up to 8 rows each (row 8 n + r: row r of head n); otherwise up to 8 NT rows of one head.
+template <int D, bool F16, int NT, int HP>
 struct Rows8Cfg {
+    static_assert(HP == 1 || HP == NT, "");
     static constexpr int ROWS = 8 * NT;
     static constexpr int PARTS = F16 ? 3 : 2;          // numbers per channel of Q
-    static constexpr int SLOT = GROUP * D;
-    static constexpr int SLOTS = 6 * 128 / D;          // per warp
+    static constexpr int SLOT = HP * GROUP * D;
+    static constexpr int SLOTS = 6 * 128 / D / HP;     // per warp
     static constexpr int RING = WARPS * SLOTS * SLOT;  // 96 KB
     static constexpr int Q_STRIDE = D + 16;            // bytes; keeps eight rows' words on different banks
-    // a warp's results wait for their join in ring slots that the next piece's first copies do not use
-    static constexpr int O_STRIDE = D + 4;             // floats; keeps the stores of four rows on different banks
-    static constexpr int SLOT_ROWS = SLOT / (O_STRIDE * 4);
-    static constexpr int JOIN_SLOTS = (ROWS + SLOT_ROWS - 1) / SLOT_ROWS;
-    static constexpr int AHEAD = SLOTS - JOIN_SLOTS;
+    // a warp's results wait for their join in ring slots that the next piece's first copies do not use: SLOT_ROWS rows of
+    // D floats to a slot, the channels of row r xor 8 (r / 2 % 4), which keeps a store's four rows on different banks
+    static constexpr int SLOT_ROWS = 8 * HP;
+    static constexpr int AHEAD = SLOTS - ROWS / SLOT_ROWS;
     static constexpr int Q_OFF = RING;
     static constexpr int ML_OFF = (Q_OFF + PARTS * ROWS * Q_STRIDE + 15) / 16 * 16;
     static constexpr int FACTOR_OFF = ML_OFF + WARPS * ROWS * 8;   // c 2^E_q of every row
@@ -104,11 +105,11 @@ __device__ __forceinline__ uint32_t code_at(int key, int chunk) {
     return key * D + ((chunk ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4);
 }
 
-template <int D, bool F16, int NT>
+template <int D, bool F16, int NT, int HP>
 __global__ void __launch_bounds__(THREADS, 2)
     attn_paged8_rows_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                             const __grid_constant__ PagedAttn8Args a) {
-    using C = Rows8Cfg<D, F16, NT>;
+    using C = Rows8Cfg<D, F16, NT, HP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -130,10 +131,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     pdl_wait();
     const PagedRange range = a.work.ranges[blockIdx.x];
-    const int n_seqs = a.work.header->n_seqs;
+    const int n_seqs = a.work.header->n_seqs, tile_heads = a.Hkv / HP;
     {
         const PagedHeader& h = *a.work.header;
-        if (h.n != a.n || h.H != a.H || h.Hkv != a.Hkv || h.D != D || h.tokens != a.tile.tokens ||
+        if (h.n != a.n || h.H != a.H || h.Hkv != tile_heads || h.D != D || h.tokens != a.tile.tokens ||
             h.block != a.tile.block || h.grid != a.tile.grid || h.causal != a.causal || h.window != a.window || h.cache8 != 1) {
             if (tid == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, h.n, h.tokens, h.grid);
             return;
@@ -144,6 +145,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int page_size = 1 << a.page_shift;
     const int box = page_size < GROUP ? page_size : GROUP;   // rows of one TMA copy: 16 or 32
     const int halves = GROUP / box;
+    // a slot holds units of 16 keys of a head: a copy's heads one after the other, its keys together
+    const int unit_keys = halves == 2 ? HP * 16 * D : 16 * D, unit_head = halves == 2 ? 16 * D : GROUP * D;
     uint32_t k_at[D / 32], v_at[D / 32];   // a lane's offsets in a slot, by 32 channels
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -161,6 +164,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     int pages = -1, pages_next = -1, page_base = 0, scales = 0, scales_next = 0;
     uint4 q_ahead[NT];
     const int* table;
+    auto row_of = [](int r) { return HP == 1 ? r : r & 7; };                          // row of its head
+    auto head_of = [](int head, int r) { return HP == 1 ? head : head * HP + (r >> 3); };   // KV head of a tile's row
     auto key_of = [&](int g) { return key0 + (warp + WARPS * g) * GROUP; };
     // page number of half `lane & 1` of group `first + lane / 2`; -1 (read as zeros) past the keys,
     // before the window and past the table
@@ -171,15 +176,17 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int col = key >> a.page_shift;
         return static_cast<unsigned>(col) < static_cast<unsigned>(a.width) ? table[col] : -1;
     };
-    // scale bytes of the 16 keys `lane & 1` of group `first + lane / 2`: K's, V's << 8
+    // scale bytes of the 16 keys `lane & 1` of group `first + lane / 2`: K's, V's << 8, the second head's << 16
     auto load_scales = [&](int first, int page) -> int {
-        int w = 127 | 127 << 8;
+        int w = 127 | 127 << 8 | 127 << 16 | 127 << 24;
         if (halves == 1) page = __shfl_sync(0xffffffffu, page, lane & ~1);
         if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
             const int off = (key_of(first + (lane >> 1)) + (lane & 1) * 16) & (page_size - 1);
             const int b = off >> a.block_shift;
-            w = a.k_scale[page * a.k_scale_strides[0] + b * a.k_scale_strides[1] + pos.head * a.k_scale_strides[2]] |
-                a.v_scale[page * a.v_scale_strides[0] + b * a.v_scale_strides[1] + pos.head * a.v_scale_strides[2]] << 8;
+            const uint8_t* k = a.k_scale + page * a.k_scale_strides[0] + b * a.k_scale_strides[1] + pos.head * HP * a.k_scale_strides[2];
+            const uint8_t* v = a.v_scale + page * a.v_scale_strides[0] + b * a.v_scale_strides[1] + pos.head * HP * a.v_scale_strides[2];
+            w = k[0] | v[0] << 8;
+            if constexpr (HP == 2) w |= k[a.k_scale_strides[2]] << 16 | v[a.v_scale_strides[2]] << 24;
         }
         return w;
     };
@@ -193,9 +200,8 @@ __global__ void __launch_bounds__(THREADS, 2)
             mbar_arrive_expect_tx(bar, C::SLOT);
             const int row = key_of(g) & (page_size - 1);
             const CUtensorMap* m = (i & 1) ? &tv : &tk;
-            const int x = pos.head * ((i & 1) ? a.v_head : a.k_head);
-            tma_load_3d(dst, m, bar, x, row, p0);
-            if (halves == 2) tma_load_3d(dst + C::SLOT / 2, m, bar, x, row, p1);
+            tma_load_4d(dst, m, bar, 0, row, pos.head * HP, p0);
+            if (halves == 2) tma_load_4d(dst + C::SLOT / 2, m, bar, 0, row, pos.head * HP, p1);
         }
     };
     auto issue_up_to = [&](int most) {   // items in slots that have been read, counted from the next to be waited for
@@ -203,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     };
     // Opens the piece at `pos`; false: the plan names a tile that is not there.
     auto open_piece = [&]() -> bool {
-        if (!paged_valid(pos, seq, n_seqs, a.tile.tokens, a.Hkv)) {
+        if (!paged_valid(pos, seq, n_seqs, a.tile.tokens, tile_heads)) {
             if (tid == 0) report_error(XS_DEVICE_BOUNDS_CODE, PAGED_MAGIC_SITE, pos.seq, pos.head, pos.tile);
             return false;
         }
@@ -227,15 +233,15 @@ __global__ void __launch_bounds__(THREADS, 2)
         pages_next = load_pages(16);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {   // 8 channels of a row, D / 8 lanes side by side
-            const int at = tid + i * THREADS, r = at / (D / 8);
+            const int at = tid + i * THREADS, r = row_of(at / (D / 8));
             q_ahead[i] = make_uint4(0, 0, 0, 0);
-            if (r < n_tok * a.G) {
+            if (r < n_tok * a.G && at / (D / 8) < C::ROWS) {
                 int t, gh;
                 fdivmod(r, a.fd_G, t, gh);
                 const long long token = static_cast<long long>(seq.q_start) + tok0 + t;
                 if (token < a.T)
                     q_ahead[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + token * a.q_stride +
-                                                                 (static_cast<long long>(pos.head) * a.G + gh) * D + at % (D / 8) * 8);
+                                                                 (static_cast<long long>(head_of(pos.head, at / (D / 8))) * a.G + gh) * D + at % (D / 8) * 8);
             }
         }
         return true;
@@ -289,11 +295,11 @@ __global__ void __launch_bounds__(THREADS, 2)
         PagedSeq next_seq = seq;
         bool more = false;
         if (!cut_end) {
-            const bool other = paged_next(next, seq, a.tile.tokens, a.Hkv);
+            const bool other = paged_next(next, seq, a.tile.tokens, tile_heads);
             more = paged_before(next, range.end);
             if (other && more && next.seq < n_seqs) next_seq = a.work.seqs[next.seq];
         }
-        const int n_rows = n_tok * a.G;
+        const int n_rows = n_tok * a.G;   // of a head
         const long long base = static_cast<long long>(seq.kv_len) - seq.q_len;
         // keys [loaded, unseen) come in with the first copy although no row of the sequence sees them
         const int loaded = lo_tile & ~(box - 1);
@@ -355,14 +361,17 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t k[4];
-                    ldmatrix4(kbase + k_at[i] + b * (16 * D), k[0], k[1], k[2], k[3]);
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int p = 0; p < C::PARTS; ++p)
+                    for (int hp = 0; hp < HP; ++hp) {
+                        uint32_t k[4];
+                        ldmatrix4(kbase + k_at[i] + b * unit_keys + hp * unit_head, k[0], k[1], k[2], k[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16832(s[b][n], k, qf[p][n][i][0], qf[p][n][i][1]);
-                }
+                        for (int p = 0; p < C::PARTS; ++p)
+#pragma unroll
+                            for (int n = hp; n < (HP == 1 ? NT : hp + 1); ++n)
+                                mma16832(s[b][n], k, qf[p][n][i][0], qf[p][n][i][1]);
+                    }
             __syncwarp();   // every lane has read the slot
             if (issued < 2 * groups) issue(issued++, slot);
             if (++slot == C::SLOTS) {
@@ -371,24 +380,28 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
             // ---- softmax of the group
             const bool masked = key + GROUP > all_hi || key < all_lo;
-            float v_inv[2];
+            float v_inv[2][HP];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int w = __shfl_sync(0xffffffffu, scales, (g - page_base) * 2 + b);
-                const int v = min(max(w >> 8, LEAST_SCALE), 254);   // (of a block that no row sees: anything)
-                const float k = scale_value(w & 255), v_exp = static_cast<float>(v - 127);
-                v_inv[b] = scale_value(254 - v);
+                const uint32_t w = __shfl_sync(0xffffffffu, scales, (g - page_base) * 2 + b);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int hp = 0; hp < HP; ++hp) {
+                    // (of a block that no row sees: anything)
+                    const int v = min(max(static_cast<int>(w >> (16 * hp + 8) & 255), LEAST_SCALE), 254);
+                    const float k = scale_value(w >> 16 * hp & 255), v_exp = static_cast<float>(v - 127);
+                    v_inv[b][hp] = scale_value(254 - v);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[b][n][e] = fmaf(s[b][n][e], factor[n][e & 1] * k, v_exp);
+                    for (int n = hp; n < (HP == 1 ? NT : hp + 1); ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[b][n][e] = fmaf(s[b][n][e], factor[n][e & 1] * k, v_exp);
+                }
             }
             if (masked) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = 8 * n + 2 * c4 + e;
+                        const int r = row_of(8 * n + 2 * c4 + e);
                         const long long p = base + tok0 + fdiv(r, a.fd_G);
                         long long h = a.causal ? p + 1 : seq.kv_len;   // the row sees keys [l, h)
                         const long long l = a.window > 0 ? p - a.window + 1 : 0;
@@ -450,8 +463,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[b][n][e] - m_run[n][e & 1]);
-                    l_run[n][0] = fmaf(p[0] + p[2], v_inv[b], l_run[n][0]);
-                    l_run[n][1] = fmaf(p[1] + p[3], v_inv[b], l_run[n][1]);
+                    l_run[n][0] = fmaf(p[0] + p[2], v_inv[b][HP == 1 ? 0 : n], l_run[n][0]);
+                    l_run[n][1] = fmaf(p[1] + p[3], v_inv[b][HP == 1 ? 0 : n], l_run[n][1]);
                     pf[b][n][0] = transposed(pack_f16x2(p[0], p[1]));
                     pf[b][n][1] = transposed(pack_f16x2(p[2], p[3]));
                 }
@@ -464,10 +477,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                 // before its first row's window): 0 * NaN must not reach the sum
                 const int bad = seq.kv_len > key ? min(seq.kv_len - key, GROUP) : 0;
                 const int from = max(loaded - key, 0), low = max(min(unseen - key, GROUP) - from, 0);   // rows
-                for (int i = lane; i < (low + GROUP - bad) * (D / 16); i += 32) {
-                    const int r = i / (D / 16) + (i < low * (D / 16) ? from : bad - low);
-                    *reinterpret_cast<uint4*>(smem + (ring - smem_addr(smem)) + slot * C::SLOT + r * D + i % (D / 16) * 16) =
-                        make_uint4(0, 0, 0, 0);
+                for (int i = lane; i < (low + GROUP - bad) * (D / 16) * HP; i += 32) {
+                    const int j = i / (D / 16) / HP, r = j + (j < low ? from : bad - low), hp = i / (D / 16) % HP;
+                    *reinterpret_cast<uint4*>(smem + (ring - smem_addr(smem)) + slot * C::SLOT + (r >> 4) * unit_keys + hp * unit_head +
+                                              (r & 15) * D + i % (D / 16) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();   // before the next TMA copy into the slot
                 __syncwarp();
@@ -476,17 +489,20 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t w[4];   // channels 32 i + g8 + (0, 8, 16, 24), a lane's four keys
-                    ldmatrix2_trans8(vbase + v_at[i] + b * (16 * D), w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t v[4] = {codes_to_f16x2(w[2 * h]), codes_to_f16x2(w[2 * h + 1]), codes_to_f16x2_high(w[2 * h]),
-                                               codes_to_f16x2_high(w[2 * h + 1])};
+                    for (int hp = 0; hp < HP; ++hp) {
+                        uint32_t w[4];   // channels 32 i + g8 + (0, 8, 16, 24), a lane's four keys
+                        ldmatrix2_trans8(vbase + v_at[i] + b * unit_keys + hp * unit_head, w[0], w[1], w[2], w[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816<true>(o[2 * i + h][n], v, pf[b][n][0], pf[b][n][1]);
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t v[4] = {codes_to_f16x2(w[2 * h]), codes_to_f16x2(w[2 * h + 1]),
+                                                   codes_to_f16x2_high(w[2 * h]), codes_to_f16x2_high(w[2 * h + 1])};
+#pragma unroll
+                            for (int n = hp; n < (HP == 1 ? NT : hp + 1); ++n)
+                                mma16816<true>(o[2 * i + h][n], v, pf[b][n][0], pf[b][n][1]);
+                        }
                     }
-                }
             __syncwarp();
             if (issued < 2 * groups) issue(issued++, slot);
             if (++slot == C::SLOTS) {
@@ -528,9 +544,9 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], d);
         const uint32_t first_slot = (slot + C::AHEAD) % C::SLOTS;
-        auto join_row = [&](int w, uint32_t first, int r) -> float* {   // row r of warp w's results
+        auto join_at = [&](int w, uint32_t first, int r, int channel) -> float* {   // row r of warp w's results
             const uint32_t at = (first + r / C::SLOT_ROWS) % C::SLOTS;
-            return reinterpret_cast<float*>(smem + (w * C::SLOTS + at) * C::SLOT) + r % C::SLOT_ROWS * C::O_STRIDE;
+            return reinterpret_cast<float*>(smem + (w * C::SLOTS + at) * C::SLOT) + r % C::SLOT_ROWS * D + (channel ^ (r / 2 % 4 * 8));
         };
         if (lane == 0) join_slot[warp] = static_cast<int>(first_slot);
 #pragma unroll
@@ -538,13 +554,12 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * n + 2 * c4 + e;
-                if (r >= n_rows) continue;
+                if (row_of(r) >= n_rows) continue;
                 if (g8 == 0) join_ml[warp * C::ROWS + r] = make_float2(m_run[n][e], l_run[n][e]);
-                float* d = join_row(warp, first_slot, r) + g8;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    d[i * 16] = o[i][n][e];
-                    d[i * 16 + 8] = o[i][n][e + 2];
+                    *join_at(warp, first_slot, r, i * 16 + g8) = o[i][n][e];
+                    *join_at(warp, first_slot, r, i * 16 + 8 + g8) = o[i][n][e + 2];
                 }
             }
         __syncthreads();
@@ -557,8 +572,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int w = 0; w < WARPS; ++w) firsts[w] = static_cast<uint32_t>(join_slot[w]);
         // this piece's CTA slot: 2c + 1 for a piece that starts its tile, 2c for one that continues it
         const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0);
-        for (int i = tid; i < n_rows * (D / 4); i += THREADS) {
-            const int r = i / (D / 4), q4 = i % (D / 4);
+        for (int i = tid; i < n_rows * HP * (D / 4); i += THREADS) {
+            const int hp = i / (D / 4) % HP, r = i / (D / 4) / HP + 8 * hp, q4 = i % (D / 4);
             float m = NO_MAX;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) m = fmaxf(m, join_ml[w * C::ROWS + r].x);
@@ -568,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int w = 0; w < WARPS; ++w) {
                 const float2 ml = join_ml[w * C::ROWS + r];
                 const float f = ex2_approx(ml.x - m);
-                const float4 v = *reinterpret_cast<const float4*>(join_row(w, firsts[w], r) + q4 * 4);
+                const float4 v = *reinterpret_cast<const float4*>(join_at(w, firsts[w], r, q4 * 4));
                 l += ml.y * f;
                 acc.x += v.x * f;
                 acc.y += v.y * f;
@@ -577,9 +592,9 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
             if (tile_whole) {
                 int t, gh;
-                fdivmod(r, a.fd_G, t, gh);
+                fdivmod(row_of(r), a.fd_G, t, gh);
                 const int token = row0 + t;
-                if (token < a.T) store_out<F16>(a, token, head * a.G + gh, q4, acc, m, l);
+                if (token < a.T) store_out<F16>(a, token, head_of(head, r) * a.G + gh, q4, acc, m, l);
             } else {
                 *reinterpret_cast<float4*>(a.work.part_o + (part * C::ROWS + r) * D + q4 * 4) = acc;
                 if (q4 == 0) a.work.part_ml[part * C::ROWS + r] = make_float2(m, l);
@@ -601,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             __syncthreads();
             if (*last_flag) {
                 __threadfence();   // the other CTAs' parts, published before their counts
-                join_parts<D, C::ROWS, THREADS, F16>(a, row0, head, n_rows, c0, c1);
+                join_parts<D, C::ROWS, THREADS, HP, F16>(a, row0, head, n_rows, c0, c1);
             }
         }
         if (opened) store_q();
@@ -612,26 +627,27 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
 }
 
-template <int D, bool F16, int NT>
+template <int D, bool F16, int NT, int HP>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, cudaStream_t stream) {
-    auto kern = attn_paged8_rows_kernel<D, F16, NT>;
-    constexpr int smem = Rows8Cfg<D, F16, NT>::ALLOC;
+    auto kern = attn_paged8_rows_kernel<D, F16, NT, HP>;
+    constexpr int smem = Rows8Cfg<D, F16, NT, HP>::ALLOC;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_overlapped(kern, dim3(static_cast<unsigned>(a.tile.grid)), THREADS, smem, stream, tk, tv, a);
 }
 
-template <int NT>
+template <int NT, int HP>
 cudaError_t launch_any(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype, cudaStream_t stream) {
-    if (a.D == 128) return dtype == 0 ? launch<128, false, NT>(tk, tv, a, stream) : launch<128, true, NT>(tk, tv, a, stream);
-    return dtype == 0 ? launch<64, false, NT>(tk, tv, a, stream) : launch<64, true, NT>(tk, tv, a, stream);
+    if (a.D == 128) return dtype == 0 ? launch<128, false, NT, HP>(tk, tv, a, stream) : launch<128, true, NT, HP>(tk, tv, a, stream);
+    return dtype == 0 ? launch<64, false, NT, HP>(tk, tv, a, stream) : launch<64, true, NT, HP>(tk, tv, a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
                                     cudaStream_t stream) {
-    return a.tile.tokens * a.G <= 8 ? launch_any<1>(tk, tv, a, dtype, stream) : launch_any<2>(tk, tv, a, dtype, stream);
+    if (a.tile.heads == 2) return launch_any<2, 2>(tk, tv, a, dtype, stream);
+    return a.tile.tokens * a.G <= 8 ? launch_any<1, 1>(tk, tv, a, dtype, stream) : launch_any<2, 1>(tk, tv, a, dtype, stream);
 }
 
 cudaError_t read_and_clear_paged8_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             __syncthreads();
             if (*last_flag) {
                 __threadfence();   // the other CTAs' parts, published before their counts
-                join_parts<D, C::ROWS, THREADS, F16>(a, seq.q_start + tok0, pos.head, n_rows, c0, c1);
+                join_parts<D, C::ROWS, THREADS, 1, F16>(a, seq.q_start + tok0, pos.head, n_rows, c0, c1);
             }
         }
         fence_proxy_async_smem();   // the joined results before the next copies into the ring

@@ -138,6 +138,7 @@ struct PagedTiling {
     // below few_keys keys per CTA on average (waves == 0) these replace start_cost and least
     int few_keys, few_start_cost, few_least;
     int cache8;     // for the 8-bit cache
+    int heads;      // KV heads of a tile: the plan's heads are so many
 };
 constexpr int MAX_PAGED_WAVES = 64;
 
@@ -240,8 +241,8 @@ cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv,
 cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PagedAttnArgs& a, int dtype, cudaStream_t stream);
 
-// tk, tv: an 8-bit cache as the 3-D tensor (element, token, page), the head in the first coordinate; a box, one
-// page's tokens of one head, lands as [token][channel] with a row's 16-byte pieces swizzled over its D bytes.
+// tk, tv: an 8-bit cache as the 4-D tensor (element, token, head, page); a box, one page's tokens of a tile's heads, lands
+// as [head][token][channel] with a row's 16-byte pieces swizzled over its D bytes.
 cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
                                     cudaStream_t stream);
 cudaError_t launch_attn_paged8(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,

@@ -211,7 +211,7 @@ inline size_t paged_work(char* base, int n, int D, int sms, xs::PagedWork* w) {
 }
 
 // Tiling of the paged attention, a function of the shape alone.
-using TilingOf = Tiling (*)(int G, int D, int max_q, int sms);
+using TilingOf = Tiling (*)(int n, int Hkv, int G, int D, int max_q, int sms);
 
 inline int plan_attn(TilingOf tiling_of, const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,
                      int window, void* workspace, size_t workspace_bytes, void* stream) {
@@ -231,11 +231,11 @@ inline int plan_attn(TilingOf tiling_of, const int* cu_q, const int* kv_lens, in
     a.kv_lens = kv_lens;
     a.n = n;
     a.H = H;
-    a.Hkv = Hkv;
     a.D = D;
     a.causal = causal ? 1 : 0;
     a.window = window;
-    a.tile = tiling_of(H / Hkv, D, max_q, dev.sms).t;
+    a.tile = tiling_of(n, Hkv, H / Hkv, D, max_q, dev.sms).t;
+    a.Hkv = Hkv / a.tile.heads;
     const cudaError_t e = xs::launch_paged_plan(a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? XS_OK : cuda_fail(e);
 }
@@ -289,7 +289,7 @@ int prepare_attn(const Args& g, TilingOf tiling_of, const Range* more, int n_mor
     DeviceInfo dev;
     if ((rc = device_info(&dev)) != XS_OK) return rc;
     if (g.workspace_bytes < paged_work(static_cast<char*>(g.workspace), n, D, dev.sms, &a->work)) return XS_ERR_WORKSPACE;
-    *tiling = tiling_of(H / Hkv, D, g.max_q, dev.sms);
+    *tiling = tiling_of(n, Hkv, H / Hkv, D, g.max_q, dev.sms);
     a->q = g.q;
     a->table = g.block_table;
     a->lse = g.lse;

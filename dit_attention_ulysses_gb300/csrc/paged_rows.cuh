@@ -14,7 +14,6 @@
 namespace xs {
 namespace {
 
-constexpr int JOIN_BATCH = 16;             // parts of a cut tile read at once
 constexpr float NO_MAX = -3.402823466e38f;           // running maximum of a row that has seen nothing
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units; P stays below 2^8
 
@@ -95,11 +94,13 @@ __device__ __forceinline__ void store_out(const PagedAttnArgs& a, int token, int
             l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000);
 }
 
-// The parts of CTAs c0 .. c1 of a cut tile, joined in CTA order and stored; by a whole CTA.
-template <int D, int ROWS, int THREADS, bool F16>
+// The parts of CTAs c0 .. c1 of a cut tile, joined in CTA order and stored; by a whole CTA.  A tile of HP KV heads
+// holds n_rows rows of each, row 8 h + r of its parts row r of head h.
+constexpr int JOIN_BATCH = 16;             // parts read at once
+template <int D, int ROWS, int THREADS, int HP, bool F16>
 __device__ __forceinline__ void join_parts(const PagedAttnArgs& a, int row0, int kv_head, int n_rows, int c0, int c1) {
-    for (int i = threadIdx.x; i < n_rows * (D / 4); i += THREADS) {
-        const int r = i / (D / 4), c4 = i % (D / 4);
+    for (int i = threadIdx.x; i < n_rows * HP * (D / 4); i += THREADS) {
+        const int hp = i / (D / 4) % HP, r = i / (D / 4) / HP + 8 * hp, c4 = i % (D / 4);
         float m = NO_MAX, l = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         // a batch at a time in flight (past the last: the last once more, at weight 0)
@@ -135,9 +136,9 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& a, int row0, int
             }
         }
         int t, gh;
-        fdivmod(r, a.fd_G, t, gh);
+        fdivmod(r - 8 * hp, a.fd_G, t, gh);
         const int token = row0 + t;
-        if (token < a.T) store_out<F16>(a, token, kv_head * a.G + gh, c4, acc, m, l);
+        if (token < a.T) store_out<F16>(a, token, (kv_head * HP + hp) * a.G + gh, c4, acc, m, l);
     }
 }
 

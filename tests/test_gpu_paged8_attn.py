@@ -110,3 +110,28 @@ def test_chunks(xs, case, dtype):
     c.check(out, lse, causal, window, c.D ** -0.5)
     rows = sum(c.q_lens)
     assert out[rows:].isnan().all() and lse[rows:].isnan().all()
+
+
+PAIRS = [   # q_lens, kv_lens, H, Hkv, D, page, block, causal, window: enough sequences for tiles of two KV heads, and odd heads
+    ([1] * 80, [1 + (37 * i) % 700 for i in range(80)], 16, 4, 128, 16, 16, True, 0),
+    ([1] * 160, [1 + (61 * i) % 500 for i in range(160)], 2, 2, 64, 64, 32, True, 0),
+    ([(i * 5) % 3 for i in range(90)], [3 + (53 * i) % 400 for i in range(90)], 12, 4, 64, 16, 16, True, 100),
+    ([1] * 53, [2000 - 31 * i for i in range(53)], 48, 6, 128, 32, 16, False, 0),
+    ([2] * 40, [2 + (97 * i) % 3000 for i in range(40)], 32, 8, 128, 128, 64, True, 33),
+    ([1] * 110, [1 + (37 * i) % 300 for i in range(110)], 6, 3, 128, 16, 16, True, 0),
+]
+
+
+@pytest.mark.parametrize("form", [dict(), dict(heads_first=True), dict(one_buffer=True), dict(q_pad=3, table_pad=2)], ids=str)
+@pytest.mark.parametrize("case", PAIRS, ids=lambda c: "n%d_H%d_%d_D%d_p%d_b%d_w%d" % (len(c[0]), *c[2:7], c[8]))
+def test_many_sequences(xs, case, form):
+    *shape, causal, window = case
+    dtype = torch.bfloat16 if len(form) != 1 else torch.float16
+    c = p8.Paged8Case(*shape, dtype=dtype, seed=sum(case[0]), extra_rows=1, window=window, freed=window > 0, **form)
+    ws = xs.PagedWorkspace(c.n, c.H, c.Hkv, c.D)
+    out, lse = _run(xs, c, causal, window, ws=ws)
+    c.check(out, lse, causal, window, c.D ** -0.5)
+    rows = sum(c.q_lens)
+    assert out[rows:].isnan().all() and lse[rows:].isnan().all()
+    out2, lse2 = _run(xs, c, causal, window, ws=ws)      # the same plan and the same bits
+    assert torch.equal(out2[:rows], out[:rows]) and torch.equal(lse2[:rows], lse[:rows])
