@@ -73,9 +73,10 @@ struct Append8Args {
     int T, H, Hkv, D, rot;
     int page_shift, block_shift;
     // set by the launch function
-    int window;               // rows whose runs a block writes
-    int kv_per, kv_groups;    // heads of K and V (2 Hkv in all) per block
-    int q_per;                // heads of q per block
+    int window;               // rows of a window of K and V, one or more of q's
+    int kv_per, kv_groups;    // heads of K, or of V, of a block, and blocks for all
+    int q_per, q_groups;      // the same of q
+    FastDiv fd_groups;        // blocks of a window: of K, of V, of q's parts
     float magnitude;
     unsigned long long turns[64];
 };

@@ -5,12 +5,15 @@
 //     e = the least exponent >= -64 with a <= 448 2^e,   E = o > 0 ? max(E, e) : e,
 //     kept numbers /= 2^(E - E_before),   new numbers = round(x 2^-E).
 //
-// Append.  A thread block owns a window of rows: the runs (adjacent rows whose slots follow one
-// another in one block) that begin there, which end at most block - 1 rows past it.  It takes two passes over
-// them, the maximum and the numbers, with the largest magnitudes of its runs and heads in
-// shared memory between; the second pass reads k and v from L2 and turns them again, which
-// costs less than holding up to 255 rows in registers would in occupancy.  Other blocks of the
-// launch turn q.  Threads hold two 16-byte chunks of a row as in rope.cu.
+// Append.  A thread block owns a window of rows and some heads of q, k or v.  D / 16 threads hold a row as in rope.cu, and
+// its sines and cosines serve all heads of the block.  Each thread's parts of its row come into
+// shared memory by asynchronous copies of its own (256 bytes to a thread at most): bytes in flight cost no
+// registers, so that several blocks share an SM, and a thread waits for nobody's copies but its own.  A window of k
+// or v is at least as many rows as tokens share a scale, with fewer heads where the threads do not hold them all at once.
+// Of k and v a block writes the runs (adjacent rows whose slots follow one another in one block of the cache) that begin in its
+// window: their largest magnitudes, their scales, the numbers.  Rows of a run past the window (none in a
+// prompt whose windows are blocks) are loaded beside the window's where there is room, else in their place, and
+// those again after them.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -23,217 +26,265 @@
 namespace xs {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
-constexpr int MAX_WINDOW = 128;   // rows of a window; with the rows past it at most THREADS
-constexpr int MAX_KV_PER = 4;
-constexpr int UNROLL = 4;
+constexpr int MAX_BLOCK = 128;   // tokens of a scale
 
-template <bool F16, bool INTERLEAVED>
-__global__ void __launch_bounds__(THREADS) append8_kernel(const __grid_constant__ Append8Args g) {
-    __shared__ long long s_slot[THREADS];
-    __shared__ short s_lead[THREADS];                          // first row of a row's run; -1: not this block's
-    __shared__ int s_last[WARPS];
-    __shared__ uint32_t s_largest[MAX_WINDOW * MAX_KV_PER];    // per run (at its first row) and head
-    __shared__ float s_inverse[MAX_WINDOW * MAX_KV_PER];       // 2^-E
-    __shared__ int s_again[MAX_WINDOW * MAX_KV_PER];           // runs and heads whose kept numbers move
-    __shared__ int s_n_again;
+template <int D, int THREADS>
+struct AppendCfg {
+    static constexpr int UNITS = D / 16;                      // threads of a row
+    static constexpr int ROWS = THREADS / UNITS;              // rows that the threads hold at once
+    static constexpr int HEADS = 8;                           // of so many rows, at most
+    static constexpr int BYTES = THREADS * HEADS * 32;
+    static constexpr int ALL = 2 * (ROWS > MAX_BLOCK ? ROWS : MAX_BLOCK);   // rows of the runs of a window
+    static constexpr int SLOT_OFF = BYTES;                    // [ALL] slots
+    static constexpr int LARGEST_OFF = SLOT_OFF + ALL * 8;    // [heads][window] largest magnitude of a run, at its first row
+    static constexpr int INVERSE_OFF = LARGEST_OFF + ROWS * HEADS * 4;  // [heads][window] 2^-E
+    static constexpr int AGAIN_OFF = INVERSE_OFF + ROWS * HEADS * 4;    // runs and heads whose kept numbers move, by how much
+    static constexpr int LEAD_OFF = AGAIN_OFF + ROWS * HEADS * 4;       // [ALL] first row of a row's run; -1: not this block's
+    static constexpr int MISC_OFF = LEAD_OFF + ALL * 2;
+    static constexpr int SMEM = MISC_OFF + 48;
+    static_assert(ALL <= 256, "eight warps' rows");
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int D, bool F16, bool INTERLEAVED, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
+    append8_kernel(const __grid_constant__ Append8Args g) {
+    using C = AppendCfg<D, THREADS>;
+    constexpr int UNITS = C::UNITS, ROWS = C::ROWS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    long long* const s_slot = reinterpret_cast<long long*>(smem + C::SLOT_OFF);
+    unsigned* const s_largest = reinterpret_cast<unsigned*>(smem + C::LARGEST_OFF);
+    float* const s_inverse = reinterpret_cast<float*>(smem + C::INVERSE_OFF);
+    int* const s_again = reinterpret_cast<int*>(smem + C::AGAIN_OFF);
+    short* const s_lead = reinterpret_cast<short*>(smem + C::LEAD_OFF);
+    int* const s_rows = reinterpret_cast<int*>(smem + C::MISC_OFF);   // rows of the block's runs
+    int* const s_n_again = s_rows + 1;
+    int* const s_last = s_rows + 2;                                   // [8] last beginning of 32 rows
     using E = uint16_t;
+    const int tid = threadIdx.x, lane = tid & 31, u = tid % UNITS, row = tid / UNITS;
     pdl_launch();
     pdl_wait();
-    const int tid = threadIdx.x, units = g.D >> 4;
-    const int tl = tid / units, u = tid - tl * units, rows_at_once = THREADS / units;
-    const long long base = static_cast<long long>(blockIdx.x) * g.window;
+    int window, group;   // a window's blocks side by side: what one row of a fused projection holds is read together
+    fdivmod(static_cast<int>(blockIdx.x), g.fd_groups, window, group);
+    // the block's heads of k, of v or of q (those of one part of the window), and its rows
+    const int kind = group < g.kv_groups ? 0 : group < 2 * g.kv_groups ? 1 : 2;
+    const int q_at = group - 2 * g.kv_groups, q_part = kind == 2 ? q_at / g.q_groups : 0;
+    const int per = kind == 2 ? g.q_per : g.kv_per;
+    const int h0 = (kind == 0 ? group : kind == 1 ? group - g.kv_groups : q_at - q_part * g.q_groups) * per;
+    const int heads = min(kind == 2 ? g.H : g.Hkv, h0 + per) - h0;
+    const int width = kind == 2 ? ROWS : g.window;
+    const long long base = static_cast<long long>(window) * g.window + q_part * ROWS;
+    if (base >= g.T) return;
+    const E* const from = static_cast<const E*>(kind == 0 ? g.k : kind == 1 ? g.v : g.q) + static_cast<long long>(h0) * D;
+    const long long stride = kind == 0 ? g.k_stride : kind == 1 ? g.v_stride : g.q_stride;
+
     int oa, ob;
     bool rot_a, rot_b;
-    rope_chunks<INTERLEAVED>(u, g.D, g.rot, oa, ob, rot_a, rot_b);
-    float c[8], s[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = s[j] = 0.0f;
-
-    if (static_cast<int>(blockIdx.y) >= g.kv_groups) {   // q
-        const int h0 = (blockIdx.y - g.kv_groups) * g.q_per, h1 = min(g.H, h0 + g.q_per);
-        for (int r = tl; r < g.window; r += rows_at_once) {
-            const long long t = base + r;
-            if (t >= g.T) break;
-            if (rot_a || rot_b)
-                rope_angles<INTERLEAVED>(g.positions[t], g.turns, oa, ob, g.magnitude, g.magnitude, c, s);
-            const E* src = static_cast<const E*>(g.q) + t * g.q_stride;
-            E* dst = static_cast<E*>(g.q_out) + t * g.qo_stride;
-            for (int h = h0; h < h1; h += UNROLL) {
-                Chunk2 x[UNROLL];
-#pragma unroll
-                for (int i = 0; i < UNROLL; ++i)
-                    if (h + i < h1) {
-                        x[i].a = *reinterpret_cast<const uint4*>(src + static_cast<long long>(h + i) * g.D + oa);
-                        x[i].b = *reinterpret_cast<const uint4*>(src + static_cast<long long>(h + i) * g.D + ob);
-                    }
-#pragma unroll
-                for (int i = 0; i < UNROLL; ++i)
-                    if (h + i < h1) {
-                        turn<F16, INTERLEAVED>(x[i], c, s, rot_a, rot_b);
-                        *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + i) * g.D + oa) = x[i].a;
-                        *reinterpret_cast<uint4*>(dst + static_cast<long long>(h + i) * g.D + ob) = x[i].b;
-                    }
+    rope_chunks<INTERLEAVED>(u, D, g.rot, oa, ob, rot_a, rot_b);
+    if (kind == 1) rot_a = rot_b = false;
+    // the thread's parts of rows first + row, + ROWS .., up to first + n, to its places at, at + 1 ..
+    const uint32_t mine = smem_addr(smem) + tid * 16;
+    auto load = [&](int first, int n, int at) {
+        for (int i = row; i < n; i += ROWS, ++at) {
+            const E* p = from + (base + first + i) * stride;
+            for (int h = 0; h < heads; ++h, p += D) {
+                copy16(mine + (at * heads + h) * (2 * 16 * THREADS), p + oa);
+                copy16(mine + (at * heads + h) * (2 * 16 * THREADS) + 16 * THREADS, p + ob);
             }
+        }
+    };
+    auto element = [&](int at, int h) -> Chunk2 {
+        const uint8_t* p = smem + tid * 16 + (at * heads + h) * (2 * 16 * THREADS);
+        Chunk2 x;
+        x.a = *reinterpret_cast<const uint4*>(p);
+        x.b = *reinterpret_cast<const uint4*>(p + 16 * THREADS);
+        return x;
+    };
+    const int here = static_cast<int>(min(static_cast<long long>(width), g.T - base));
+    load(0, here, 0);
+    float c[8] = {}, s[8] = {};
+    int turned = -1;
+    auto turn_to = [&](int r) {   // the sines and cosines of row r of the window
+        const long long t = base + r;
+        if (turned != r && (rot_a || rot_b) && t < g.T)
+            rope_angles<INTERLEAVED>(g.positions[t], g.turns, oa, ob, g.magnitude, g.magnitude, c, s);
+        turned = r;
+    };
+    turn_to(row);
+    if (kind == 2) {
+        copies_done();
+        if (row >= here) return;
+        E* const out = static_cast<E*>(g.q_out) + (base + row) * g.qo_stride + static_cast<long long>(h0) * D;
+#pragma unroll 2
+        for (int h = 0; h < heads; ++h) {
+            Chunk2 x = element(0, h);
+            turn<F16, INTERLEAVED>(x, c, s, rot_a, rot_b);
+            *reinterpret_cast<uint4*>(out + h * D + oa) = x.a;
+            *reinterpret_cast<uint4*>(out + h * D + ob) = x.b;
         }
         return;
     }
 
-    // ---- runs
-    const int block = 1 << g.block_shift, rows = g.window + block - 1;
-    const int h0 = blockIdx.y * g.kv_per, heads = min(2 * g.Hkv, h0 + g.kv_per) - h0;   // K 0 .. Hkv - 1, then V
-    {
-        const long long t = base + tid;
-        const bool here = tid < rows && t < g.T;
-        const long long slot = here ? g.slots[t] : -1, before = here && t > 0 ? g.slots[t - 1] : -2;
+    if (tid == 0) *s_rows = *s_n_again = 0;
+    for (int i = tid; i < width * heads; i += THREADS) s_largest[i] = 0;
+
+    // ---- runs: a row that does not continue the one before begins one
+    const int block = 1 << g.block_shift;
+    constexpr int TURNS = C::ALL / THREADS;
+    int lead[TURNS];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int r = tid + i * THREADS, w = r >> 5;
+        const long long t = base + r;
+        const bool there = r < width + block - 1 && t < g.T;
+        const long long slot = there ? g.slots[t] : -1, before = there && t > 0 ? g.slots[t - 1] : -2;
         const bool stored = slot >= 0 && slot < g.n_slots;
         const bool begins = !stored || before + 1 != slot || (slot & (block - 1)) == 0;
-        const unsigned flags = __ballot_sync(0xffffffffu, begins);
-        const unsigned mine = flags & (0xffffffffu >> (31 - (tid & 31)));
-        if ((tid & 31) == 0) {
-            s_last[tid >> 5] = flags ? (tid & ~31) + 31 - __clz(flags) : -1;
-            if (tid == 0) s_n_again = 0;
-        }
-        for (int i = tid; i < g.window * heads; i += THREADS) s_largest[i] = 0;
-        __syncthreads();
-        int lead = mine ? (tid & ~31) + 31 - __clz(mine) : -1;
-        for (int w = (tid >> 5) - 1; w >= 0 && lead < 0; --w) lead = s_last[w];
-        s_slot[tid] = slot;
-        s_lead[tid] = static_cast<short>(stored && lead < g.window ? lead : -1);
+        const unsigned flags = __ballot_sync(0xffffffffu, begins), up_to = flags & (0xffffffffu >> (31 - lane));
+        if (lane == 0) s_last[w] = flags ? w * 32 + 31 - __clz(flags) : -1;
+        s_slot[r] = slot;
+        lead[i] = !stored ? -2 : up_to ? w * 32 + 31 - __clz(up_to) : -1;
     }
     __syncthreads();
-    auto scale_at = [&](int row, int hh) -> uint8_t* {
-        const long long slot = s_slot[row];
-        const int h = h0 + hh, off = static_cast<int>(slot & ((1 << g.page_shift) - 1));
-        const Codes8& x = h < g.Hkv ? g.kc : g.vc;
-        return x.scale + (slot >> g.page_shift) * x.ss[0] + (off >> g.block_shift) * x.ss[1] +
-               (h < g.Hkv ? h : h - g.Hkv) * x.ss[2];
-    };
-    auto source = [&](long long t, int hh) -> const E* {
-        const int h = h0 + hh;
-        if (h < g.Hkv) return static_cast<const E*>(g.k) + t * g.k_stride + static_cast<long long>(h) * g.D;
-        return static_cast<const E*>(g.v) + t * g.v_stride + static_cast<long long>(h - g.Hkv) * g.D;
-    };
-    // scales of the blocks that keep tokens
-    constexpr int PAIRS = MAX_WINDOW * MAX_KV_PER / THREADS;
-    int kept_scale[PAIRS];
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        const int pair = tid + i * THREADS, row = pair / heads;
-        kept_scale[i] = -1;
-        if (pair < g.window * heads && s_lead[row] == row && (s_slot[row] & (block - 1)) != 0)
-            kept_scale[i] = *scale_at(row, pair - row * heads);
+    for (int i = 0; i < TURNS; ++i) {
+        const int r = tid + i * THREADS;
+        for (int w = (r >> 5) - 1; w >= 0 && lead[i] == -1; --w) lead[i] = s_last[w];
+        if (lead[i] >= width) lead[i] = -1;
+        s_lead[r] = static_cast<short>(lead[i] < 0 ? -1 : lead[i]);
+        const unsigned ours = __ballot_sync(0xffffffffu, lead[i] >= 0);
+        if (lane == 0 && ours) atomicMax(s_rows, r + 32 - __clz(ours));
     }
+    __syncthreads();
+    const int rows = *s_rows, past = rows - width;   // past: rows past the window
+    if (rows == 0) {
+        copies_done();
+        return;
+    }
+    // as many turns of the threads each; `place` of the rows past the window
+    const int turns = (width + ROWS - 1) / ROWS;
+    const bool both = past > 0 && (turns + (past + ROWS - 1) / ROWS) * heads <= C::HEADS;
+    const int place = both ? turns : 0;
+    copies_done();
+    if (both) load(width, past, place);
 
     // ---- largest magnitudes
-    const bool turns = h0 < g.Hkv && (rot_a || rot_b);
-    for (int r = tl; r - tl < rows; r += rows_at_once) {   // (every lane takes part in the shuffles)
-        const int lead = r < rows ? s_lead[r] : -1;
-        if (!__any_sync(0xffffffffu, lead >= 0)) continue;
-        const long long t = base + r;
-        if (turns && lead >= 0) rope_angles<INTERLEAVED>(g.positions[t], g.turns, oa, ob, g.magnitude, g.magnitude, c, s);
-        Chunk2 x[MAX_KV_PER];
+    auto largest = [&](int first, int n, int at) {
+        for (int i = row; i - row < n; i += ROWS, ++at) {   // (whole warps: shuffles)
+            const int r0 = i < n ? s_lead[first + i] : -1;
+            if (!__any_sync(0xffffffffu, r0 >= 0)) continue;
+            turn_to(first + i);
+#pragma unroll 2
+            for (int h = 0; h < heads; ++h) {
+                float a[8], b[8], m = 0.0f;
+                turn_wide<F16, INTERLEAVED>(element(at, h), c, s, rot_a, rot_b, a, b);
 #pragma unroll
-        for (int i = 0; i < MAX_KV_PER; ++i) {
-            x[i].a = x[i].b = make_uint4(0, 0, 0, 0);
-            if (i < heads && lead >= 0) {
-                const E* p = source(t, i);
-                x[i].a = *reinterpret_cast<const uint4*>(p + oa);
-                x[i].b = *reinterpret_cast<const uint4*>(p + ob);
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(a[j]), fabsf(b[j])));
+#pragma unroll
+                for (int d = UNITS / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                if (u == 0 && r0 >= 0) atomicMax(&s_largest[h * width + r0], __float_as_uint(m));
             }
         }
-#pragma unroll
-        for (int i = 0; i < MAX_KV_PER; ++i) {
-            if (i >= heads) break;
-            float a[8], b[8], m = 0.0f;
-            const bool k = h0 + i < g.Hkv;
-            turn_wide<F16, INTERLEAVED>(x[i], c, s, k && rot_a, k && rot_b, a, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, fmaxf(fabsf(a[j]), fabsf(b[j])));
-            for (int d = units >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            if (u == 0 && lead >= 0) atomicMax(&s_largest[lead * heads + i], __float_as_uint(m));
-        }
+    };
+    largest(0, min(rows, width), 0);
+    if (past > 0) {
+        if (!both) load(width, past, place);
+        copies_done();
+        largest(width, past, place);
     }
     __syncthreads();
 
-    // ---- scales
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        const int pair = tid + i * THREADS, row = pair / heads;
-        if (pair >= g.window * heads || s_lead[row] != row) continue;
-        const int before = kept_scale[i];
-        int now = scale_byte(s_largest[pair]);
-        if (before >= 0 && now > before) s_again[atomicAdd(&s_n_again, 1)] = (pair << 8) | (now - before);
+    // ---- scales of the runs
+    const Codes8& to = kind == 0 ? g.kc : g.vc;
+    for (int i = tid; i < width * heads; i += THREADS) {
+        const int h = i / width, r0 = i - h * width;
+        if (s_lead[r0] != r0) continue;
+        const long long slot = s_slot[r0];
+        const int off = static_cast<int>(slot & ((1 << g.page_shift) - 1));
+        uint8_t* const at = to.scale + (slot >> g.page_shift) * to.ss[0] + (off >> g.block_shift) * to.ss[1] + (h0 + h) * to.ss[2];
+        const int before = (off & (block - 1)) != 0 ? *at : -1;
+        int now = scale_byte(s_largest[i]);
+        if (before >= 0 && now > before) s_again[atomicAdd(s_n_again, 1)] = i << 8 | (now - before);
         now = max(now, before);
-        if (now != before) *scale_at(row, pair - row * heads) = static_cast<uint8_t>(now);
-        s_inverse[pair] = scale_value(254 - now);
+        if (now != before) *at = static_cast<uint8_t>(now);
+        s_inverse[i] = scale_value(254 - now);
     }
     __syncthreads();
 
-    // ---- numbers that a block keeps under a larger scale
-    for (int i = tid >> 5; i < s_n_again; i += WARPS) {
-        const int pair = s_again[i] >> 8, by = s_again[i] & 255, row = pair / heads, h = h0 + pair - row * heads;
-        const float f = by < 127 ? scale_value(127 - by) : 0.0f;
-        const long long slot = s_slot[row];
-        const int keep = static_cast<int>(slot & (block - 1));
-        const Codes8& x = h < g.Hkv ? g.kc : g.vc;
-        uint8_t* p = x.code + (slot >> g.page_shift) * x.cs[0] + (h < g.Hkv ? h : h - g.Hkv) * x.cs[2];
-        const long long token0 = (slot & ((1 << g.page_shift) - 1)) - keep;
-        for (int j = tid & 31; j < keep * units; j += 32) {
-            const int token = j / units;
-            uint4* at = reinterpret_cast<uint4*>(p + (token0 + token) * x.cs[1] + (j - token * units) * 16);
-            uint4 w = *at;
-            uint32_t* const ws = reinterpret_cast<uint32_t*>(&w);
+    // ---- numbers that a block keeps under a larger scale: 16 bytes to a thread at a time, MOVE of them on their way
+    constexpr int MOVE = 4;
+    const int each = block * UNITS, all = *s_n_again * each;
+    for (int i0 = tid; i0 < all; i0 += MOVE * THREADS) {
+        uint4 w[MOVE];
+        uint4* at[MOVE];
+        float f[MOVE];
+#pragma unroll
+        for (int m = 0; m < MOVE; ++m) {
+            const int i = i0 + m * THREADS, item = i >> (g.block_shift + (D == 128 ? 3 : 2)), k = i & (each - 1);
+            at[m] = nullptr;
+            if (i >= all) continue;
+            const int pair = s_again[item] >> 8, by = s_again[item] & 255, h = pair / width;
+            const long long slot = s_slot[pair - h * width];
+            const int keep = static_cast<int>(slot & (block - 1)), token = k / UNITS;
+            if (token >= keep) continue;
+            f[m] = by < 127 ? scale_value(127 - by) : 0.0f;
+            at[m] = reinterpret_cast<uint4*>(to.code + (slot >> g.page_shift) * to.cs[0] + (h0 + h) * to.cs[2] +
+                                             ((slot & ((1 << g.page_shift) - 1)) - keep + token) * to.cs[1] + k % UNITS * 16);
+            w[m] = *at[m];
+        }
+#pragma unroll
+        for (int m = 0; m < MOVE; ++m) {
+            if (at[m] == nullptr) continue;
+            uint32_t* const ws = reinterpret_cast<uint32_t*>(&w[m]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 lo = f16x2_values(codes_to_f16x2(ws[e])), hi = f16x2_values(codes_to_f16x2_high(ws[e]));
-                ws[e] = to_codes(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+                ws[e] = to_codes(lo.x * f[m], lo.y * f[m], hi.x * f[m], hi.y * f[m]);
             }
-            *at = w;
+            *at[m] = w[m];
         }
     }
 
-    // ---- new numbers
-    for (int r = tl; r < rows; r += rows_at_once) {
-        const int lead = s_lead[r];
-        if (lead < 0) continue;
-        const long long t = base + r, slot = s_slot[r];
-        const long long page = slot >> g.page_shift, off = slot & ((1 << g.page_shift) - 1);
-        if (turns) rope_angles<INTERLEAVED>(g.positions[t], g.turns, oa, ob, g.magnitude, g.magnitude, c, s);
-        Chunk2 x[MAX_KV_PER];
-#pragma unroll
-        for (int i = 0; i < MAX_KV_PER; ++i)
-            if (i < heads) {
-                const E* p = source(t, i);
-                x[i].a = *reinterpret_cast<const uint4*>(p + oa);
-                x[i].b = *reinterpret_cast<const uint4*>(p + ob);
+    // ---- new numbers, of the rows loaded last first
+    auto store = [&](int first, int n, int at) {
+        for (int i = row; i < n; i += ROWS, ++at) {
+            const int r = first + i, r0 = s_lead[r];
+            if (r0 < 0) continue;
+            turn_to(r);
+            const long long slot = s_slot[r];
+            uint8_t* const p = to.code + (slot >> g.page_shift) * to.cs[0] + (slot & ((1 << g.page_shift) - 1)) * to.cs[1];
+#pragma unroll 2
+            for (int h = 0; h < heads; ++h) {
+                float a[8], b[8];
+                turn_wide<F16, INTERLEAVED>(element(at, h), c, s, rot_a, rot_b, a, b);
+                const float f = s_inverse[h * width + r0];
+                uint8_t* const q = p + (h0 + h) * to.cs[2];
+                *reinterpret_cast<uint2*>(q + oa) = make_uint2(to_codes(a[0] * f, a[1] * f, a[2] * f, a[3] * f),
+                                                               to_codes(a[4] * f, a[5] * f, a[6] * f, a[7] * f));
+                *reinterpret_cast<uint2*>(q + ob) = make_uint2(to_codes(b[0] * f, b[1] * f, b[2] * f, b[3] * f),
+                                                               to_codes(b[4] * f, b[5] * f, b[6] * f, b[7] * f));
             }
-#pragma unroll
-        for (int i = 0; i < MAX_KV_PER; ++i) {
-            if (i >= heads) break;
-            float a[8], b[8];
-            const int h = h0 + i;
-            const bool k = h < g.Hkv;
-            turn_wide<F16, INTERLEAVED>(x[i], c, s, k && rot_a, k && rot_b, a, b);
-            const float f = s_inverse[lead * heads + i];
-            const Codes8& z = k ? g.kc : g.vc;
-            uint8_t* p = z.code + page * z.cs[0] + off * z.cs[1] + (k ? h : h - g.Hkv) * z.cs[2];
-            uint2 wa, wb;
-            wa.x = to_codes(a[0] * f, a[1] * f, a[2] * f, a[3] * f);
-            wa.y = to_codes(a[4] * f, a[5] * f, a[6] * f, a[7] * f);
-            wb.x = to_codes(b[0] * f, b[1] * f, b[2] * f, b[3] * f);
-            wb.y = to_codes(b[4] * f, b[5] * f, b[6] * f, b[7] * f);
-            *reinterpret_cast<uint2*>(p + oa) = wa;
-            *reinterpret_cast<uint2*>(p + ob) = wb;
+        }
+    };
+    if (past > 0) {
+        store(width, past, place);
+        if (!both) {
+            load(0, width, 0);
+            copies_done();
         }
     }
+    store(0, min(rows, width), 0);
 }
 
 // ------------------------------------------------------------------- read back
 // A thread block gathers READ_ROWS rows: their sequences, pages and offsets once, into shared
 // memory, then 16-channel pieces of K and V.
-constexpr int READ_ROWS = 32;
+constexpr int THREADS = 256;
+constexpr int READ_ROWS = 16;
 constexpr int READ_UNROLL = 4;
 
 // The last sequence i of [0, n) with cu[i] <= r (empty ones behind it excluded), by a warp: 32 places at once.
@@ -332,25 +383,50 @@ __global__ void __launch_bounds__(THREADS) read8_kernel(const __grid_constant__ 
 
 }  // namespace
 
-cudaError_t launch_append8(const Append8Args& args, int dtype, int layout, int num_sms, cudaStream_t stream) {
+namespace {
+
+template <int D, int THREADS>
+cudaError_t launch_append(const Append8Args& args, int dtype, int layout, int num_sms, cudaStream_t stream) {
+    using C = AppendCfg<D, THREADS>;
     Append8Args a = args;
-    const int block = 1 << a.block_shift, at_once = THREADS * 16 / a.D;
-    a.window = block > at_once ? block : at_once;
+    const int parts = (1 << a.block_shift) > C::ROWS ? (1 << a.block_shift) / C::ROWS : 1;
+    a.window = C::ROWS * parts;
     const long long windows = (static_cast<long long>(a.T) + a.window - 1) / a.window;
+    // heads of a block: as many as fit, fewer where that leaves SMs without a block
     auto groups = [](int heads, int per) { return (heads + per - 1) / per; };
-    a.kv_per = MAX_KV_PER;
-    while (a.kv_per > 1 && windows * groups(2 * a.Hkv, a.kv_per) < num_sms) a.kv_per /= 2;
-    a.q_per = 8;
-    while (a.q_per > 1 && windows * groups(a.H, a.q_per) < 2 * num_sms) a.q_per /= 2;
-    a.kv_groups = groups(2 * a.Hkv, a.kv_per);
-    const dim3 grid(static_cast<unsigned>(windows), static_cast<unsigned>(a.kv_groups + groups(a.H, a.q_per)));
-    auto launch = [&](auto kernel) { return launch_overlapped(kernel, grid, THREADS, 0, stream, a); };
+    auto per_block = [&](long long count, int heads, int most) {
+        while (most > 1 && count * groups(heads, most) < num_sms) most /= 2;
+        return most;
+    };
+    a.kv_per = per_block(2 * windows, a.Hkv, C::HEADS / parts);
+    a.q_per = per_block(windows * parts, a.H, C::HEADS);
+    a.kv_groups = groups(a.Hkv, a.kv_per);
+    a.q_groups = groups(a.H, a.q_per);
+    const int blocks = 2 * a.kv_groups + parts * a.q_groups;   // of a window
+    if (windows * blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    a.fd_groups = make_fastdiv(blocks);
+    auto launch = [&](auto kernel) {
+        if (C::SMEM > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_overlapped(kernel, dim3(static_cast<unsigned>(windows * blocks)), THREADS, C::SMEM, stream, a);
+    };
     switch (dtype * 2 + layout) {
-        case 0: return launch(append8_kernel<false, false>);
-        case 1: return launch(append8_kernel<false, true>);
-        case 2: return launch(append8_kernel<true, false>);
-        default: return launch(append8_kernel<true, true>);
+        case 0: return launch(append8_kernel<D, false, false, THREADS>);
+        case 1: return launch(append8_kernel<D, false, true, THREADS>);
+        case 2: return launch(append8_kernel<D, true, false, THREADS>);
+        default: return launch(append8_kernel<D, true, true, THREADS>);
     }
+}
+
+}  // namespace
+
+cudaError_t launch_append8(const Append8Args& a, int dtype, int layout, int num_sms, cudaStream_t stream) {
+    const bool few = ((a.D / 16) << a.block_shift) <= 128;   // 128 threads hold a block's rows
+    if (a.D == 64)
+        return few ? launch_append<64, 128>(a, dtype, layout, num_sms, stream) : launch_append<64, 256>(a, dtype, layout, num_sms, stream);
+    return few ? launch_append<128, 128>(a, dtype, layout, num_sms, stream) : launch_append<128, 256>(a, dtype, layout, num_sms, stream);
 }
 
 cudaError_t launch_read8(const Read8Args& args, int dtype, int num_sms, cudaStream_t stream) {
