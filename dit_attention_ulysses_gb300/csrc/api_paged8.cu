@@ -82,6 +82,11 @@ int encode_cache8(CUtensorMap* m, const void* base, const CacheStrides& s, const
     return XS_OK;
 }
 
+// Up to 16 packed rows (new tokens x heads to a KV head) go to the kernel of few tokens, more to that of chunks.  With
+// 12 and 16 rows (32 heads of 128 over 8 KV heads, us, few tokens / chunks): 1 x 300 keys 10.4 / 11.8 and 10.7 / 11.9,
+// 1 x 4096 15.0 / 22.5 and 16.4 / 22.7, 64 x 2048 77 / 103 and 80 / 103, but 16 x 1000 20.4 / 17.2 and 20.8 / 17.3,
+// 1 x 32768 33.5 / 31.1 and 36.2 / 31.1.  With 20 rows and the first kernel widened to 32: 1 x 4096 19.8 / 22.5,
+// otherwise slower (16 ragged sequences of up to 5000 keys, fp16, 24 rows: 44.6 / 28.8).
 Tiling make_tiling8(int n, int Hkv, int G, int D, int max_q, int sms) {
     Tiling x{};
     x.t.cache8 = 1;
@@ -94,22 +99,25 @@ Tiling make_tiling8(int n, int Hkv, int G, int D, int max_q, int sms) {
         x.t.start_cost = 512;
         x.t.snap = 4;
         x.t.whole = 12;
-        x.t.least = 1024;
+        x.t.least = 512;        // (1 x 4096 keys, 32 rows: 19.2 us; 1024: 23.2; 384: 19.0)
         x.t.join = 38;
         x.t.join_rows = 32;
         x.t.waves = xs::MAX_PAGED_WAVES;
-        x.t.one_each = 1280;
+        x.t.one_each = 2304;    // (24 rows: 64 x 2048 keys 88.6 us, 48 x 4096 116; 1280: 107, 122; ragged batches the same)
         x.t.l2_bytes = 64 << 20;
         return x;
     }
     x.rows = static_cast<int64_t>(G) * max_q <= ROWS_FEW / 2 ? ROWS_FEW / 2 : ROWS_FEW;
     x.t.tokens = x.rows / G;
+    // Pairs of KV heads (half the tiles, starts and joins, twice the work between waits) where a CTA still gets two of
+    // them: 64 x 8192 keys 182 us, 199 with single heads; 200 ragged sequences 56 and 62.  With the heads of a page
+    // apart in memory they cost a little: 64 x 8192 178 and 171.
     if (x.rows == ROWS_FEW / 2 && Hkv % 2 == 0 && static_cast<int64_t>(n) * Hkv >= 2 * sms) x.t.heads = 2;
     x.t.block = 32;
     x.t.grid = 2 * sms;
-    x.t.start_cost = 512;
+    x.t.start_cost = 512;   // (64 ragged sequences: 60 us, 200 ragged: 56; 256: 71 and 61; 1024: 58 and 67)
     x.t.snap = 4;
-    x.t.whole = 20;
+    x.t.whole = 40;         // (16 x 1000 keys: 15.3 us; 20 and 30: 17.2; otherwise the same)
     x.t.least = 512;
     x.t.join = 4;
     x.t.join_rows = 512 / D;   // four channels to a thread

@@ -649,7 +649,8 @@ typedef struct xs_paged_cache8 {
  *     o > 0:   it becomes the larger of 2^e and the block's scale; where that is 2^e, the first
  *              o tokens' numbers are divided by the ratio (rounded to nearest even: exact but
  *              for numbers that end below 2^-6);
- *     numbers = x / scale, rounded to nearest even.
+ *     numbers = x / scale, rounded to nearest even; an infinity becomes the largest number of a
+ *     scale of 2^120, NaN stays NaN and does not count for a.
  * A slot outside [0, n_pages * page_size) (padding) stores no K and V.
  *   rope == NULL: nothing is rotated, q, q_out and positions must be NULL, H 0 (a cache filled
  *   from keys that are rotated already).
@@ -695,8 +696,10 @@ int xs_paged_read8(const xs_paged_read8_args* args, void* stream);
  * xs_attn_paged8_plan, xs_attn_paged8_fwd -- xs_attn_paged_plan and xs_attn_paged_fwd over an
  * 8-bit cache: the same rows, keys, layouts, lse and workspace, on plans of their own (a plan of
  * the other cache computes nothing, see there).  Elements are those that the cache stands for
- * (scale bytes 63 .. 254); q keeps 18 or more bits relative to its row's largest channel, the
- * probabilities enter the second product in fp16, sums, maxima and accumulators are fp32.
+ * (scale bytes 63 .. 254, V's of one sequence within a factor of 2^90 of one another); q keeps 18
+ * or more bits relative to its row's largest channel, the probabilities enter the second product in
+ * fp16, off by up to 2^-25 of the largest product of a probability and its V's scale where they are
+ * small; sums, maxima and accumulators are fp32.
  * Places that no row sees may hold anything, also in the scales.
  */
 int xs_attn_paged8_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,

@@ -10,7 +10,7 @@ if ROOT not in sys.path:
 
 
 # Calls with made-up addresses: the accepted ones would reach a GPU if the process saw one.
-NO_GPU_FILES = ("test_abi_host.py", "test_paged_host.py")
+NO_GPU_FILES = ("test_abi_host.py", "test_paged_host.py", "test_paged8_host.py")
 
 
 def _sees_a_gpu():
