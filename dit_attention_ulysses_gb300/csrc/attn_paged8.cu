@@ -19,6 +19,15 @@
 // softmax two conversions back and forth per pair, 12 of its issue cycles, where V's
 // conversion takes 2 and is another warp's.)
 //
+// What bounds it: 2 sequences' 2048 new tokens after 14336 each (causal, 32 heads of 128 over 8) take 831 us,
+// 1230 TFLOP/s, 66 % of the measured bf16 rate; 4608 over 18432 keys, not causal, 24 heads, 825 us.  (attn_paged.cu, over
+// twice the bytes: 748 and 743.)  The tensor pipes are busy for 54 % of it, the issue slots for 56 %, and a quarter of
+// the warps' waiting is for the pipelines' own latencies with two softmax warps to a scheduler.  No single part is the
+// bound: without V's conversion 785 us, with one product for S in place of eight 765, without exponentials 775, without
+// the maximum 783, without all of these 575.  The text of the roles is as large as the instruction cache that they share:
+// the same loops in another order are 2 to 10 % slower (masking or rescaling out of line, producers merged, a
+// smaller unrolling here or there), and a softmax in two passes over TMEM, half the code, 25 %.
+//
 // Organisation (one persistent CTA per SM, 16 warps):
 //   warps 0-7   softmax + epilogue, two threads per row
 //   warp  8     producer of V and of the scales of K and V
@@ -151,7 +160,8 @@ __device__ __forceinline__ void regs_down() {
 
 // The waits of device_wait.cuh, in line as far as their first test.  All roles' loops together have to fit the
 // instruction cache of an SM: with every wait in line (700 bytes each) and the producers' loops apart, 41 % of the
-// warps' time went to instruction fetches (causal chunk: 1474 us).
+// warps' time went to instruction fetches (the causal chunk above: 1474 us).  Not the softmax's: a call in its loop
+// moves its registers to memory and back (1488 us).
 __device__ __noinline__ bool thread_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
                                             int blk) {
     return thread_wait(bar, parity, abort_flag, timeout_ns, unit, blk);

@@ -14,6 +14,10 @@
 // window: their largest magnitudes, their scales, the numbers.  Rows of a run past the window (none in a
 // prompt whose windows are blocks) are loaded beside the window's where there is room, else in their place, and
 // those again after them.
+//
+// 8192 tokens (32 heads of 128 over 8, blocks of 16): 38.5 us, 4.8 TB/s of 186 MB (27.4 us at the copy rate).  A block
+// runs once through long code, and fetching it is what holds it up most beside its own two trips to memory (86 % of the
+// fetches hit the SM's cache; loops over heads unrolled by two: 41.0 us).  Rows held in registers: 53 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
             const int r0 = i < n ? s_lead[first + i] : -1;
             if (!__any_sync(0xffffffffu, r0 >= 0)) continue;
             turn_to(first + i);
-#pragma unroll 2
+#pragma unroll 1
             for (int h = 0; h < heads; ++h) {
                 float a[8], b[8], m = 0.0f;
                 turn_wide<F16, INTERLEAVED>(element(at, h), c, s, rot_a, rot_b, a, b);
@@ -216,7 +220,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
     __syncthreads();
 
     // ---- numbers that a block keeps under a larger scale: 16 bytes to a thread at a time, MOVE of them on their way
-    constexpr int MOVE = 4;
+    // (4: the loop is larger, 8192 tokens in blocks of 32 take 41.7 us instead of 38.3)
+    constexpr int MOVE = 2;
     const int each = block * UNITS, all = *s_n_again * each;
     for (int i0 = tid; i0 < all; i0 += MOVE * THREADS) {
         uint4 w[MOVE];
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
             turn_to(r);
             const long long slot = s_slot[r];
             uint8_t* const p = to.code + (slot >> g.page_shift) * to.cs[0] + (slot & ((1 << g.page_shift) - 1)) * to.cs[1];
-#pragma unroll 2
+#pragma unroll 1
             for (int h = 0; h < heads; ++h) {
                 float a[8], b[8];
                 turn_wide<F16, INTERLEAVED>(element(at, h), c, s, rot_a, rot_b, a, b);
@@ -281,10 +286,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
 }
 
 // ------------------------------------------------------------------- read back
-// A thread block gathers READ_ROWS rows: their sequences, pages and offsets once, into shared
-// memory, then 16-channel pieces of K and V.
+// A thread block gathers ROWS rows, 8 or 16: their sequences, pages and offsets once, into
+// shared memory, then 16-channel pieces of K and V.  Bound by HBM: 32768 rows of 8 x 128 take 37.3 us,
+// 5.4 TB/s of 201 MB (29.6 us at the copy rate), with 8 rows to a block 40.0, with 32 39.3.  1000 sequences of 8
+// rows take 13.2 us with 8 rows to a block (each waits for a search, a page, then the rows), 17.1 with 16 and 22.1
+// with 32; 24 ragged ones of up to 500 rows of 6 x 64 4.8, 5.7 and 5.7.
 constexpr int THREADS = 256;
-constexpr int READ_ROWS = 16;
 constexpr int READ_UNROLL = 4;
 
 // The last sequence i of [0, n) with cu[i] <= r (empty ones behind it excluded), by a warp: 32 places at once.
@@ -308,15 +315,15 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t f16x2, float scale) {
     return narrow<F16>(fminf(fmaxf(f.x * scale, -most), most), fminf(fmaxf(f.y * scale, -most), most));
 }
 
-template <bool F16>
+template <bool F16, int ROWS>
 __global__ void __launch_bounds__(THREADS) read8_kernel(const __grid_constant__ Read8Args g) {
-    __shared__ int s_page[READ_ROWS];   // -1: zeros
-    __shared__ int s_off[READ_ROWS];
+    __shared__ int s_page[ROWS];   // -1: zeros
+    __shared__ int s_off[ROWS];
     pdl_launch();
     pdl_wait();
-    const int base = blockIdx.x * READ_ROWS, tid = threadIdx.x;
+    const int base = blockIdx.x * ROWS, tid = threadIdx.x;
     const int total = g.cu[g.n];
-    const int rows = min(min(g.T, total) - base, READ_ROWS);
+    const int rows = min(min(g.T, total) - base, ROWS);
     if (rows <= 0) return;
     if (tid < 32) {
         int i = find_sequence(g.cu, g.n, base);
@@ -392,7 +399,9 @@ cudaError_t launch_append(const Append8Args& args, int dtype, int layout, int nu
     const int parts = (1 << a.block_shift) > C::ROWS ? (1 << a.block_shift) / C::ROWS : 1;
     a.window = C::ROWS * parts;
     const long long windows = (static_cast<long long>(a.T) + a.window - 1) / a.window;
-    // heads of a block: as many as fit, fewer where that leaves SMs without a block
+    // heads of a block: as many as fit, fewer where that leaves SMs without a block.  512 tokens (32 heads of 128 over 8):
+    // 6.3 us, 7.1 if halved from half as many blocks on, 7.0 from twice as many, 8.2 if never; 7200 tokens at most, ragged
+    // (12 of 64 over 6, blocks of 64): 7.9, 9.7, 10.3, 12.9; 2048 tokens: 14.7, 14.7, 13.8, 14.7
     auto groups = [](int heads, int per) { return (heads + per - 1) / per; };
     auto per_block = [&](long long count, int heads, int most) {
         while (most > 1 && count * groups(heads, most) < num_sms) most /= 2;
@@ -423,7 +432,10 @@ cudaError_t launch_append(const Append8Args& args, int dtype, int layout, int nu
 }  // namespace
 
 cudaError_t launch_append8(const Append8Args& a, int dtype, int layout, int num_sms, cudaStream_t stream) {
-    const bool few = ((a.D / 16) << a.block_shift) <= 128;   // 128 threads hold a block's rows
+    // 128 threads where they hold a block's rows (blocks of 16, D = 128: 256 tokens 5.7 us, 512 6.3, 8192 40.8; with 256
+    // threads 6.3, 7.6, 42.5), else 256 (blocks of 128: 8192 tokens 49.4 us, with 128 threads 58.6; the ragged batch above
+    // 7.9 and 11.7)
+    const bool few = ((a.D / 16) << a.block_shift) <= 128;
     if (a.D == 64)
         return few ? launch_append<64, 128>(a, dtype, layout, num_sms, stream) : launch_append<64, 256>(a, dtype, layout, num_sms, stream);
     return few ? launch_append<128, 128>(a, dtype, layout, num_sms, stream) : launch_append<128, 256>(a, dtype, layout, num_sms, stream);
@@ -432,9 +444,12 @@ cudaError_t launch_append8(const Append8Args& a, int dtype, int layout, int num_
 cudaError_t launch_read8(const Read8Args& args, int dtype, int num_sms, cudaStream_t stream) {
     Read8Args a = args;
     a.fd_row = make_fastdiv(a.Hkv * a.D / 16);
-    const dim3 grid(static_cast<unsigned>((a.T + READ_ROWS - 1) / READ_ROWS));
-    return dtype == 0 ? launch_overlapped(read8_kernel<false>, grid, THREADS, 0, stream, a)
-                      : launch_overlapped(read8_kernel<true>, grid, THREADS, 0, stream, a);
+    auto launch = [&](auto kernel, int rows) {
+        return launch_overlapped(kernel, dim3(static_cast<unsigned>((a.T - 1) / rows + 1)), THREADS, 0, stream, a);
+    };
+    // 8 rows to a block where all blocks are then on the SMs at once, eight to one
+    if ((a.T - 1) / 8 < 8 * num_sms) return dtype == 0 ? launch(read8_kernel<false, 8>, 8) : launch(read8_kernel<true, 8>, 8);
+    return dtype == 0 ? launch(read8_kernel<false, 16>, 16) : launch(read8_kernel<true, 16>, 16);
 }
 
 }  // namespace xs

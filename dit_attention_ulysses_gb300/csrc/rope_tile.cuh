@@ -27,14 +27,14 @@ __device__ __forceinline__ void rope_chunks(int u, int D, int rot, int& oa, int&
     }
 }
 
-// Cosines (times cos_by) and sines (times sin_by) of N of the chunks' pairs, from the first-th on, at a position.
-template <bool INTERLEAVED, int N>
+// Cosines (times cos_by) and sines (times sin_by) of the chunks' pairs at a position.
+template <bool INTERLEAVED>
 __device__ __forceinline__ void rope_angles(int position, const unsigned long long (&turns)[64], int oa, int ob, float cos_by,
-                                            float sin_by, float (&c)[N], float (&s)[N], int first = 0) {
+                                            float sin_by, float (&c)[8], float (&s)[8]) {
     const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(position));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int j = first + i, pair = INTERLEAVED ? ((j < 4 ? oa : ob) >> 1) + (j & 3) : oa + j;
+    for (int i = 0; i < 8; ++i) {
+        const int pair = INTERLEAVED ? ((i < 4 ? oa : ob) >> 1) + (i & 3) : oa + i;
         const unsigned long long turn64 = pos * turns[pair < 64 ? pair : 63];
         const float half_turns = static_cast<float>(static_cast<int>(turn64 >> 32)) * 4.656612873077393e-10f;
         sincospif(half_turns, &s[i], &c[i]);
