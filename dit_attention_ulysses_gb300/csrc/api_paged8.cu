@@ -99,11 +99,11 @@ Tiling make_tiling8(int n, int Hkv, int G, int D, int max_q, int sms) {
         x.t.start_cost = 512;
         x.t.snap = 4;
         x.t.whole = 12;
-        x.t.least = 512;        // (1 x 4096 keys, 32 rows: 19.2 us; 1024: 23.2; 384: 19.0)
+        x.t.least = 512;        // (1 x 4096 keys, 32 rows: 18.6 us; with 1024 a fifth more, with 384 the same)
         x.t.join = 38;
         x.t.join_rows = 32;
         x.t.waves = xs::MAX_PAGED_WAVES;
-        x.t.one_each = 2304;    // (24 rows: 64 x 2048 keys 88.6 us, 48 x 4096 116; 1280: 107, 122; ragged batches the same)
+        x.t.one_each = 2304;    // (24 rows: 64 x 2048 keys 79 us; with 1280 a fifth more, and 48 x 4096 5 %; ragged batches the same)
         x.t.l2_bytes = 64 << 20;
         return x;
     }

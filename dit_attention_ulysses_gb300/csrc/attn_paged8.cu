@@ -19,20 +19,22 @@
 // softmax two conversions back and forth per pair, 12 of its issue cycles, where V's
 // conversion takes 2 and is another warp's.)
 //
-// What bounds it: 2 sequences' 2048 new tokens after 14336 each (causal, 32 heads of 128 over 8) take 831 us,
-// 1230 TFLOP/s, 66 % of the measured bf16 rate; 4608 over 18432 keys, not causal, 24 heads, 825 us.  (attn_paged.cu, over
-// twice the bytes: 748 and 743.)  The tensor pipes are busy for 54 % of it, the issue slots for 56 %, and a quarter of
-// the warps' waiting is for the pipelines' own latencies with two softmax warps to a scheduler.  No single part is the
-// bound: without V's conversion 785 us, with one product for S in place of eight 765, without exponentials 775, without
-// the maximum 783, without all of these 575.  The text of the roles is as large as the instruction cache that they share:
-// the same loops in another order are 2 to 10 % slower (masking or rescaling out of line, producers merged, a
-// smaller unrolling here or there), and a softmax in two passes over TMEM, half the code, 25 %.
+// What bounds it: 2 sequences' 2048 new tokens after 14336 each (causal, 32 heads of 128 over 8) take 788 us,
+// 1310 TFLOP/s, 70 % of the measured bf16 rate; 4608 over 18432 keys, not causal, 24 heads, 795 us.  (attn_paged.cu, over
+// twice the bytes: 748 and 743.)  Heads of 64, whose products are half as large: 2 x 2048 after 8192 452 us (353).
+// What the warps wait for is instructions: the loops of five roles do not fit the SM's instruction cache together (92 to
+// 94 % of the fetches hit it, 98 % in attn_paged.cu), and the cache behind it, which the SMs of a GPC share, is near its
+// rate.  So no single part is the bound: at 830 us in all, it was 785 without V's conversion, 765 with one instruction for
+// S in place of eight, 775 without exponentials, 783 without the maximum, 575 without all of these; and as the
+// cache's misses depend on where the code comes to lie, smaller code is not faster by itself: masks or rescaling out of
+// the loop, the two producers as one, smaller unrollings, or the next piece's Q ahead of V's last block measured
+// 1 % faster to 20 % slower, a softmax of half the code in two passes over TMEM 25 %.
 //
 // Organisation (one persistent CTA per SM, 16 warps):
 //   warps 0-7   softmax + epilogue, two threads per row
 //   warp  8     producer of V and of the scales of K and V
-//   warp  9     issuer of the S MMAs (one lane) and TMEM owner
-//   warp 10     issuer of the O += P V MMAs (one lane)
+//   warp  9     issuer of the S MMAs and TMEM owner
+//   warp 10     issuer of the O += P V MMAs
 //   warp 11     producer of K: walks the CTA's part of the plan
 //   warps 12-15 converters: Q of the next tile, V block by block
 #include <cuda.h>
@@ -62,7 +64,7 @@ constexpr int WARP_CONVERT = 12;
 constexpr int CONVERTERS = 4;
 // Registers of a thread by warpgroup: 2 * 168 + 80 + 96 = 4 * 128, what the block is launched with
 constexpr int REGS_SOFTMAX = 168, REGS_ISSUE = 80, REGS_CONVERT = 96;
-constexpr int SCALE_SLOTS = 8;      // blocks whose scales are kept (see producer_v_role)
+constexpr int SCALE_SLOTS = 8;      // blocks whose scales are kept (see load_blocks)
 
 // Scales of 16 keys.
 struct alignas(16) Scales {
@@ -162,16 +164,6 @@ __device__ __forceinline__ void regs_down() {
 // instruction cache of an SM: with every wait in line (700 bytes each) and the producers' loops apart, 41 % of the
 // warps' time went to instruction fetches (the causal chunk above: 1474 us).  Not the softmax's: a call in its loop
 // moves its registers to memory and back (1488 us).
-__device__ __noinline__ bool thread_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
-                                            int blk) {
-    return thread_wait(bar, parity, abort_flag, timeout_ns, unit, blk);
-}
-
-__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
-                                          int blk = -1) {
-    return mbar_test_wait(bar, parity) || thread_wait_on(bar, parity, abort_flag, timeout_ns, unit, blk);
-}
-
 __device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
                                           int blk) {
     return warp_wait(bar, parity, abort_flag, timeout_ns, unit, blk);
@@ -233,15 +225,11 @@ __device__ __forceinline__ bool load_blocks(const CUtensorMap* map, const PagedA
                 continue;
             }
         }
-        bool ok = true;
-        if (lane == 0) {
-            if (round > 0) ok = lane_wait(free0 + stage * 8u, (round - 1) & 1, abort_flag, a.timeout_ns, u, j);
-            if (ok) {
-                mbar_arrive_expect_tx(full0 + stage * 8u, BLOCK_N * D);
-                loaded[stage] = round + 1;
-            }
+        const bool ok = round == 0 || all_wait(free0 + stage * 8u, (round - 1) & 1, abort_flag, a.timeout_ns, u, j);
+        if (ok && lane == 0) {
+            mbar_arrive_expect_tx(full0 + stage * 8u, BLOCK_N * D);
+            loaded[stage] = round + 1;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         const int page = __shfl_sync(0xffffffffu, cur, (j & 3) * 8 + (lane & 7));
         __syncwarp();
         if (!ok) return false;
@@ -282,9 +270,7 @@ __device__ void producer_k_role(const CUtensorMap* tk, const PagedAttn8Args& a, 
 #pragma unroll 1
     for (int u = 0;; ++u) {
         if (u >= 2) {
-            if (lane == 0) ok = lane_wait(bar(C::B_Q_FREE + (u & 1)), ((u >> 1) - 1) & 1, abort_flag, a.timeout_ns, u);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            __syncwarp();
+            ok = all_wait(bar(C::B_Q_FREE + (u & 1)), ((u >> 1) - 1) & 1, abort_flag, a.timeout_ns, u);
         }
         if (!ok) break;
         Piece d{};
@@ -469,7 +455,11 @@ __device__ void convert_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t ba
 }
 
 // --------------------------------------------------------------------- MMA
-// Issuer of S(j) = Q K_j^T into S buffer (block index) % 3: the parts of Q one after the other.  One thread.
+// Both issuers run as whole warps, with one elected thread at the instructions: what these take (descriptors, TMEM
+// addresses) is then uniform, in registers where they can use it.  With one lane in the role, a dozen instructions
+// more per MMA moved it there (causal chunk 834 us, video 825, 24 mixed requests with heads of 64 25.6; now 788, 795, 22.2).
+//
+// Issuer of S(j) = Q K_j^T into S buffer (block index) % 3: the parts of Q one after the other.
 template <int D, bool F16>
 __device__ void mma_s_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0, uint32_t tmem_base, volatile int* abort_flag) {
     using C = Cfg8<D, F16>;
@@ -481,31 +471,34 @@ __device__ void mma_s_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0
     uint32_t sb = 0, sph = 0;   // S buffer of block g (g % 3) and its phase parity ((g / 3) & 1)
     bool ok = true;
     for (int u = 0; ok; ++u) {
-        ok = lane_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
+        ok = all_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
-        const int n = piece_of(smem, C::PIECE_OFF, u).nb;
+        const int n = __shfl_sync(0xffffffffu, piece_of(smem, C::PIECE_OFF, u).nb, 0);
         if (n == 0) break;
-        ok = lane_wait(bar(C::B_Q_FULL), u & 1, abort_flag, a.timeout_ns, u);
+        ok = all_wait(bar(C::B_Q_FULL), u & 1, abort_flag, a.timeout_ns, u);
         // the previous piece's last PV first: its epilogue waits for it
-        if (ok && u > 0) ok = lane_wait(bar(C::B_O_FINAL), (u - 1) & 1, abort_flag, a.timeout_ns, u);
+        if (ok && u > 0) ok = all_wait(bar(C::B_O_FINAL), (u - 1) & 1, abort_flag, a.timeout_ns, u);
         for (int j = 0; j < n && ok; ++j, ++g) {
-            if (g >= S_BUFS) ok = lane_wait(bar(C::B_P_FREE + sb), sph ^ 1u, abort_flag, a.timeout_ns, u, j);
+            if (g >= S_BUFS) ok = all_wait(bar(C::B_P_FREE + sb), sph ^ 1u, abort_flag, a.timeout_ns, u, j);
             const uint32_t stage = g % C::K_STAGES;
-            if (ok) ok = lane_wait(bar(C::B_K_FULL + stage), (g / C::K_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok) ok = all_wait(bar(C::B_K_FULL + stage), (g / C::K_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kdesc = desc_add(kdesc0, stage * (C::CODE_BYTES >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int p = 0; p < C::PARTS; ++p)
+                for (int p = 0; p < C::PARTS; ++p)
 #pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk) {
-                    const int at = p * D + kk * 32;   // byte of a Q row
-                    mma_ss_e4m3(tmem_base + S_COL + sb * 128u, desc_add(qdesc, ((at >> 7) * PANEL_BYTES + (at & 127)) >> 4),
-                                desc_add(kdesc, kk * 2), IDESC, p > 0 || kk > 0);
-                }
-            mma_commit(bar(C::B_S_FULL + sb));
-            mma_commit(bar(C::B_K_FREE + stage));
-            if (j == n - 1) mma_commit(bar(C::B_Q_FREE + (u & 1)));
+                    for (int kk = 0; kk < D / 32; ++kk) {
+                        const int at = p * D + kk * 32;   // byte of a Q row
+                        mma_ss_e4m3(tmem_base + S_COL + sb * 128u, desc_add(qdesc, ((at >> 7) * PANEL_BYTES + (at & 127)) >> 4),
+                                    desc_add(kdesc, kk * 2), IDESC, p > 0 || kk > 0);
+                    }
+                mma_commit(bar(C::B_S_FULL + sb));
+                mma_commit(bar(C::B_K_FREE + stage));
+                if (j == n - 1) mma_commit(bar(C::B_Q_FREE + (u & 1)));
+            }
+            __syncwarp();
             if (++sb == S_BUFS) {
                 sb = 0;
                 sph ^= 1u;
@@ -513,11 +506,12 @@ __device__ void mma_s_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0
         }
     }
     // B_DRAIN completes when both issuers' MMAs have all completed (TMEM is freed after it)
-    mma_commit(bar(C::B_DRAIN));
+    if (elect_one()) mma_commit(bar(C::B_DRAIN));
+    __syncwarp();
     drain_wait(bar(C::B_DRAIN), 0, a.timeout_ns > 20000000ull ? a.timeout_ns : 20000000ull);
 }
 
-// Issuer of PV(j): O += P(j) V_j.  One thread.
+// Issuer of PV(j): O += P(j) V_j.
 template <int D, bool F16>
 __device__ void mma_pv_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar0, uint32_t tmem_base, volatile int* abort_flag) {
     using C = Cfg8<D, F16>;
@@ -528,33 +522,37 @@ __device__ void mma_pv_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t bar
     uint32_t pb = 0, pph = 0;   // buffer of block g (g % 3) and its phase parity ((g / 3) & 1)
     bool ok = true;
     for (int u = 0; ok; ++u) {
-        ok = lane_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
+        ok = all_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
-        const int n = piece_of(smem, C::PIECE_OFF, u).nb;
+        const int n = __shfl_sync(0xffffffffu, piece_of(smem, C::PIECE_OFF, u).nb, 0);
         if (n == 0) break;
         for (int j = 0; j < n && ok; ++j, ++g) {
-            ok = lane_wait(bar(C::B_P_FULL + pb), pph, abort_flag, a.timeout_ns, u, j);
+            ok = all_wait(bar(C::B_P_FULL + pb), pph, abort_flag, a.timeout_ns, u, j);
             // the epilogue has read the previous piece's O (PV(0) overwrites it)
-            if (ok && j == 0 && u > 0) ok = lane_wait(bar(C::B_O_FREE), (u - 1) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok && j == 0 && u > 0) ok = all_wait(bar(C::B_O_FREE), (u - 1) & 1, abort_flag, a.timeout_ns, u, j);
             const uint32_t stage = g % C::V_STAGES;
-            if (ok) ok = lane_wait(bar(C::B_V_FULL + stage), (g / C::V_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
+            if (ok) ok = all_wait(bar(C::B_V_FULL + stage), (g / C::V_STAGES) & 1, abort_flag, a.timeout_ns, u, j);
             if (!ok) break;
             tc_fence_after();
             const uint64_t vdesc = desc_add(vdesc0, stage * (C::V_BYTES >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < BLOCK_N / 16; ++kk)
-                mma_ts(tmem_base + O_COL, tmem_base + S_COL + pb * 128u + kk * 8, desc_add(vdesc, kk * (2 * C::GROUP >> 4)), IDESC,
-                       j > 0 || kk > 0);
-            mma_commit(bar(C::B_P_FREE + pb));
-            mma_commit(bar(C::B_V_FREE + stage));
-            if (j == n - 1) mma_commit(bar(C::B_O_FINAL));
+                for (int kk = 0; kk < BLOCK_N / 16; ++kk)
+                    mma_ts(tmem_base + O_COL, tmem_base + S_COL + pb * 128u + kk * 8, desc_add(vdesc, kk * (2 * C::GROUP >> 4)),
+                           IDESC, j > 0 || kk > 0);
+                mma_commit(bar(C::B_P_FREE + pb));
+                mma_commit(bar(C::B_V_FREE + stage));
+                if (j == n - 1) mma_commit(bar(C::B_O_FINAL));
+            }
+            __syncwarp();
             if (++pb == S_BUFS) {
                 pb = 0;
                 pph ^= 1u;
             }
         }
     }
-    mma_commit(bar(C::B_DRAIN));
+    if (elect_one()) mma_commit(bar(C::B_DRAIN));
+    __syncwarp();
     drain_wait(bar(C::B_DRAIN), 0, a.timeout_ns > 20000000ull ? a.timeout_ns : 20000000ull);
 }
 
@@ -593,7 +591,7 @@ __device__ void softmax_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t ba
                              volatile int* abort_flag) {
     using C = Cfg8<D, F16>;
     constexpr int DH = D / 2;  // O columns owned by each of a row's two threads
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(lane_id());
     const int quarter = warp & 3;             // TMEM lane quarter this warp may access
     const int half = lane >> 4;               // key columns [64*half, 64*half + 64), O columns [DH*half, +DH)
@@ -612,7 +610,7 @@ __device__ void softmax_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t ba
         ok = warp_wait(bar(C::B_PIECE + u % PIECES), (u / PIECES) & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
         const Piece& d = piece_of(smem, C::PIECE_OFF, u);
-        const int n = d.nb;
+        const int n = __shfl_sync(0xffffffffu, d.nb, 0);
         if (n == 0) break;
         const bool idle = warp_row >= d.n_rows;   // no query row in this warp
         // columns [lo, hi) of the piece that this row sees; rows past the tile take the last one's
@@ -731,7 +729,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t bar0 = smem_addr(smem + C::BAR_OFF);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);   // [1]: who joins a cut tile
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // (uniform, as the compiler sees)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NUM_BARS; ++i) {
@@ -756,7 +754,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_holder;
+    const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     pdl_wait();
 
     if (warp < NUM_SOFTMAX_WARPS) {
@@ -768,9 +766,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             producer_k_role<D, F16>(&tk, args, smem, bar0, abort_flag);
         else if (warp == WARP_V)
             producer_v_role<D, F16>(&tv, args, smem, bar0, abort_flag);
-        else if (warp == WARP_MMA_PV && lane_id() == 0)
+        else if (warp == WARP_MMA_PV)
             mma_pv_role<D, F16>(args, smem, bar0, tmem_base, abort_flag);
-        else if (warp == WARP_MMA_S && lane_id() == 0)
+        else if (warp == WARP_MMA_S)
             mma_s_role<D, F16>(args, smem, bar0, tmem_base, abort_flag);
     } else {
         regs_down<REGS_CONVERT>();
