@@ -82,16 +82,16 @@ int encode_cache8(CUtensorMap* m, const void* base, const CacheStrides& s, const
     return XS_OK;
 }
 
-// Up to 16 packed rows (new tokens x heads to a KV head) go to the kernel of few tokens, more to that of chunks.  With
-// 12 and 16 rows (32 heads of 128 over 8 KV heads, us, few tokens / chunks): 1 x 300 keys 10.4 / 11.8 and 10.7 / 11.9,
-// 1 x 4096 15.0 / 22.5 and 16.4 / 22.7, 64 x 2048 77 / 103 and 80 / 103, but 16 x 1000 20.4 / 17.2 and 20.8 / 17.3,
-// 1 x 32768 33.5 / 31.1 and 36.2 / 31.1.  With 20 rows and the first kernel widened to 32: 1 x 4096 19.8 / 22.5,
-// otherwise slower (16 ragged sequences of up to 5000 keys, fp16, 24 rows: 44.6 / 28.8).
+// Up to 8 packed rows (new tokens x heads to a KV head), with D = 64 up to 16, go to the kernel of few tokens, more to
+// that of chunks.  12 and 16 rows of 128 (us, few tokens / chunks): 16 x 1000 keys 20.4 / 15.1 and 20.9 / 15.1, 1 x 32768
+// 35.2 / 28.1 and 38.1 / 28.0, 64 x 8192 219 / 195 and 222 / 196 (fp16, whose Q has a part more, 266 / 238), 200 ragged
+// sequences 78.5 / 75.3 and 79.2 / 77.7, but 1 x 4096 15.7 / 16.7 and 17.1 / 16.7, 64 ragged ones in fp16 66 / 72.  12 rows
+// of 64: 1 x 4096 12.4 / 15.1, 64 x 4096 91.8 / 98.5, 200 ragged 56.9 / 67.6, but 16 x 1000 15.6 / 13.4.
 Tiling make_tiling8(int n, int Hkv, int G, int D, int max_q, int sms) {
     Tiling x{};
     x.t.cache8 = 1;
     x.t.heads = 1;
-    if (static_cast<int64_t>(G) * max_q > ROWS_FEW) {
+    if (static_cast<int64_t>(G) * max_q > (D == 128 ? ROWS_FEW / 2 : ROWS_FEW)) {
         x.rows = ROWS_TILE;
         x.t.tokens = ROWS_TILE / G;
         x.t.block = 128;

@@ -1,4 +1,4 @@
-// Attention of a few new tokens over an 8-bit paged cache: up to 16 packed query rows per KV head.
+// Attention of a few new tokens over an 8-bit paged cache: up to 8 packed query rows per KV head, 16 with heads of 64.
 //
 //   x_t = c 2^(E_q + E_k) <q, k_t> + E_v,  M = a running maximum of x_t,  l = sum_t 2^-E_v 2^(x_t - M),
 //   O = sum_t 2^(x_t - M) v_t / l,  lse = (M + log2 l) ln 2,  c = scale log2(e),
@@ -652,7 +652,8 @@ cudaError_t launch_any(const CUtensorMap& tk, const CUtensorMap& tv, const Paged
 cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
                                     cudaStream_t stream) {
     if (a.tile.heads == 2) return launch_any<2, 2>(tk, tv, a, dtype, stream);
-    return a.tile.tokens * a.G <= 8 ? launch_any<1, 1>(tk, tv, a, dtype, stream) : launch_any<2, 1>(tk, tv, a, dtype, stream);
+    if (a.tile.tokens * a.G <= 8) return launch_any<1, 1>(tk, tv, a, dtype, stream);
+    return dtype == 0 ? launch<64, false, 2, 1>(tk, tv, a, stream) : launch<64, true, 2, 1>(tk, tv, a, stream);
 }
 
 cudaError_t read_and_clear_paged8_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {

@@ -151,6 +151,35 @@ def test_serving_steps_in_a_graph(xs, max_q):
         s.step([a if a >= 0 else 0 for a in new], s.launch if sum(new) % 2 else graph.replay)
 
 
+def test_readme_example(xs):
+    """The README's steps over both caches run as printed, and the second's results are those of its elements."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "xs_paged_step" in b or "xs_attn_paged8_fwd" in b]
+    assert len(blocks) == 2
+    ns = dict(torch=torch, xs=xs)
+    for b in blocks:
+        exec(b, ns)
+    assert xs.xs_attn_get_device_error() == xs.XS_OK
+    n, H, Hkv, D = (ns[k] for k in ("n", "H", "Hkv", "D"))
+    q8, kd, vd = (ns[k].double().cpu().numpy() for k in ("q8", "k_back", "v_back"))
+    k, v = (ns[x].double().cpu().numpy()[:20 * n] for x in "kv")
+    k, _ = pg.rope_reference(k, ns["positions"].cpu().numpy()[:20 * n], pg.frequencies(D), False)
+    # half a step, and of the smallest numbers half a step of a scale that is at most 2^-7 of a magnitude below 8
+    assert (np.abs(vd - v) <= 2.0 ** -4 * np.abs(v) + 2.0 ** -16).all()
+    assert (np.abs(kd - k) <= 2.0 ** -4 * np.abs(k) + 2.0 ** -15).all()
+    u = pg.U[torch.bfloat16]
+    for i in (0, n - 1):
+        rows = slice(20 * i, 20 * i + 20)
+        for h in (0, H - 1):
+            g = h // (H // Hkv)
+            ref, mass, _ = pg.attention_reference(q8[rows, h], kd[rows, g], vd[rows, g], 20, True, 0, D ** -0.5)
+            before = (2.0 ** -11 + 1.5e-4) * mass + 2.0 ** -25 * 20 * 448 * 2.0 ** -6
+            assert (np.abs(ns["out8"][rows, h].double().cpu().numpy() - ref) <= before + u * (np.abs(ref) + before)).all()
+
+
 def test_two_graphs_share_a_workspace(xs):
     """Captured plans and attentions replayed in turn, both kernels of this cache and one of the 16-bit cache."""
     cases = [p8.Paged8Case([1] * 6, [5000, 10, 900, 4000, 77, 1], 8, 2, 128, 16, seed=1),
