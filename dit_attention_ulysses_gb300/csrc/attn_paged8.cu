@@ -21,14 +21,17 @@
 //
 // What bounds it: 2 sequences' 2048 new tokens after 14336 each (causal, 32 heads of 128 over 8) take 788 us,
 // 1310 TFLOP/s, 70 % of the measured bf16 rate; 4608 over 18432 keys, not causal, 24 heads, 795 us.  (attn_paged.cu, over
-// twice the bytes: 748 and 743.)  Heads of 64, whose products are half as large: 2 x 2048 after 8192 452 us (353).
-// What the warps wait for is instructions: the loops of five roles do not fit the SM's instruction cache together (92 to
-// 94 % of the fetches hit it, 98 % in attn_paged.cu), and the cache behind it, which the SMs of a GPC share, is near its
-// rate.  So no single part is the bound: at 830 us in all, it was 785 without V's conversion, 765 with one instruction for
-// S in place of eight, 775 without exponentials, 783 without the maximum, 575 without all of these; and as the
-// cache's misses depend on where the code comes to lie, smaller code is not faster by itself: masks or rescaling out of
-// the loop, the two producers as one, smaller unrollings, or the next piece's Q ahead of V's last block measured
-// 1 % faster to 20 % slower, a softmax of half the code in two passes over TMEM 25 %.
+// twice the bytes: 748 and 743.)  Heads of 64, whose products are half as large: 2 x 2048 after 8192 452 us (353).  As there
+// it is the softmax's chain, with two of its warps to a scheduler, and a converter beside them: the issue slots
+// are busy for 57 % of the time, the tensor pipes for 58 %, the warps wait for their own results.
+//
+// The loops of five roles have to share the SM's instruction cache.  While they did not (MMA issuers of one lane
+// each, whose operands every instruction moved to uniform registers; 90 to 94 % of the fetches hit, and the cache
+// behind it, which the SMs of a GPC share, ran at 84 to 91 % of its rate: 834 us) no part was the bound: 785 without V's
+// conversion, 765 with one instruction for S in place of eight, 775 without exponentials, 783 without the maximum.  Now 99 %
+// hit.  Measured and not kept: masks or rescaling out of the loop, the two producers as one, smaller unrollings, the
+// epilogue out of line (1 % faster to 20 % slower, by where the code came to lie), the next piece's Q before V's last
+// block (+1.5 %), S of the next piece before the last PV (+1 %), a softmax of half the code in two passes over TMEM (+25 %).
 //
 // Organisation (one persistent CTA per SM, 16 warps):
 //   warps 0-7   softmax + epilogue, two threads per row
@@ -160,10 +163,9 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The waits of device_wait.cuh, in line as far as their first test.  All roles' loops together have to fit the
-// instruction cache of an SM: with every wait in line (700 bytes each) and the producers' loops apart, 41 % of the
-// warps' time went to instruction fetches (the causal chunk above: 1474 us).  Not the softmax's: a call in its loop
-// moves its registers to memory and back (1488 us).
+// The waits of device_wait.cuh, in line as far as their first test.  With every wait in line (700 bytes each) and the
+// producers' loops apart, 41 % of the warps' time went to instruction fetches (the causal chunk above: 1474 us).  Not the
+// softmax's: a call in its loop moves its registers to memory and back (1488 us).
 __device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t timeout_ns, int unit,
                                           int blk) {
     return warp_wait(bar, parity, abort_flag, timeout_ns, unit, blk);
