@@ -611,3 +611,46 @@ def test_append_of_what_is_not_finite(xs, first, second):
             else:
                 assert got[row, at] == value * (e < 0)
         assert (got[0, 10:] == (e < 0)).all()
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_append_rotates_q_in_place(xs, T):
+    """q_out may be q, a slice of a fused projection: the same bits, k and v left alone."""
+    H, Hkv, D, page, block = 6, 2, 128, 64, 32
+    qkv = torch.randn((T, H + 2 * Hkv, D), device="cuda").bfloat16()
+    slots, rope = torch.randperm(40, device="cuda")[torch.arange(T, device="cuda") // page] * page + \
+        torch.arange(T, device="cuda") % page, xs.Rope(D)
+    results = []
+    for in_place in (False, True):
+        x = qkv.clone()
+        q, k, v = x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+        out = q if in_place else torch.empty((T, H, D), dtype=x.dtype, device="cuda")
+        cache = [torch.zeros((40, page, Hkv, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in "kv"] + \
+                [torch.zeros((40, page // block, Hkv), dtype=torch.uint8, device="cuda") for _ in "kv"]
+        xs.xs_rope_append_paged8(q, k, v, torch.arange(T, device="cuda").int(), slots, out, *cache, rope)
+        assert torch.equal(x[:, H:], qkv[:, H:])
+        results.append([out.clone(), *(c.view(torch.uint8) for c in cache)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    out16 = torch.empty((T, H, D), dtype=qkv.dtype, device="cuda")
+    xs.xs_rope_fwd(qkv[:, :H], torch.arange(T, device="cuda").int(), out16, rope)
+    assert torch.equal(out16, results[0][0])
+
+
+def test_two_streams_append_to_one_cache(xs):
+    """Requests' appends on streams of their own, twenty steps of them, equal those one after the other."""
+    Hkv, D, page, block, n = 4, 64, 32, 16, 3
+    streams = [torch.cuda.Stream() for _ in range(n)]
+    x = torch.randn((n, 20, 7, Hkv, D), device="cuda").bfloat16()
+    results = []
+    for side in (True, False):
+        cache = [torch.zeros((n * 5, page, Hkv, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in "kv"] + \
+                [torch.zeros((n * 5, page // block, Hkv), dtype=torch.uint8, device="cuda") for _ in "kv"]
+        slots = [[(i * 5) * page + 7 * s + torch.arange(7, device="cuda") for s in range(20)] for i in range(n)]
+        torch.cuda.synchronize()
+        for s in range(20):
+            for i in range(n):
+                xs.xs_rope_append_paged8(None, x[i, s], x[i, s], None, slots[i][s], None, *cache, None,
+                                         stream=streams[i] if side else None)
+        torch.cuda.synchronize()
+        results.append([c.view(torch.uint8) for c in cache])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
