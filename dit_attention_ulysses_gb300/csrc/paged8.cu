@@ -308,11 +308,18 @@ __device__ __forceinline__ int find_sequence(const int* cu, int n, int r) {
     return lo;
 }
 
+// x, or the nearer end of [-most, most]; NaN stays NaN (fminf and fmaxf would give an end).
+__device__ __forceinline__ float saturated(float x, float most) {
+    float y;
+    asm("{\n.reg .f32 t;\nmax.NaN.f32 t, %1, %2;\nmin.NaN.f32 %0, t, %3;\n}" : "=f"(y) : "f"(x), "f"(-most), "f"(most));
+    return y;
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t value_pair(uint32_t f16x2, float scale) {
     const float2 f = f16x2_values(f16x2);
     const float most = F16 ? 65504.0f : 3.3895313892515355e38f;
-    return narrow<F16>(fminf(fmaxf(f.x * scale, -most), most), fminf(fmaxf(f.y * scale, -most), most));
+    return narrow<F16>(saturated(f.x * scale, most), saturated(f.y * scale, most));
 }
 
 template <bool F16, int ROWS>
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(THREADS) read8_kernel(const __grid_constant__ 
             if (row[j] < 0) continue;
             const bool k = row[j] < rows;
             const int r = k ? row[j] : row[j] - rows;
-            const float f = scale_value(scale[j]);
+            const float f = any_scale_value(scale[j]);
             const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
             uint32_t o[8];
 #pragma unroll

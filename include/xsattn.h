@@ -610,7 +610,7 @@ int xs_attn_paged_fwd(const xs_attn_paged_args* args, void* stream);
  *
  * xs_paged_cache8 holds K and V as e4m3 numbers in pages as above, and for every block of
  * `block` tokens of a page and every head a scale, a power of two in e8m0 (byte s stands for
- * 2^(s - 127)); an element stands for its number times its block's scale.  A power of two,
+ * 2^(s - 127), 255 for NaN); an element stands for its number times its block's scale.  A power of two,
  * because e4m3 numbers are floating point: another factor would not make their relative
  * rounding smaller, while a block whose range grows with a later token is rescaled by moving
  * exponents, without a second rounding.  The library writes scales from 2^-64 on.
@@ -676,7 +676,7 @@ int xs_rope_append_paged8(const xs_rope_append8_args* args, void* stream);
  * is the token of sequence i at position first[i] + r - cu_rows[i]:
  *     k_out[r, h, :] = numbers * scale
  * rounded once to nearest even (bf16: exact), magnitudes past the type's largest finite
- * number become that.  Rows from cu_rows[n] on are left as they are; positions outside
+ * number become that, NaN (of a number or a scale) stays NaN.  Rows from cu_rows[n] on are left as they are; positions outside
  * [0, table_width * page_size) and page numbers outside [0, n_pages) give zeros.
  */
 typedef struct xs_paged_read8_args {

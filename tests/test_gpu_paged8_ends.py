@@ -1,0 +1,81 @@
+"""The 8-bit paged cache at the ends of what it holds.  References and roundings: _paged8.py."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+DTYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+
+
+@pytest.fixture(scope="module")
+def xs():
+    from conftest import build_library
+    build_library()
+    import dit_attention_ulysses_gb300 as xs
+    assert torch.cuda.is_available()
+    return xs
+
+
+def _same(got, want):
+    assert np.array_equal(np.isnan(got), np.isnan(want)), np.argwhere(np.isnan(got) != np.isnan(want))[:5]
+    bad = ~np.isnan(want) & (got != want)
+    assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
+
+
+# ------------------------------------------------------------------------------- read
+def _read_all_numbers(xs, scales, dtype):
+    """Every e4m3 number under each of the scale bytes, read back: got and wanted, [scale, number], of K and of V."""
+    n = len(scales)
+    code = torch.arange(256, dtype=torch.uint8).view(1, 2, 1, 128).repeat(n, 8, 1, 1)    # two tokens hold them all
+    scale = torch.tensor(scales, dtype=torch.uint8).view(n, 1, 1)
+    k, v = (c.cuda().view(torch.float8_e4m3fn) for c in (code, code.flip(-1)))
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n)
+    out = [torch.full((16 * n, 1, 128), 7.0, dtype=dtype, device="cuda") for _ in "kv"]
+    xs.xs_paged_read8(k, v, scale.cuda(), scale.cuda(), table, torch.tensor([0, 16 * n], dtype=torch.int32, device="cuda"), None, *out)
+    number = code[0, :2].view(torch.float8_e4m3fn).float().double().numpy()
+    with np.errstate(over="ignore"):
+        # four bits times a power of two: exact in 32 bits, so that what follows is the one rounding
+        by = [np.float64("nan") if s == 255 else 2.0 ** (s - 127) for s in scales]
+        most = torch.finfo(dtype).max
+        want = [torch.from_numpy(np.clip(number * b, -most, most)).float().to(dtype).double().numpy() for b in by]
+    got = [o.double().cpu().numpy().reshape(n, 8, 2, 1, 128) for o in out]
+    for o, flip in zip(got, (False, True)):
+        for s in range(n):
+            w = want[s][..., ::-1] if flip else want[s]
+            for t in range(8):
+                yield o[s, t], w
+
+
+@DTYPES
+def test_read_of_every_number_under_every_scale(xs, dtype):
+    """numbers * scale, rounded once, what is past the type's largest its largest, NaN as NaN."""
+    for got, want in _read_all_numbers(xs, list(range(1, 255)), dtype):
+        _same(got, want)
+
+
+@DTYPES
+def test_read_of_a_scale_that_is_nan(xs, dtype):
+    for got, want in _read_all_numbers(xs, [127, 255, 130], dtype):
+        _same(got, want)
+
+
+@DTYPES
+def test_what_is_not_finite_comes_back(xs, dtype):
+    """Appended, then read: NaN stays NaN beside its neighbours, an infinity becomes the type's largest number."""
+    x = torch.ones((48, 2, 64), dtype=dtype, device="cuda")
+    x[3, 0, 5], x[4, 1, 60] = float("nan"), float("nan")           # a block with NaN
+    x[20, 0, 7], x[21, 0, 8], x[22, 1, 9] = float("inf"), float("-inf"), float("nan")
+    cache = [torch.zeros((3, 16, 2, 64), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in "kv"] + \
+            [torch.zeros((3, 1, 2), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    xs.xs_rope_append_paged8(None, x, -x, None, torch.arange(48, device="cuda"), None, *cache, None)
+    table = torch.arange(3, dtype=torch.int32, device="cuda").view(1, 3)
+    k, v = (torch.empty_like(x) for _ in "kv")
+    xs.xs_paged_read8(*cache, table, torch.tensor([0, 48], dtype=torch.int32, device="cuda"), None, k, v)
+    want = np.ones((48, 2, 64))
+    want[3, 0, 5] = want[4, 1, 60] = want[22, 1, 9] = np.nan
+    want[16:32, 0] = 0                                             # beside an infinity 1 is nothing
+    most = torch.finfo(dtype).max
+    want[20, 0, 7], want[21, 0, 8] = most, -most
+    _same(k.double().cpu().numpy(), want)
+    _same(v.double().cpu().numpy(), -want)
