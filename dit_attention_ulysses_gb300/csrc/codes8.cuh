@@ -9,11 +9,13 @@ namespace xs {
 
 constexpr int LEAST_SCALE = 63;   // the smallest scale byte that is written: 2^-64
 
-// 2^(byte - 127), byte 1 .. 254 (0: 0)
+// 2^(byte - 127), byte 1 .. 254
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// The same, and NaN for byte 255.
-__device__ __forceinline__ float any_scale_value(uint32_t byte) { return byte == 255 ? __uint_as_float(0x7fffffffu) : scale_value(byte); }
+// The same of any byte: 0 is 2^-127, a subnormal, 255 NaN.
+__device__ __forceinline__ float any_scale_value(uint32_t byte) {
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
+}
 
 // Scale byte of values up to `largest` (the bits of a non-negative float): the least s >= 63 with
 // largest <= 448 * 2^(s - 127) = 1.75 * 2^(s - 119).  The sum carries into the exponent if the

@@ -675,7 +675,7 @@ int xs_rope_append_paged8(const xs_rope_append8_args* args, void* stream);
  * xs_paged_read8 -- elements of an 8-bit cache in 16 bits: row r of [cu_rows[i], cu_rows[i+1])
  * is the token of sequence i at position first[i] + r - cu_rows[i]:
  *     k_out[r, h, :] = numbers * scale
- * rounded once to nearest even (bf16: exact), magnitudes past the type's largest finite
+ * rounded once to nearest even (bf16: exact from 2^-126 on), magnitudes past the type's largest finite
  * number become that, NaN (of a number or a scale) stays NaN.  Rows from cu_rows[n] on are left as they are; positions outside
  * [0, table_width * page_size) and page numbers outside [0, n_pages) give zeros.
  */

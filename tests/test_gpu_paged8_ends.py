@@ -79,3 +79,10 @@ def test_what_is_not_finite_comes_back(xs, dtype):
     want[20, 0, 7], want[21, 0, 8] = most, -most
     _same(k.double().cpu().numpy(), want)
     _same(v.double().cpu().numpy(), -want)
+
+
+@DTYPES
+def test_read_of_the_least_scale(xs, dtype):
+    """Byte 0 stands for 2^-127 as every other for its power."""
+    for got, want in _read_all_numbers(xs, [0, 1, 2], dtype):
+        _same(got, want)
