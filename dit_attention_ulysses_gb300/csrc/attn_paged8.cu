@@ -244,7 +244,7 @@ __device__ __forceinline__ bool load_blocks(const CUtensorMap* map, const PagedA
                 // (of keys that no row sees: anything; a factor that stays positive keeps their scores at -infinity)
                 const int k = min(max(bytes & 255, 1), 254), v = min(max(bytes >> 8, LEAST_SCALE), 254);
                 scales[slot * 8 + (lane & 7)] =
-                    Scales{scale_value(k), static_cast<float>(v - 127), scale_value(254 - v), 0.0f};
+                    Scales{scale_value(k), static_cast<float>(v - 127), inverse_scale(v), 0.0f};
             }
             warp_arrive(bar(C::B_SCALES + slot));
         }

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     // (of a block that no row sees: anything)
                     const int v = min(max(static_cast<int>(w >> (16 * hp + 8) & 255), LEAST_SCALE), 254);
                     const float k = scale_value(w >> 16 * hp & 255), v_exp = static_cast<float>(v - 127);
-                    v_inv[b][hp] = scale_value(254 - v);
+                    v_inv[b][hp] = inverse_scale(v);
 #pragma unroll
                     for (int n = hp; n < (HP == 1 ? NT : hp + 1); ++n)
 #pragma unroll

@@ -17,6 +17,9 @@ __device__ __forceinline__ float any_scale_value(uint32_t byte) {
     return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fffffffu : byte << 23);
 }
 
+// 2^(127 - byte), byte 1 .. 254 (254: 2^-127, a subnormal)
+__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float(max((254u - byte) << 23, 0x00400000u)); }
+
 // Scale byte of values up to `largest` (the bits of a non-negative float): the least s >= 63 with
 // largest <= 448 * 2^(s - 127) = 1.75 * 2^(s - 119).  The sum carries into the exponent if the
 // significand is above 1.75.

@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
         if (before >= 0 && now > before) s_again[atomicAdd(s_n_again, 1)] = i << 8 | (now - before);
         now = max(now, before);
         if (now != before) *at = static_cast<uint8_t>(now);
-        s_inverse[i] = scale_value(254 - now);
+        // (a block that keeps a scale of NaN: NaN)
+        s_inverse[i] = now == 255 ? any_scale_value(255) : inverse_scale(now);
     }
     __syncthreads();
 

@@ -648,7 +648,8 @@ typedef struct xs_paged_cache8 {
  *     o == 0:  the scale becomes 2^e;
  *     o > 0:   it becomes the larger of 2^e and the block's scale; where that is 2^e, the first
  *              o tokens' numbers are divided by the ratio (rounded to nearest even: exact but
- *              for numbers that end below 2^-6);
+ *              for numbers that end below 2^-6); a scale of NaN stays, and the
+ *              run's numbers become NaN;
  *     numbers = x / scale, rounded to nearest even; an infinity becomes the largest number of a
  *     scale of 2^120, NaN stays NaN and does not count for a.
  * A slot outside [0, n_pages * page_size) (padding) stores no K and V.

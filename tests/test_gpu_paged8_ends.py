@@ -2,6 +2,11 @@
 import numpy as np
 import pytest
 
+import _paged as pg
+import _paged8 as p8
+from test_gpu_paged8_attn import _run
+from test_gpu_paged8_cache import Append
+
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
@@ -86,3 +91,61 @@ def test_read_of_the_least_scale(xs, dtype):
     """Byte 0 stands for 2^-127 as every other for its power."""
     for got, want in _read_all_numbers(xs, [0, 1, 2], dtype):
         _same(got, want)
+
+
+# ----------------------------------------------------------------------------- append
+@pytest.mark.parametrize("before", [0, 1, 50, 62, 63, 64, 119, 247, 248, 253, 254])
+@pytest.mark.parametrize("size", [2.0 ** -120, 1.0, 2.0 ** 124])
+def test_append_under_a_scale_that_another_program_wrote(xs, before, size):
+    """Rows into a begun block whose scale is any power of two: the numbers kept and the new ones by the definition."""
+    a = Append([3, 40], [5, 18], 2, 64, 32, 16, seed=before, spread=0)
+    a.x64 *= size
+    x = torch.from_numpy(a.x64).to(a.dtype)
+    a.x64 = x.double().numpy()
+    k, v = (x[:, a.H + i * a.Hkv:a.H + (i + 1) * a.Hkv].cuda() for i in (0, 1))
+    for i in (0, 1):
+        given = a.exp[i] != 128
+        a.exp[i][given] = before - 127
+        a.cache[2 + i].view(torch.uint8)[torch.from_numpy(given).cuda()] = before
+    xs.xs_rope_append_paged8(None, k, v, None, a.slots_d, None, *a.cache, None)
+    a.check_exact(0, a.x64[:, a.H:a.H + a.Hkv])
+    a.check_exact(1, a.x64[:, a.H + a.Hkv:])
+
+
+def test_append_under_a_scale_that_is_nan(xs):
+    """A begun block whose scale is NaN: it stays so, and what is appended is NaN by itself too."""
+    a = Append([3], [5], 1, 64, 16, 16, seed=1, spread=0)
+    at = a.slots_d[0].item() // 16
+    a.cache[2].view(torch.uint8)[at] = 255
+    kept = a.cache[0].view(torch.uint8)[at, :5].clone()
+    xs.xs_rope_append_paged8(None, a.k, a.v, None, a.slots_d, None, *a.cache, None)
+    assert a.cache[2].view(torch.uint8)[at].item() == 255
+    assert torch.equal(a.cache[0].view(torch.uint8)[at, :5], kept)
+    assert a.cache[0][at, 5:8].float().isnan().all()
+    a.check_exact(1, a.x64[:, a.H + a.Hkv:])
+
+
+# -------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("q", [1, 90])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("apart", [0, 1, 9], ids=lambda a: "apart%d" % a)
+def test_values_under_the_largest_scale(xs, apart, D, q):
+    """V's scales at the upper end of their range, 2^127, alone or beside smaller ones: outputs of up to 2^127, and the
+    log-sum-exp as ever."""
+    c = p8.Paged8Case([q, q], [300, 40], 4, 2, D, 32, block=16, seed=apart)
+    r = np.random.default_rng(apart)
+    c.vmax = 2.0 ** 127
+    for i, kv in enumerate(c.kv_lens):
+        blocks = pg.ceil_div(kv, 16)
+        num = p8.nearest(np.clip(r.standard_normal((kv, 2, D)) * 0.25, -0.9375, 0.9375))
+        exp = 127 - apart * r.integers(0, 2, size=(blocks, 2))
+        c.values[i] = num * np.exp2(exp[np.arange(kv) // 16].astype(float))[..., None]
+        code = p8.codes(num)
+        for j in range(pg.ceil_div(kv, 32)):
+            e = int(c.table[i, j])
+            hi = min(kv - 32 * j, 32)
+            c.v.view(torch.uint8)[e, :hi] = code[32 * j:32 * j + hi].cuda()
+            n = pg.ceil_div(hi, 16)
+            c.vs.view(torch.uint8)[e, :n] = torch.from_numpy((exp[2 * j:2 * j + n] + 127).astype(np.uint8)).cuda()
+    out, lse = _run(xs, c)
+    c.check(out, lse, True, 0, c.D ** -0.5)
