@@ -569,7 +569,8 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
  *     0 <= t < kv_len_i,   t <= p if causal,   t > p - window if window > 0:
  *     O = sum_t exp(x_t - m) V_t / sum_t exp(x_t - m),   x_t = scale <Q, K_t>,
  *     lse = m + ln sum_t exp(x_t - m);
- * a row that sees no key (kv_len_i < q_len_i, say) gets O = 0 and lse = -infinity.
+ * a row that sees no key (kv_len_i < q_len_i, say) gets O = 0 and lse = -infinity, one with a
+ * score that is NaN O and lse that are.
  * Without `causal` a chunk's tokens see each other and the whole cache (the next chunk
  * of a video).  Query head h reads KV head h / (H / Hkv).  K, V and the probabilities
  * enter the products in `dtype`; sums, maxima and the accumulators are fp32.  Scores x_t

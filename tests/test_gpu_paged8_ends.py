@@ -6,6 +6,7 @@ import _paged as pg
 import _paged8 as p8
 from test_gpu_paged8_attn import _run
 from test_gpu_paged8_cache import Append
+from test_gpu_paged_attn import _run as _run16
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -149,3 +150,20 @@ def test_values_under_the_largest_scale(xs, apart, D, q):
             c.vs.view(torch.uint8)[e, :n] = torch.from_numpy((exp[2 * j:2 * j + n] + 127).astype(np.uint8)).cuda()
     out, lse = _run(xs, c)
     c.check(out, lse, True, 0, c.D ** -0.5)
+
+
+@DTYPES
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("q", [1, 3, 90])
+def test_rows_that_are_nan(xs, q, bits, dtype):
+    """Their outputs are NaN and so are their log-sum-exps, whole tiles and cut ones; the other rows keep their bits."""
+    make, run = (p8.Paged8Case, _run) if bits == 8 else (pg.PagedCase, _run16)
+    c = make([q, q, 1], [500, 70, 20000], 8, 2, 128, 32, seed=3, dtype=dtype)
+    want, z = run(xs, c)
+    hit = torch.zeros((2 * q + 1, 8), dtype=torch.bool, device="cuda")
+    for t, h, d in [(0, 5, 17), (2 * q - 1, 0, 127), (2 * q, 7, 0)]:
+        c.q[t, h, d] = float("nan")
+        hit[t, h] = True
+    out, lse = run(xs, c)
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], z[~hit])
