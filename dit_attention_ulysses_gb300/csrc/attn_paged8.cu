@@ -352,9 +352,8 @@ __device__ __forceinline__ void convert_q(const PagedAttn8Args& a, const Piece& 
             }
 #pragma unroll
             for (int s = PER_ROW / 2; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            // the least scale whose 448-fold holds the row, 2^-126 at least
-            const int e = max(static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 8, 1);
-            const float f = scale_value(254 - e);
+            float f;
+            const int e = row_scale(m, f);
             if (piece == 0) factor[r] = a.c * scale_value(e);
 #pragma unroll
             for (int j = 0; j < 16; ++j) x[j] *= f;

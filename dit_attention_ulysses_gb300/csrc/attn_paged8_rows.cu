@@ -266,11 +266,11 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
 #pragma unroll
             for (int d = D / 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            // the least scale whose 448-fold holds the row, 2^-126 at least
-            const int e = max(static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 8, 1);
+            float f;
+            const int e = row_scale(m, f);
             if (at % (D / 8) == 0) factors[r] = a.c * scale_value(e);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] *= scale_value(254 - e);
+            for (int j = 0; j < 8; ++j) x[j] *= f;
 #pragma unroll
             for (int p = 0; p < C::PARTS; ++p) {
                 uint32_t o[2];

@@ -28,6 +28,14 @@ __device__ __forceinline__ int scale_byte(uint32_t largest) {
     return s > LEAST_SCALE ? s : LEAST_SCALE;
 }
 
+// A row of Q as numbers: the exponent byte of the least scale whose 448-fold holds its largest magnitude, 2^-126 at least,
+// and the inverse; NaN for an infinity (whose number would be 448 and its scores finite).
+__device__ __forceinline__ int row_scale(float largest, float& inverse) {
+    const int e = max(static_cast<int>((__float_as_uint(largest) + 0x1fffffu) >> 23) - 8, 1);
+    inverse = largest <= 3.402823466e38f ? scale_value(254 - e) : __uint_as_float(0x7fffffffu);
+    return e;
+}
+
 // Two e4m3 numbers (a byte each) as two fp16 ones: exact.
 __device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t two) {
     uint32_t r;

@@ -699,9 +699,9 @@ int xs_paged_read8(const xs_paged_read8_args* args, void* stream);
  * 8-bit cache: the same rows, keys, layouts, lse and workspace, on plans of their own (a plan of
  * the other cache computes nothing, see there).  Elements are those that the cache stands for
  * (scale bytes 63 .. 254, V's of one sequence within a factor of 2^90 of one another); q keeps 18
- * or more bits relative to its row's largest channel, the probabilities enter the second product in
- * fp16, off by up to 2^-25 of the largest product of a probability and its V's scale where they are
- * small; sums, maxima and accumulators are fp32.
+ * or more bits relative to its row's largest channel (an infinity makes the row NaN); the
+ * probabilities enter the second product in fp16, off by up to 2^-25 of the largest product of a
+ * probability and its V's scale where they are small; sums, maxima and accumulators are fp32.
  * Places that no row sees may hold anything, also in the scales.
  */
 int xs_attn_paged8_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,

@@ -167,3 +167,31 @@ def test_rows_that_are_nan(xs, q, bits, dtype):
     out, lse = run(xs, c)
     assert out[hit].isnan().all() and lse[hit].isnan().all()
     assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], z[~hit])
+
+
+@DTYPES
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("q", [1, 90])
+def test_rows_of_q_that_are_not_finite(xs, q, value, dtype):
+    """Their outputs and log-sum-exps are NaN; the other rows keep their bits."""
+    c = p8.Paged8Case([q, q], [500, 70], 8, 2, 128, 32, seed=3, dtype=dtype)
+    want, z = _run(xs, c)
+    rows = [(0, 5, 17), (2 * q - 1, 0, 127)]
+    for t, h, d in rows:
+        c.q[t, h, d] = value
+    out, lse = _run(xs, c)
+    hit = torch.zeros((2 * q, 8), dtype=torch.bool, device="cuda")
+    for t, h, _ in rows:
+        hit[t, h] = True
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], z[~hit])
+
+
+@DTYPES
+@pytest.mark.parametrize("q", [1, 90])
+def test_a_row_that_is_not_finite_and_sees_no_key(xs, q, dtype):
+    c = p8.Paged8Case([q, 2], [0, 30], 4, 1, 64, 16, seed=3, dtype=dtype)
+    c.q[:q] = float("inf")
+    out, lse = _run(xs, c)
+    assert not out[:q].any() and torch.isneginf(lse[:q]).all()
+    assert out[q:].isfinite().all()
