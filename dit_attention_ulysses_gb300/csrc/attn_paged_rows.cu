@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 alpha[e] = 1.0f;
-                if (mx > m_run[e] + RESCALE_THRESHOLD) {
+                if (mx - m_run[e] > RESCALE_THRESHOLD) {   // (the sum would be rounded: far from 0, up to a P of 2^16)
                     alpha[e] = ex2_approx(m_run[e] - mx);
                     m_run[e] = mx;
                     moved = true;
