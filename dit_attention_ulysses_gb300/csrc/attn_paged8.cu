@@ -15,7 +15,7 @@
 //
 // V's numbers are converted to fp16 (exact) on their way: four warps read a block from the
 // ring of copies and write it as the fp16 operand, keys that no row may see as zeros.  The
-// probabilities go in as fp16, below 2^8.  (As sums of e4m3 numbers they would cost the
+// probabilities go in as fp16, up to 2^15.  (As sums of e4m3 numbers they would cost the
 // softmax two conversions back and forth per pair, 12 of its issue cycles, where V's
 // conversion takes 2 and is another warp's.)
 //
@@ -668,9 +668,10 @@ __device__ void softmax_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t ba
                 }
                 uint32_t pk[32];
                 float sum = 0.0f;
+                const float ref = m_use - HEADROOM;   // what P, l and O are relative to
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    sum = fmaf(exp16(&sr[b >> 1][(b & 1) * 16], f[b], z[b].v - m_use, pk + b * 8), z[b].v_inv, sum);
+                    sum = fmaf(exp16(&sr[b >> 1][(b & 1) * 16], f[b], z[b].v - ref, pk + b * 8), z[b].v_inv, sum);
                 // Rescale of this thread's half of the O row (rare); PV(g-1) must have completed
                 // first.  Warp-uniform: TMEM access is collective.
                 if (__any_sync(0xffffffffu, rescale)) {
@@ -705,6 +706,7 @@ __device__ void softmax_role(const PagedAttn8Args& a, uint8_t* smem, uint32_t ba
         if (!ok) break;
         // ---- epilogue: the owner of this tile stores it to the destination shard
         const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+        m_run -= HEADROOM;
         ok = warp_wait(bar(C::B_O_FINAL), u & 1, abort_flag, a.timeout_ns, u);
         if (!ok) break;
         tc_fence_after();

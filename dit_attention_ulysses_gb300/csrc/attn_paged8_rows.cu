@@ -441,9 +441,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (int e = 0; e < 2; ++e) {
                     const float mx = alpha[n][e];
                     alpha[n][e] = 1.0f;
-                    if (mx > m_run[n][e] + RESCALE_THRESHOLD) {
-                        alpha[n][e] = ex2_approx(m_run[n][e] - mx);
-                        m_run[n][e] = mx;
+                    if (mx - m_run[n][e] > RESCALE_THRESHOLD + HEADROOM) {
+                        const float m = mx - HEADROOM;
+                        alpha[n][e] = ex2_approx(m_run[n][e] - m);
+                        m_run[n][e] = m;
                         moved = true;
                     }
                 }
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                         for (int e = 0; e < 4; ++e) o[i][n][e] *= alpha[n][e & 1];
                 }
             }
-            // P in fp16 (below 2^8; its relative rounding, half a step, is at most of the size of the output's own), keys
+            // P in fp16 (up to 2^15; its relative rounding, half a step, is at most of the size of the output's own), keys
             // side by side; the sum takes the fp32 values
             uint32_t pf[2][NT][2];
 #pragma unroll

@@ -700,7 +700,7 @@ int xs_paged_read8(const xs_paged_read8_args* args, void* stream);
  * the other cache computes nothing, see there).  Elements are those that the cache stands for
  * (scale bytes 63 .. 254, V's of one sequence within a factor of 2^90 of one another); q keeps 18
  * or more bits relative to its row's largest channel (an infinity makes the row NaN); the
- * probabilities enter the second product in fp16, off by up to 2^-25 of the largest product of a
+ * probabilities enter the second product in fp16, off by up to 2^-32 of the largest product of a
  * probability and its V's scale where they are small; sums, maxima and accumulators are fp32.
  * Places that no row sees may hold anything, also in the scales.
  */

@@ -195,3 +195,36 @@ def test_a_row_that_is_not_finite_and_sees_no_key(xs, q, dtype):
     out, lse = _run(xs, c)
     assert not out[:q].any() and torch.isneginf(lse[:q]).all()
     assert out[q:].isfinite().all()
+
+
+@DTYPES
+@pytest.mark.parametrize("q,heads", [(1, 1), (2, 2), (70, 2)])
+@pytest.mark.parametrize("down", [22, 24, 26, 28])
+def test_small_probabilities_beside_large_ones(xs, q, heads, down, dtype):
+    """A key of 32 has a probability 2^down times the others' and values of 0: the output is what the others add up to.
+    A probability is off by half a step of fp16, 2^-11, or by 2^-32 of its row's largest where it is small."""
+    kv = 640
+    c = p8.Paged8Case([q], [kv], heads, 1, 64, 32, block=32, seed=1, dtype=dtype)
+    few = np.arange(kv) % 32 == 5
+    k, v = np.zeros((kv, 1, 64)), np.full((kv, 1, 64), 256.0)
+    k[~few, 0, 0], v[few] = -down, 0.0                       # (four significant bits)
+    for cache, scale, x, e in ((c.k, c.ks, k, 0), (c.v, c.vs, v, 6)):
+        for j in range(kv // 32):
+            at = int(c.table[0, j])
+            cache.view(torch.uint8)[at] = p8.codes(x[32 * j:32 * j + 32]).cuda()
+            scale.view(torch.uint8)[at] = 127 + e
+    c.keys, c.values = [k], [v * 2.0 ** 6]
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.q64 = c.q.double().cpu().numpy()
+    scale = float(np.log(2.0))                               # a score is a power of two's exponent
+    out, lse = _run(xs, c, scale=scale)
+    ref, mass, z = c.reference(True, 0, scale)
+    # every 32 keys have a large one, so that the small ones are 31 of at most 2^-down / (keys / 32) each
+    floor = 2.0 ** -32 * 32 * 256 * 2.0 ** 6
+    before = (2.0 ** -11 + 1.5e-4) * mass + floor
+    got = out.double().cpu().numpy()
+    u = pg.U[dtype]
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0     # half of fp16's least step
+    assert (np.abs(got - ref) <= before + u * (np.abs(ref) + before) + tiny).all(), (got.ravel()[0], ref.ravel()[0])
+    assert (np.abs(lse.double().cpu().numpy() - z) <= 6e-5 + 2.0 ** -22 * np.abs(z)).all()
