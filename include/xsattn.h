@@ -574,8 +574,8 @@ int xs_attn_paged_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hk
  * Without `causal` a chunk's tokens see each other and the whole cache (the next chunk
  * of a video).  Query head h reads KV head h / (H / Hkv).  K, V and the probabilities
  * enter the products in `dtype`; sums, maxima and the accumulators are fp32.  Scores x_t
- * stay below 1e9 in magnitude (a chunk's exponents are formed in one fused step, whose
- * rounding is a common factor of a row up to there).
+ * stay below 1e9 in magnitude, in fp16 below 9e7 (a chunk's exponents are formed in one fused
+ * step, whose rounding is a common factor of a row; P holds it up to there).
  * The sums of a tile that is cut among SMs are joined in a fixed order: equal calls on
  * equal plans give equal bits.  After XS_ERR_DEVICE_TIMEOUT plan again.
  */
@@ -702,6 +702,8 @@ int xs_paged_read8(const xs_paged_read8_args* args, void* stream);
  * or more bits relative to its row's largest channel (an infinity makes the row NaN); the
  * probabilities enter the second product in fp16, off by up to 2^-32 of the largest product of a
  * probability and its V's scale where they are small; sums, maxima and accumulators are fp32.
+ * Scores x_t stay below 4e6 in magnitude: a V block's exponent is added to them in fp32, which
+ * weighs a block off by a factor of up to 2^(2^-22 |x|), |x| the row's largest.
  * Places that no row sees may hold anything, also in the scales.
  */
 int xs_attn_paged8_plan(const int* cu_q, const int* kv_lens, int n, int H, int Hkv, int D, int max_q, int causal,

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import _paged as pg
+import _paged8 as p8
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -32,3 +33,34 @@ def test_a_maximum_that_rises_by_one_step(xs, base):
     # 2^-16 of the values beside it, and half a step of fp16
     assert (np.abs(out.double().cpu().numpy()[0, 0] - want) <= 2.0 ** -14 + 2.0 ** -11 * np.abs(want)).all()
     assert lse.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("q", [1, 200])
+@pytest.mark.parametrize("power", [4, 6, 8, 9])
+def test_scores_far_from_zero_over_8_bits(xs, power, q, dtype):
+    """All scores alike and far below zero, up to -2.1e6: the mean of the values, of blocks with unlike scales; and one key as
+    far above: its values."""
+    from test_gpu_paged8_attn import _run
+    c = p8.Paged8Case([q], [700], 2, 2, 64, 16, seed=6, dtype=dtype, spread=3)
+    big = 2.0 ** power
+    score = 64 * big * big / 8
+    c.q.fill_(big)
+    c.k.view(torch.uint8)[:] = int(p8.codes(np.array([-1.0]))[0])
+    c.ks.view(torch.uint8)[:] = 127 + power
+    out, lse = _run(xs, c, causal=False)
+    u = pg.U[dtype]
+    v, a = np.mean(c.values[0], axis=0), np.mean(np.abs(c.values[0]), axis=0)
+    # the maximum, the block's exponent and their difference are rounded once each: 2^-22 |score log2(e)| powers of two
+    # in all, ln 2 times as much of a weight; numerator and denominator are weighed alike but for v_inv
+    off = 2 * np.expm1(score * 2.0 ** -22)
+    before = (off + 2.0 ** -11 + 1.5e-4) * a + 2.0 ** -32 * 700 * c.vmax
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - v) <= before + u * (np.abs(v) + before)).all()
+    assert ((lse.double() / -score - 1).abs() <= 2.0 ** -21 + 8 / score).all()     # the logarithm of 700, and its error
+    c.k.view(torch.uint8)[c.table[0, 30].long(), 5] = int(p8.codes(np.array([1.0]))[0])
+    out, lse = _run(xs, c, causal=False)
+    one = torch.from_numpy(c.values[0][30 * 16 + 5]).cuda()
+    # its probability is rounded to fp16, its quotient by the sum to the type
+    assert ((out.double() - one).abs() <= (2.0 ** -11 + 1e-6 + u) * 1.01 * one.abs()).all()
+    assert ((lse.double() / score - 1).abs() <= 2.0 ** -21).all()
