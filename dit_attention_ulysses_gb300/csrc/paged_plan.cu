@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
     int waves = 0, slot_ctas = grid;
     long long per_slot = 1;
     const long long share = ranges > 0 && total > 0 ? paged_div(total, ranges) : 0;   // of every CTA
-    const bool spilling = all_tiles > 0 && paged_div(keys, all_tiles) * heads * a.D * 4 > a.tile.l2_bytes;
+    const int key_bytes = a.D * (a.tile.cache8 ? 2 : 4);   // of K and V
+    const bool spilling = all_tiles > 0 && paged_div(keys, all_tiles) * heads * key_bytes > a.tile.l2_bytes;
     const bool shared = all_tiles >= 4 * heads || (spilling && all_tiles >= 2 * heads);
     if (a.tile.waves > 0 && kept > 0 && (shared || all_tiles <= SORTED)) {
         // one tile per slot, more (up to 64) where there are more tiles than slots; what is left is cut
