@@ -5,7 +5,7 @@ import pytest
 import _paged as pg
 import _paged8 as p8
 from test_gpu_paged8_attn import _run
-from test_gpu_paged8_cache import Append
+from test_gpu_paged8_cache import APPENDS, Append
 from test_gpu_paged_attn import _run as _run16
 
 pytestmark = pytest.mark.gpu
@@ -124,6 +124,29 @@ def test_append_under_a_scale_that_is_nan(xs):
     assert torch.equal(a.cache[0].view(torch.uint8)[at, :5], kept)
     assert a.cache[0][at, 5:8].float().isnan().all()
     a.check_exact(1, a.x64[:, a.H + a.Hkv:])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@DTYPES
+@pytest.mark.parametrize("case,rot", [(APPENDS[i], r) for i, r in ((1, 128), (2, 48), (3, 64), (4, 128), (6, 16), (7, 32), (9, 128))],
+                         ids=lambda c: str(c) if isinstance(c, int) else "T%d" % sum(c[0]))
+def test_scales_of_rotated_keys(xs, case, rot, dtype, layout):
+    """Every block's and head's scale lies between those of magnitudes lowered and raised by the rotation's error: it is
+    the definition's but where the largest magnitude lies within that error of 448 times a scale."""
+    a = Append(*case, dtype=dtype, seed=7, pad=2)
+    rope = xs.Rope(a.D, rot, layout=("half", "interleaved").index(layout), base=5e5)
+    a.launch(xs, rope)
+    x, mass = pg.rope_reference(a.x64[:, a.H:a.H + a.Hkv], a.pos, pg.frequencies(rot, base=5e5), layout == "interleaved")
+    off = (np.pi * 2.0 ** -24 + 4 * 2.0 ** -23) * mass + 2.0 ** -25 * np.abs(x)
+    ends = []
+    for y in (np.maximum(np.abs(x) - off, 0), np.abs(x) + off):
+        num, exp = a.num[0].copy(), a.exp[0].copy()
+        p8.append_reference(num, exp, y, a.slots, a.block)
+        ends.append(exp)
+    got = a.cache[2].view(torch.uint8).cpu().numpy().astype(float) - 127
+    bad = (got < ends[0]) | (got > ends[1])
+    assert not bad.any(), np.argwhere(bad)[:5]
+    assert (ends[0] == ends[1]).mean() > 0.9      # nearly all are pinned
 
 
 # -------------------------------------------------------------------------- attention
