@@ -171,6 +171,11 @@ __device__ __forceinline__ uint16_t* dest_row(const PagedAttnArgs& a, const Piec
     return reinterpret_cast<uint16_t*>(a.epi.ptr[p]) + (static_cast<size_t>(s) * a.epi.Hl + h) * a.D;
 }
 
+// Log-sum-exp of a row from its maximum (log2 units) and its sum: -infinity if it saw no key, NaN if its sum is.
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // The join of a tile of up to 128 / SHARE rows: SHARE warps for every 16 rows, each with a share of the channels of
 // both half rows and SHARE parts in flight, in CTA order (past the last: the last, at weight 0).
 template <int D, bool F16, int SHARE>

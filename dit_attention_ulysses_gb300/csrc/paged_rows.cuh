@@ -89,7 +89,10 @@ __device__ __forceinline__ void store_out(const PagedAttnArgs& a, int token, int
         w.y = pack2<F16>(o.z * inv, o.w * inv);
         *reinterpret_cast<uint2*>(p + c4 * 4) = w;
     }
-    if (c4 == 0 && a.lse != nullptr) a.lse[static_cast<size_t>(token) * a.H + head] = log_sum(m, l);
+    // (-infinity if the row saw no key, NaN if its sum is)
+    if (c4 == 0 && a.lse != nullptr)
+        a.lse[static_cast<size_t>(token) * a.H + head] =
+            l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // The parts of CTAs c0 .. c1 of a cut tile, joined in CTA order and stored; by a whole CTA.  A tile of HP KV heads

@@ -292,11 +292,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
-// Log-sum-exp of a row from its maximum (log2 units) and its sum: -infinity if it saw no key, NaN if its sum is.
-__device__ __forceinline__ float log_sum(float m, float l) {
-    return l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * 0.6931471805599453f;
-}
-
 // Three-input maximum (sm_100 family).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
