@@ -112,7 +112,7 @@ Tiling make_tiling8(int n, int Hkv, int G, int D, int max_q, int sms) {
     x.t.tokens = x.rows / G;
     // Pairs of KV heads (half the tiles, starts and joins, twice the work between waits) where a CTA still gets two of
     // them: 64 x 8192 keys 182 us, 199 with single heads; 200 ragged sequences 56 and 62.  With the heads of a page
-    // apart in memory they cost a little: 64 x 8192 178 and 171.
+    // apart in memory, which a plan does not know, they cost a little: 64 x 8192 178 and 171.
     if (x.rows == ROWS_FEW / 2 && Hkv % 2 == 0 && static_cast<int64_t>(n) * Hkv >= 2 * sms) x.t.heads = 2;
     x.t.block = 32;
     x.t.grid = 2 * sms;

@@ -19,9 +19,9 @@
 // softmax two conversions back and forth per pair, 12 of its issue cycles, where V's
 // conversion takes 2 and is another warp's.)
 //
-// What bounds it: 2 sequences' 2048 new tokens after 14336 each (causal, 32 heads of 128 over 8) take 788 us,
-// 1310 TFLOP/s, 70 % of the measured bf16 rate; 4608 over 18432 keys, not causal, 24 heads, 795 us.  (attn_paged.cu, over
-// twice the bytes: 748 and 743.)  Heads of 64, whose products are half as large: 2 x 2048 after 8192 452 us (353).  As there
+// What bounds it: 2 sequences' 2048 new tokens after 14336 each (causal, 32 heads of 128 over 8) take 785 us,
+// 1310 TFLOP/s, 70 % of the measured bf16 rate; 4608 over 18432 keys, not causal, 24 heads, 793 us.  (attn_paged.cu, over
+// twice the bytes: 749 and 743.)  Heads of 64, whose products are half as large: 2 x 2048 after 8192 452 us (353).  As there
 // it is the softmax's chain, with two of its warps to a scheduler, and a converter beside them: the issue slots
 // are busy for 57 % of the time, the tensor pipes for 58 %, the warps wait for their own results.
 //

@@ -20,9 +20,10 @@
 //     of a CTA's next piece are under way before it joins the current one (64 sequences of 8192 keys, 32 heads of 128
 //     over 8, one token each: 203 -> 197 us with the transposed products, ragged 75 -> 71).
 //
-// The same batch with tiles of two heads: 182 us, 5.9 TB/s of 1.07 GB (158 us at the copy rate); 64
-// ragged sequences of up to 8192 keys 58 us, 4.5 TB/s (over the 16-bit cache's twice as many bytes 101); one sequence of
-// 4096 keys 10.4 us, a chain of dependent trips to memory (plan, page, keys, parts), of which one of 300 keys has 7.7.
+// The same batch with tiles of two heads: 181 us, 5.9 TB/s of 1.07 GB (158 us at the copy rate; over the 16-bit cache 324);
+// 64 ragged sequences of up to 16385 keys, 126409 in all, 58.7 us, 4.4 TB/s (over the 16-bit cache 88.9, 5.8 TB/s: a tile's start
+// and end, which the plan counts as 512 keys, weigh twice as much beside half the bytes); one sequence of
+// 4096 keys 10.5 us, a chain of dependent trips to memory (plan, page, keys, parts), of which one of 300 keys has 7.7.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

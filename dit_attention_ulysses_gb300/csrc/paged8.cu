@@ -15,9 +15,12 @@
 // prompt whose windows are blocks) are loaded beside the window's where there is room, else in their place, and
 // those again after them.
 //
-// 8192 tokens (32 heads of 128 over 8, blocks of 16): 38.5 us, 4.8 TB/s of 186 MB (27.4 us at the copy rate).  A block
-// runs once through long code, and fetching it is what holds it up most beside its own two trips to memory (86 % of the
-// fetches hit the SM's cache; loops over heads unrolled by two: 41.0 us).  Rows held in registers: 53 us.
+// 8192 tokens (32 heads of 128 over 8, blocks of 16): 38.4 us, 4.8 TB/s of 186 MB (27.4 us at the copy rate).  A block
+// runs once through long code, and fetching it holds it up beside its trips to memory (92 % of the fetches hit the SM's
+// cache; loops over heads unrolled by two: 40.6 us).  Rows held in registers: 53 us.  64 tokens, one to a sequence: 5.1 us
+// where no kept number moves, 10.4 where those of every block do (calls whose magnitudes double each time).  Positions,
+// slots, a block's scale and its kept numbers are loaded one after the other, though their addresses depend on the slots
+// alone.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -288,10 +291,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 5 : 2)
 
 // ------------------------------------------------------------------- read back
 // A thread block gathers ROWS rows, 8 or 16: their sequences, pages and offsets once, into
-// shared memory, then 16-channel pieces of K and V.  Bound by HBM: 32768 rows of 8 x 128 take 37.3 us,
-// 5.4 TB/s of 201 MB (29.6 us at the copy rate), with 8 rows to a block 40.0, with 32 39.3.  1000 sequences of 8
-// rows take 13.2 us with 8 rows to a block (each waits for a search, a page, then the rows), 17.1 with 16 and 22.1
-// with 32; 24 ragged ones of up to 500 rows of 6 x 64 4.8, 5.7 and 5.7.
+// shared memory, then 16-channel pieces of K and V.  Bound by HBM: 32768 rows of 8 x 128 take 35.4 us,
+// 5.7 TB/s of 201 MB (29.6 us at the copy rate), with 8 rows to a block 36.2, with 32 38.2.  1000 sequences of 8
+// rows take 12.1 us with 8 rows to a block (each waits for a search, a page, then the rows), 16.1 with 16 and 19.6
+// with 32; 24 ragged ones of up to 500 rows of 6 x 64 4.5, 5.6 and 5.5.
 constexpr int THREADS = 256;
 constexpr int READ_UNROLL = 4;
 
@@ -408,8 +411,8 @@ cudaError_t launch_append(const Append8Args& args, int dtype, int layout, int nu
     a.window = C::ROWS * parts;
     const long long windows = (static_cast<long long>(a.T) + a.window - 1) / a.window;
     // heads of a block: as many as fit, fewer where that leaves SMs without a block.  512 tokens (32 heads of 128 over 8):
-    // 6.3 us, 7.1 if halved from half as many blocks on, 7.0 from twice as many, 8.2 if never; 7200 tokens at most, ragged
-    // (12 of 64 over 6, blocks of 64): 7.9, 9.7, 10.3, 12.9; 2048 tokens: 14.7, 14.7, 13.8, 14.7
+    // 6.1 us, 7.0 if halved from half as many blocks on, 6.9 from twice as many, 8.1 if never; 7200 tokens at most, ragged
+    // (12 of 64 over 6, blocks of 64): 7.9, 9.7, 10.1, 13.0; 256 tokens: 5.5, 5.7, 5.2, 7.0; 2048: 14.2, 14.1, 12.8, 14.1
     auto groups = [](int heads, int per) { return (heads + per - 1) / per; };
     auto per_block = [&](long long count, int heads, int most) {
         while (most > 1 && count * groups(heads, most) < num_sms) most /= 2;
@@ -440,9 +443,9 @@ cudaError_t launch_append(const Append8Args& args, int dtype, int layout, int nu
 }  // namespace
 
 cudaError_t launch_append8(const Append8Args& a, int dtype, int layout, int num_sms, cudaStream_t stream) {
-    // 128 threads where they hold a block's rows (blocks of 16, D = 128: 256 tokens 5.7 us, 512 6.3, 8192 40.8; with 256
-    // threads 6.3, 7.6, 42.5), else 256 (blocks of 128: 8192 tokens 49.4 us, with 128 threads 58.6; the ragged batch above
-    // 7.9 and 11.7)
+    // 128 threads where they hold a block's rows (blocks of 16, D = 128: 256 tokens 5.5 us, 512 6.1, 8192 38.4; with 256
+    // threads 6.3, 7.5, 42.1), else 256 (blocks of 128: 512 tokens 19.5 us, 8192 48.6, with 128 threads 30.5 and 55.2; blocks
+    // of 32: 8.6 and 9.8, but 8192 42.1 and 39.2, heads first 38.4 and 39.4; the ragged batch above 7.9 and 11.4)
     const bool few = ((a.D / 16) << a.block_shift) <= 128;
     if (a.D == 64)
         return few ? launch_append<64, 128>(a, dtype, layout, num_sms, stream) : launch_append<64, 256>(a, dtype, layout, num_sms, stream);
@@ -455,7 +458,8 @@ cudaError_t launch_read8(const Read8Args& args, int dtype, int num_sms, cudaStre
     auto launch = [&](auto kernel, int rows) {
         return launch_overlapped(kernel, dim3(static_cast<unsigned>((a.T - 1) / rows + 1)), THREADS, 0, stream, a);
     };
-    // 8 rows to a block where all blocks are then on the SMs at once, eight to one
+    // 8 rows to a block where all blocks are then on the SMs at once, eight to one (8000 rows of 8 x 128: 10.6 us, with 16
+    // rows to a block 14.4; 12000 rows 17.0 and 17.3)
     if ((a.T - 1) / 8 < 8 * num_sms) return dtype == 0 ? launch(read8_kernel<false, 8>, 8) : launch(read8_kernel<true, 8>, 8);
     return dtype == 0 ? launch(read8_kernel<false, 16>, 16) : launch(read8_kernel<true, 16>, 16);
 }

@@ -656,7 +656,8 @@ typedef struct xs_paged_cache8 {
  * A slot outside [0, n_pages * page_size) (padding) stores no K and V.
  *   rope == NULL: nothing is rotated, q, q_out and positions must be NULL, H 0 (a cache filled
  *   from keys that are rotated already).
- * The scales share no byte with anything else that the call reads or writes.
+ * K's and V's scales may lie in one buffer as K and V may; their address ranges overlap no other
+ * tensor's, K's and V's numbers among them (XS_ERR_OVERLAP).
  */
 typedef struct xs_rope_append8_args {
     const void* q;            /* as in xs_rope_append_args                                   */
