@@ -22,7 +22,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["attn_fwd.cu", "attn_paged.cu", "attn_paged8.cu", "attn_paged8_rows.cu", "attn_paged_rows.cu", "paged_plan.cu", "paged_step.cu", "rope.cu", "relayout.cu",
            "burst_gap.cu", "paged8.cu", "api.cu", "api_paged.cu", "api_paged8.cu"]
-HEADERS = ["kernels.h", "host.h", "paged.h", "paged_host.h", "rope_tile.cuh", "codes8.cuh", "paged_walk.cuh", "paged_chunk.cuh", "paged_rows.cuh", "attn_tile.cuh", "device_wait.cuh", "ptx.cuh", os.path.join("..", "..", "include", "xsattn.h")]
+HEADERS = ["kernels.h", "host.h", "paged.h", "paged_host.h", "rope_tile.cuh", "codes8.cuh", "paged_walk.cuh", "paged_chunk.cuh", "paged_rows.cuh", "attn_tile.cuh", "device_wait.cuh", "error_words.cuh", "ptx.cuh", os.path.join("..", "..", "include", "xsattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -536,6 +536,33 @@ int pipe_streams(PipeStreams** out) {
     return XS_OK;
 }
 
+// ---- one look at the error words of all paged kernels: with two copies for each family a read of a clean state takes
+// 96 us, with this and the dense kernels' two 41
+struct PagedErrorWords {
+    xs::ErrorWords of[4];
+};
+
+__device__ int g_any_paged_error;
+
+__global__ void any_paged_error_kernel(const __grid_constant__ PagedErrorWords w) {
+    int any = 0;
+    for (const xs::ErrorWords& x : w.of) any |= *static_cast<const volatile int*>(x.error) | *static_cast<const volatile int*>(x.drain);
+    g_any_paged_error = any;
+}
+
+// On the legacy stream, as the copies.
+cudaError_t any_paged_error(int* any) {
+    PagedErrorWords w;
+    cudaError_t e = cudaSuccess;
+    int i = 0;
+    for (auto words : {xs::paged_error_words, xs::paged_rows_error_words, xs::paged8_error_words, xs::paged8_rows_error_words})
+        if (e == cudaSuccess) e = words(&w.of[i++]);
+    if (e != cudaSuccess) return e;
+    any_paged_error_kernel<<<1, 1>>>(w);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return cudaMemcpyFromSymbol(any, g_any_paged_error, sizeof *any);
+}
+
 }  // namespace
 
 extern "C" {
@@ -989,12 +1016,14 @@ int xs_attn_get_device_error_info(void* stream, int* info, int n_info) {
     if (n_info < 0 || n_info > 8 || (n_info > 0 && !info)) return XS_ERR_NULL;
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
-    int v = 0, drain = 0;
+    int v = 0, drain = 0, any = 0;
     xs::DeviceErrorInfo r{};
     unsigned long long t = 0;
+    if ((e = any_paged_error(&any)) != cudaSuccess) return cuda_fail(e);
     // each kernel family keeps its own words: the earliest record is reported, all are cleared
     for (auto read : {xs::read_and_clear_device_error, xs::read_and_clear_paged_error, xs::read_and_clear_paged_rows_error,
                       xs::read_and_clear_paged8_error, xs::read_and_clear_paged8_rows_error}) {
+        if (!any && read != xs::read_and_clear_device_error) continue;
         int v1 = 0, d1 = 0;
         unsigned long long t1 = 0;
         xs::DeviceErrorInfo r1{};

@@ -44,6 +44,7 @@
 
 #include "attn_tile.cuh"
 #include "device_wait.cuh"
+#include "error_words.cuh"
 #include "kernels.h"
 #include "paged.h"
 #include "paged_chunk.cuh"
@@ -593,6 +594,8 @@ cudaError_t launch_attn_paged(const CUtensorMap& tq, const CUtensorMap& tk, cons
     if (a.D == 128) return dtype == 0 ? launch<128, false>(tq, tk, tv, a, stream) : launch<128, true>(tq, tk, tv, a, stream);
     return dtype == 0 ? launch<64, false>(tq, tk, tv, a, stream) : launch<64, true>(tq, tk, tv, a, stream);
 }
+
+cudaError_t paged_error_words(ErrorWords* w) { return error_words_here(w); }
 
 cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
     return read_and_clear_error_words(value, info, drain_failed, when);

@@ -48,6 +48,7 @@
 #include "attn_tile.cuh"
 #include "codes8.cuh"
 #include "device_wait.cuh"
+#include "error_words.cuh"
 #include "kernels.h"
 #include "paged.h"
 #include "paged_chunk.cuh"
@@ -808,6 +809,8 @@ cudaError_t launch_attn_paged8(const CUtensorMap& tk, const CUtensorMap& tv, con
     if (a.D == 128) return dtype == 0 ? launch<128, false>(tk, tv, a, stream) : launch<128, true>(tk, tv, a, stream);
     return dtype == 0 ? launch<64, false>(tk, tv, a, stream) : launch<64, true>(tk, tv, a, stream);
 }
+
+cudaError_t paged8_error_words(ErrorWords* w) { return error_words_here(w); }
 
 cudaError_t read_and_clear_paged8_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
     return read_and_clear_error_words(value, info, drain_failed, when);

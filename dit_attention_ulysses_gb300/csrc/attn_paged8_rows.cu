@@ -32,6 +32,7 @@
 
 #include "codes8.cuh"
 #include "device_wait.cuh"
+#include "error_words.cuh"
 #include "kernels.h"
 #include "paged.h"
 #include "paged_rows.cuh"
@@ -657,6 +658,8 @@ cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv
     if (a.tile.tokens * a.G <= 8) return launch_any<1, 1>(tk, tv, a, dtype, stream);
     return dtype == 0 ? launch<64, false, 2, 1>(tk, tv, a, stream) : launch<64, true, 2, 1>(tk, tv, a, stream);
 }
+
+cudaError_t paged8_rows_error_words(ErrorWords* w) { return error_words_here(w); }
 
 cudaError_t read_and_clear_paged8_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
     return read_and_clear_error_words(value, info, drain_failed, when);

@@ -35,6 +35,7 @@
 #include <cstdint>
 
 #include "device_wait.cuh"
+#include "error_words.cuh"
 #include "kernels.h"
 #include "paged.h"
 #include "paged_rows.cuh"
@@ -454,6 +455,8 @@ cudaError_t launch_attn_paged_rows(const CUtensorMap& tk, const CUtensorMap& tv,
     if (a.D == 128) return dtype == 0 ? launch_rows<128, false>(tk, tv, a, stream) : launch_rows<128, true>(tk, tv, a, stream);
     return dtype == 0 ? launch_rows<64, false>(tk, tv, a, stream) : launch_rows<64, true>(tk, tv, a, stream);
 }
+
+cudaError_t paged_rows_error_words(ErrorWords* w) { return error_words_here(w); }
 
 cudaError_t read_and_clear_paged_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when) {
     return read_and_clear_error_words(value, info, drain_failed, when);

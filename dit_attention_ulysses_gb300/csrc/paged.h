@@ -249,6 +249,16 @@ cudaError_t launch_attn_paged8_rows(const CUtensorMap& tk, const CUtensorMap& tv
 cudaError_t launch_attn_paged8(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttn8Args& a, int dtype,
                                cudaStream_t stream);
 
+// Where a kernel family records that there is an error, or copies that did not land.
+struct ErrorWords {
+    const int* error;
+    const int* drain;
+};
+cudaError_t paged_error_words(ErrorWords* w);
+cudaError_t paged8_error_words(ErrorWords* w);
+cudaError_t paged8_rows_error_words(ErrorWords* w);
+cudaError_t paged_rows_error_words(ErrorWords* w);
+
 cudaError_t read_and_clear_paged_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 cudaError_t read_and_clear_paged8_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
 cudaError_t read_and_clear_paged8_rows_error(int* value, DeviceErrorInfo* info, int* drain_failed, unsigned long long* when);
